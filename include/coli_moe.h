@@ -306,6 +306,125 @@ int coli_moe_forward_dump(const coli_moe_cfg* cfg, const coli_moe_weights* weigh
                           void* ws, size_t ws_bytes,
                           int32_t* acc_gu, int32_t* acc_d, cudaStream_t stream);
 
+/* ---- 4-bit microscaled (MX4) experts ---------------------------------------
+ * The container of fp4 checkpoints ("JustVugg/colibri" README: MXFP4 expert
+ * formats of other families) for activations and weights alike.  A row of K
+ * values (K % 32 == 0) is
+ *     codes  [K/2]  bytes: element 2j in the low half of byte j, 2j+1 in the
+ *                   high half; sign, two exponent bits, one mantissa bit: the
+ *                   magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *     scales [K/32] bytes: b stands for 2^(b - 127); 255: the block has no
+ *                   value (NaN)
+ * and rows of a matrix are consecutive.  Products multiply the values that
+ * codes and scales stand for and accumulate in fp32.
+ *
+ * Value types of the arguments named *_type: */
+#define COLI_F32  0
+#define COLI_BF16 1
+#define COLI_F16  2
+#define COLI_MX4  3   /* codes, with their scales in a second argument */
+
+/* Quantise rows to MX4: per block of 32 with largest magnitude A,
+ * b = max(0, floor(log2 A) + 125) (0 for a block of zeros), every element
+ * divided by 2^(b - 127), rounded to the nearest code (ties to the even code)
+ * and saturated at 6.  A block holding an infinity or NaN gets b = 255 and
+ * codes 0.
+ *   x       [T] rows of K values of x_type (COLI_F32, _BF16, _F16), row t at
+ *           element t * ldx; any ldx >= K (16-byte aligned rows are read in
+ *           16-byte pieces, others value by value)
+ *   codes   [T][K/2] out;  scales [T][K/32] out
+ * K % 32 == 0 (COLI_EINVAL otherwise).  T == 0 is a no-op. */
+int coli_mx4_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t T, int32_t K,
+                      uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+
+/* The values of MX4 rows: out[t][k] (row t at element t * ldo, out_type as
+ * x_type above) = code * 2^(b - 127), rounded to out_type once. */
+int coli_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t T, int32_t K,
+                        void* out, int32_t out_type, int64_t ldo, cudaStream_t stream);
+
+/* Products of MX4 rows, grouped: row p of the activations belongs to group g
+ * with offsets[g] <= p < offsets[g+1] and
+ *     y[p][n] = sum_k x[p][k] * w[g][n][k].
+ *   x_codes [P][K/2], x_scales [P][K/32]
+ *   w_codes [G][N][K/2], w_scales [G][N][K/32]
+ *   offsets [G+1] int32 on the device, ascending; NULL: one group (G == 1) of
+ *           all P rows.  Groups may be empty; values are clamped to [0, P] and
+ *           to ascending order; rows of no group are not written.
+ *   y       [P] rows of N values of y_type, row p at element p * ldy
+ *   ws      a workspace prepared with coli_moe_workspace_init, at least
+ *           COLI_MX4_PRODUCT_WS_BYTES (status word: COLI_STATUS_TIMEOUT)
+ * K % 32 == 0, any N >= 1, any ldy >= N, 1 <= G <= COLI_MX4_MAX_GROUPS. */
+#define COLI_MX4_MAX_GROUPS 1024
+#define COLI_MX4_PRODUCT_WS_BYTES 8704u
+int coli_mx4_product(const uint8_t* x_codes, const uint8_t* x_scales, int32_t P,
+                     const uint8_t* w_codes, const uint8_t* w_scales, int32_t G, int32_t N, int32_t K,
+                     const int32_t* offsets, void* y, int32_t y_type, int64_t ldy,
+                     void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* MX4 expert weights: one record per expert, gate [Ie][H], up [Ie][H],
+ * down [H][Ie], and the records of their scales in the same order:
+ * record bytes 3*Ie*H/2, scale bytes 3*Ie*H/32. */
+typedef struct coli_mx4_weights {
+    const uint8_t* experts;        /* [n_experts] records (ep shards: as above) */
+    const uint8_t* expert_scales;  /* [n_experts][3*inter*hidden/32]            */
+    const uint8_t* shared;         /* [n_shared] records (shared_inter)         */
+    const uint8_t* shared_scales;
+} coli_mx4_weights;
+
+/* Bytes of workspace for coli_mx4_forward with up to max_T positions; the
+ * same workspace also serves coli_moe_route with the same cfg.  0 on an
+ * invalid config.  Prepared once with coli_moe_workspace_init. */
+size_t coli_mx4_workspace_size(const coli_moe_cfg* cfg, int32_t max_T);
+
+/* The expert layer of coli_moe_forward on MX4 weights and activations:
+ *     xq = MX4(x[t]);  g = Wg xq, u = Wu xq;  hq = MX4(silu(g) * u);
+ *     o = Wd hq;  y[t] = sum_j topk_w[t][j] * o[t,j] + sum_s o_shared_s[t]
+ * with fp32 accumulation, fp32 silu and a combine in fixed order.  cfg as for
+ * coli_moe_forward with weight_bits 4 and group_size 0 (COLI_EINVAL
+ * otherwise); expert-parallel shards as there.
+ *   x         [T][H] of x_type, or codes [T][H/2] with x_type COLI_MX4 and
+ *             x_scales [T][H/32] (NULL otherwise)
+ *   topk_idx  [T][k] int32 (-1: slot skipped);  topk_w [T][k] fp32
+ *   y         [T][H] of y_type (COLI_F32, _BF16, _F16)
+ * Ids outside [-1, E) are skipped and set COLI_STATUS_BADIDX.  A block of x
+ * or h with an infinity or NaN makes its token's outputs NaN and sets
+ * COLI_STATUS_NONFINITE.  T == 0 is a no-op. */
+int coli_mx4_forward(const coli_moe_cfg* cfg, const coli_mx4_weights* weights,
+                     const void* x, int32_t x_type, const uint8_t* x_scales, int32_t T,
+                     const int32_t* topk_idx, const float* topk_w, void* y, int32_t y_type,
+                     void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The norms around a block, with its gate and the scaled residual add:
+ *     r  = y * rsqrt(mean(y^2) + eps) * post_w    (post_w NULL: r = y)
+ *     x' = x + res_scale * gate * r               (gate NULL: 1; y NULL: x' = x)
+ *     n  = x' * rsqrt(mean(x'^2) + eps) * pre_w   (pre_w NULL: no weight)
+ * in fp32; x', n and the MX4 codes of n are each rounded once from there.
+ *   x, y    [T][H] of `type`, row strides ldx, ldy in elements
+ *   gate    `type`; row stride ld_gate, 0: one [H] row for all positions
+ *   post_w, pre_w [H] fp32
+ *   x_out   [T][H] of `type` (may be x itself), n_out [T][H] of n_type
+ *           (`type` or COLI_F32), codes [T][H/2] with scales [T][H/32]
+ *           (H % 32 == 0); each may be NULL, not all of them.
+ * Any H from 1 to COLI_NORM_MAX_H and any strides; H % 8 == 0 with 16-byte
+ * aligned rows is read in 16-byte pieces.  T == 0 is a no-op. */
+#define COLI_NORM_MAX_H 16384
+typedef struct coli_moe_norm_args {
+    const void*  x;       int64_t ldx;
+    const void*  y;       int64_t ldy;
+    const void*  gate;    int64_t ld_gate;
+    void*        x_out;   int64_t ld_x_out;
+    void*        n_out;   int64_t ld_n_out;
+    const float* post_w;
+    const float* pre_w;
+    uint8_t*     codes;
+    uint8_t*     scales;
+    float        res_scale;
+    float        eps;
+    int32_t      type;
+    int32_t      n_type;
+} coli_moe_norm_args;
+int coli_moe_block_norm(const coli_moe_norm_args* args, int32_t T, int32_t H, cudaStream_t stream);
+
 /* ---- no-allocation variant ----------------------------------------------
  * The pages have no counterpart to this entry point; it exists for callers
  * that cannot allocate device memory to pass a workspace -- a plain C or FFI

@@ -31,8 +31,12 @@ EXPORTS = (
     "coli_moe_status", "coli_moe_strerror", "coli_moe_workspace_layout",
     "coli_moe_forward_dump", "coli_moe_forward_static", "coli_moe_layer",
     "coli_moe_stack_forward",
+    "coli_mx4_quantize", "coli_mx4_dequantize", "coli_mx4_product", "coli_mx4_workspace_size",
+    "coli_mx4_forward", "coli_moe_block_norm",
 )
 STATIC_WS_BYTES = 24 << 20
+MX4_PRODUCT_WS_BYTES = 8704
+COLI_F32, COLI_BF16, COLI_F16, COLI_MX4 = 0, 1, 2, 3
 
 
 class Cfg(ctypes.Structure):
@@ -63,6 +67,21 @@ class StackLayer(ctypes.Structure):
     _fields_ = [("cfg", Cfg), ("weights", Weights), ("router_w", ctypes.c_void_p), ("corr_bias", ctypes.c_void_p)]
 
 
+class Mx4Weights(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_void_p), ("expert_scales", ctypes.c_void_p),
+                ("shared", ctypes.c_void_p), ("shared_scales", ctypes.c_void_p)]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+                ("x_out", ctypes.c_void_p), ("ld_x_out", ctypes.c_int64),
+                ("n_out", ctypes.c_void_p), ("ld_n_out", ctypes.c_int64),
+                ("post_w", ctypes.c_void_p), ("pre_w", ctypes.c_void_p),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("res_scale", ctypes.c_float), ("eps", ctypes.c_float), ("type", ctypes.c_int32), ("n_type", ctypes.c_int32)]
+
+
 class WsLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in (
         "status", "n_entries", "entry_expert", "entry_count", "entry_offset", "pair_token",
@@ -75,6 +94,7 @@ def _load():
                           "(there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, S, I32, U32P = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint32)
+    I64 = ctypes.c_int64
     CP, WP = ctypes.POINTER(Cfg), ctypes.POINTER(Weights)
     sig = {
         "coli_moe_workspace_size": ([CP, I32], ctypes.c_size_t),
@@ -92,6 +112,12 @@ def _load():
         "coli_moe_layer": ([CP, WP, P, I32, P, P, P, P, P, P, S, P], ctypes.c_int),
         "coli_moe_stack_forward": ([ctypes.POINTER(StackLayer), I32, I32, P, P, I32, P, P, P, P, S, P],
                                    ctypes.c_int),
+        "coli_mx4_quantize": ([P, I32, I64, I32, I32, P, P, P], ctypes.c_int),
+        "coli_mx4_dequantize": ([P, P, I32, I32, P, I32, I64, P], ctypes.c_int),
+        "coli_mx4_product": ([P, P, I32, P, P, I32, I32, I32, P, P, I32, I64, P, S, P], ctypes.c_int),
+        "coli_mx4_workspace_size": ([CP, I32], ctypes.c_size_t),
+        "coli_mx4_forward": ([CP, ctypes.POINTER(Mx4Weights), P, I32, P, I32, P, P, P, I32, P, S, P], ctypes.c_int),
+        "coli_moe_block_norm": ([ctypes.POINTER(NormArgs), I32, I32, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -256,3 +282,165 @@ def capture_stack_step(layers, xs, residual, topk_idx, topk_w, y, ws, add_output
     with torch.cuda.graph(g, capture_error_mode="thread_local"):
         coli_moe_stack_forward(layers, xs, residual, topk_idx, topk_w, y, ws, add_output)
     return g
+
+
+# ------------------------------------------------------------------ MX4 experts
+# These entry points are called many times a token with few bytes each, so the
+# bindings below pass plain integers (ctypes converts them in place).
+_TYPES = {}
+
+
+def _type(t) -> int:
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float16: COLI_F16})
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"values are float32, bfloat16 or float16, not {t.dtype}")
+    return code
+
+
+def _rows(t, name: str):
+    """A [T, K] tensor with consecutive elements in each row, and its row stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, columns] with consecutive columns")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _bytes(t, shape, name: str):
+    """A contiguous uint8 tensor of `shape`."""
+    if t.element_size() != 1 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _stream_int(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+def coli_mx4_quantize(x, codes, scales, stream=None):
+    """MX4 of the rows of x [T, K] (any row stride) into codes [T, K/2] and scales [T, K/32]."""
+    T, K = x.shape
+    ld = _rows(x, "x")
+    _check(lib.coli_mx4_quantize(x.data_ptr(), _type(x), ld, T, K, _bytes(codes, (T, K // 2), "codes"),
+                                 _bytes(scales, (T, K // 32), "scales"), _stream_int(stream)), "coli_mx4_quantize")
+
+
+def coli_mx4_dequantize(codes, scales, out, stream=None):
+    """The values of codes [T, K/2] and scales [T, K/32] into out [T, K] (any row stride)."""
+    T, K = out.shape
+    ld = _rows(out, "out")
+    _check(lib.coli_mx4_dequantize(_bytes(codes, (T, K // 2), "codes"), _bytes(scales, (T, K // 32), "scales"), T, K,
+                                   out.data_ptr(), _type(out), ld, _stream_int(stream)), "coli_mx4_dequantize")
+
+
+def new_mx4_product_workspace(device="cuda"):
+    """Allocate (with torch) and initialise a workspace for coli_mx4_product."""
+    import torch
+    ws = torch.empty(MX4_PRODUCT_WS_BYTES, dtype=torch.uint8, device=device)
+    coli_moe_workspace_init(ws)
+    return ws
+
+
+def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, stream=None):
+    """y[p] = w[group of p] x[p] for x_codes [P, K/2], w_codes [G, N, K/2] (or [N, K/2]) with their
+    scales; ``offsets`` [G + 1] int32 on the device gives each group's first row (None: one group)."""
+    P, K = x_codes.shape[0], 2 * x_codes.shape[1]
+    G, N = (w_codes.shape[0], w_codes.shape[1]) if w_codes.dim() == 3 else (1, w_codes.shape[0])
+    lead = tuple(w_codes.shape[:-1])
+    if tuple(y.shape) != (P, N):
+        raise ValueError(f"y must be {(P, N)}, not {tuple(y.shape)}")
+    if offsets is not None and (tuple(offsets.shape) != (G + 1,) or offsets.element_size() != 4 or offsets.is_floating_point()
+                                or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int32 tensor of one entry more than groups")
+    ld = _rows(y, "y")
+    _check(lib.coli_mx4_product(_bytes(x_codes, (P, K // 2), "x_codes"), _bytes(x_scales, (P, K // 32), "x_scales"), P,
+                                _bytes(w_codes, lead + (K // 2,), "w_codes"), _bytes(w_scales, lead + (K // 32,), "w_scales"),
+                                G, N, K, None if offsets is None else offsets.data_ptr(), y.data_ptr(), _type(y), ld,
+                                ws.data_ptr(), ws.numel(), _stream_int(stream)), "coli_mx4_product")
+
+
+def make_mx4_weights(experts, expert_scales, shared=None, shared_scales=None) -> Mx4Weights:
+    """An MX4 weights struct from uint8 torch tensors (keep the tensors alive)."""
+    return Mx4Weights(experts.data_ptr(), expert_scales.data_ptr(),
+                      shared.data_ptr() if shared is not None and shared.numel() else None,
+                      shared_scales.data_ptr() if shared_scales is not None and shared_scales.numel() else None)
+
+
+def coli_mx4_workspace_size(cfg, max_T: int) -> int:
+    return int(lib.coli_mx4_workspace_size(ctypes.byref(_cfg(cfg)), int(max_T)))
+
+
+def new_mx4_workspace(cfg, max_T: int, device="cuda"):
+    """Allocate (with torch) and initialise a workspace for coli_mx4_forward (and coli_moe_route)."""
+    import torch
+    n = coli_mx4_workspace_size(cfg, max_T)
+    if n == 0:
+        raise ColiError(COLI_EINVAL, "coli_mx4_workspace_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    coli_moe_workspace_init(ws)
+    return ws
+
+
+def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_scales=None, stream=None):
+    """The MX4 expert layer: x [T, H] values, or codes [T, H/2] with ``x_scales`` [T, H/32]; y [T, H]."""
+    c = _cfg(cfg)
+    T, H = y.shape
+    if H != c.hidden or not y.is_contiguous():
+        raise ValueError(f"y must be contiguous [positions, {c.hidden}]")
+    if tuple(topk_idx.shape) != (T, c.top_k) or tuple(topk_w.shape) != (T, c.top_k):
+        raise ValueError(f"topk_idx and topk_w must be {(T, c.top_k)}")
+    if not topk_idx.is_contiguous() or not topk_w.is_contiguous():
+        raise ValueError("topk_idx and topk_w must be contiguous")
+    if x_scales is None:
+        if tuple(x.shape) != (T, H) or not x.is_contiguous():
+            raise ValueError(f"x must be contiguous {(T, H)}")
+        xp, xt, sp = x.data_ptr(), _type(x), None
+    else:
+        xp, xt, sp = _bytes(x, (T, H // 2), "x"), COLI_MX4, _bytes(x_scales, (T, H // 32), "x_scales")
+    _check(lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, topk_idx.data_ptr(), topk_w.data_ptr(),
+                                y.data_ptr(), _type(y), ws.data_ptr(), ws.numel(), _stream_int(stream)), "coli_mx4_forward")
+
+
+def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=None, eps=1e-6, x_out=None, n_out=None,
+                        codes=None, scales=None, stream=None):
+    """x' = x + res_scale * gate * (y, normed with post_w) and n = x' normed with pre_w, for rows of
+    x [T, H]: writes whichever of x_out (may be x), n_out, codes + scales (MX4 of n) are given.
+    ``gate`` is [H] or [T, H]."""
+    T, H = x.shape
+
+    def rows(t, name):
+        if t is None:
+            return None, 0
+        if tuple(t.shape) != (T, H):
+            raise ValueError(f"{name} must be {(T, H)}, not {tuple(t.shape)}")
+        if t.dtype != x.dtype and name != "n_out":
+            raise TypeError(f"{name} must have x's type")
+        return t.data_ptr(), _rows(t, name)
+
+    def vec(t, name):
+        if t is None:
+            return None
+        if tuple(t.shape) != (H,) or t.element_size() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of {H}")
+        return t.data_ptr()
+
+    ty = _type(x)
+    if gate is not None and gate.dim() == 1:
+        if gate.shape[0] != H or gate.dtype != x.dtype or not gate.is_contiguous():
+            raise ValueError(f"gate must be {H} or {(T, H)} values of x's type")
+        g, ldg = gate.data_ptr(), 0
+    else:
+        g, ldg = rows(gate, "gate")
+    xp, ldx = rows(x, "x")
+    yp, ldy = rows(y, "y")
+    xo, ldxo = rows(x_out, "x_out")
+    no, ldno = rows(n_out, "n_out")
+    a = NormArgs(xp, ldx, yp, ldy, g, ldg, xo, ldxo, no, ldno, vec(post_w, "post_w"), vec(pre_w, "pre_w"),
+                 None if codes is None else _bytes(codes, (T, H // 2), "codes"),
+                 None if scales is None else _bytes(scales, (T, H // 32), "scales"),
+                 res_scale, eps, ty, ty if n_out is None else _type(n_out))
+    _check(lib.coli_moe_block_norm(ctypes.byref(a), T, H, _stream_int(stream)), "coli_moe_block_norm")

@@ -1,0 +1,224 @@
+// coli_moe_block_norm: the norm, gate and residual add behind a block fused
+// with the norm before the next one, optionally with the MX4 codes of its
+// result (mx4_common.cuh).
+//
+//   r  = y * rsqrt(mean(y^2) + eps) * post_w     (post_w NULL: r = y)
+//   x' = x + res_scale * gate * r                (gate NULL: 1; y NULL: x' = x)
+//   n  = x' * rsqrt(mean(x'^2) + eps) * pre_w    (pre_w NULL: no weight)
+//
+// One pass: a row stays in registers between its two reductions, so x, y and
+// gate are read once and x', n and the codes written once; bound by HBM (a
+// single row by its load, two reductions and store).  All arithmetic is fp32;
+// n and its codes are formed from the unrounded x'.
+#include "mx4_common.cuh"
+
+namespace {
+
+using namespace colimoe;
+
+struct NormParams {
+  const void* x;
+  const void* y;
+  const void* gate;
+  const float* post_w;
+  const float* pre_w;
+  void* x_out;
+  void* n_out;
+  uint8_t* codes;
+  uint8_t* scales;
+  long long ldx, ldy, ldg, ldxo, ldno;
+  int rows, H;
+  float res_scale, eps;
+};
+
+// sum over the threads of a row: a warp, or the whole CTA through `red`
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if (WARP) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  // every warp sums the same partials in the same order
+  v = warp_sum(lane < nw ? red[lane] : 0.f);
+  return v;
+}
+
+// 8 weights, which every row reads again: cached loads
+template <bool VEC>
+__device__ __forceinline__ void load_w(const float* p, int n, float* v) {
+  if (VEC) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(p + i) : 0.f;
+  }
+}
+
+// U units of 8 elements per thread; WARP: one row per warp, else per CTA
+template <typename T, typename TN, int U, bool VEC, bool WARP>
+__global__ void __launch_bounds__(U == 4 ? 512 : 1024) norm_kernel(const NormParams P) {
+  __shared__ float red[2][32];
+  const int H = P.H;
+  const int nthr = WARP ? 32 : (int)blockDim.x, t = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+  const int per_cta = WARP ? (int)(blockDim.x >> 5) : 1;
+  const long long first = (long long)blockIdx.x * per_cta + (WARP ? (threadIdx.x >> 5) : 0);
+  pdl_wait();
+  pdl_trigger();
+  for (long long row = first; row < P.rows; row += (long long)gridDim.x * per_cta) {
+    const T* xr = static_cast<const T*>(P.x) + row * P.ldx;
+    const T* yr = P.y ? static_cast<const T*>(P.y) + row * P.ldy : nullptr;
+    const T* gr = P.gate ? static_cast<const T*>(P.gate) + row * P.ldg : nullptr;
+    float x[U][8], y[U][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (u * nthr + t) * 8;
+      const int n = H - k;
+      if (n > 0) {
+        load8<T, VEC>(xr + k, n, x[u]);
+        if (yr) load8<T, VEC>(yr + k, n, y[u]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = y[u][i] = 0.f;
+      }
+    }
+    if (yr) {
+      float c = P.res_scale;
+      if (P.post_w) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss += y[u][i] * y[u][i];
+        c *= rsqrtf(row_sum<WARP>(ss, red[0]) / (float)H + P.eps);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (u * nthr + t) * 8;
+        const int n = H - k;
+        if (n <= 0) continue;
+        float w[8];
+        if (P.post_w) {
+          load_w<VEC>(P.post_w + k, n, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[u][i] *= w[i];
+        }
+        if (gr) {
+          load8<T, VEC>(gr + k, n, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[u][i] *= w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] += c * y[u][i];
+        if (P.x_out) store8<T, VEC>(static_cast<T*>(P.x_out) + row * P.ldxo + k, n, x[u]);
+      }
+    } else if (P.x_out) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = (u * nthr + t) * 8;
+        if (k < H) store8<T, VEC>(static_cast<T*>(P.x_out) + row * P.ldxo + k, H - k, x[u]);
+      }
+    }
+    if (!P.n_out && !P.codes) {
+      if (!WARP) __syncthreads();
+      continue;
+    }
+    ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += x[u][i] * x[u][i];
+    const float c = rsqrtf(row_sum<WARP>(ss, red[1]) / (float)H + P.eps);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (u * nthr + t) * 8;
+      const int n = H - k;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[u][i] * c;
+      if (P.pre_w && n > 0) {
+        float w[8];
+        load_w<VEC>(P.pre_w + k, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= w[i];
+      }
+      if (P.n_out && n > 0) store8<TN, VEC>(static_cast<TN*>(P.n_out) + row * P.ldno + k, n, v);
+      if (P.codes) {  // H % 32 == 0: a block's four lanes are in or out together
+        uint32_t b;
+        const uint32_t q = mx4_quant8(v, &b);
+        if (n > 0) {
+          reinterpret_cast<uint32_t*>(P.codes)[(row * H + k) / 8] = q;
+          if ((t & 3) == 0) P.scales[(row * H + k) / MXB] = (uint8_t)b;
+        }
+      }
+    }
+    if (!WARP) __syncthreads();  // both partial arrays are free for the next row
+  }
+}
+
+template <typename T, typename TN, int U>
+cudaError_t launch_u(const NormParams& P, bool vec, bool warp, unsigned grid, unsigned block, cudaStream_t st) {
+  if (warp)
+    return vec ? launch_pdl(norm_kernel<T, TN, U, true, true>, grid, block, 0, st, P)
+               : launch_pdl(norm_kernel<T, TN, U, false, true>, grid, block, 0, st, P);
+  return vec ? launch_pdl(norm_kernel<T, TN, U, true, false>, grid, block, 0, st, P)
+             : launch_pdl(norm_kernel<T, TN, U, false, false>, grid, block, 0, st, P);
+}
+
+// Threads of a row: one warp up to 512 elements (no barrier); else a CTA with
+// one unit per thread, which is the shortest chain for few rows, or with more
+// rows than SMs up to four units per thread, so that several small CTAs share
+// an SM and their loads cover each other's reductions.
+template <typename T, typename TN>
+cudaError_t launch(const NormParams& P, bool vec, cudaStream_t st) {
+  const int units = (P.H + 7) / 8;
+  const int sms = device_sms() > 0 ? device_sms() : 152;
+  if (units <= 64) {
+    const long long blocks = ((long long)P.rows + 7) / 8;
+    const long long cap = 8LL * sms;
+    const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
+    return units <= 32 ? launch_u<T, TN, 1>(P, vec, true, grid, 256, st) : launch_u<T, TN, 2>(P, vec, true, grid, 256, st);
+  }
+  int u = units > 1024 ? 2 : 1;
+  while (u < 4 && P.rows > sms && (units + u - 1) / u > 256) u *= 2;
+  const unsigned block = (unsigned)(((units + u - 1) / u + 31) / 32 * 32);
+  const long long cap = (2048 / block) * (long long)sms;
+  const unsigned grid = (unsigned)(P.rows < cap ? P.rows : cap);
+  if (u == 1) return launch_u<T, TN, 1>(P, vec, false, grid, block, st);
+  if (u == 2) return launch_u<T, TN, 2>(P, vec, false, grid, block, st);
+  return launch_u<T, TN, 4>(P, vec, false, grid, block, st);
+}
+
+int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+extern "C" int coli_moe_block_norm(const coli_moe_norm_args* a, int32_t T, int32_t H, cudaStream_t stream) {
+  if (!a || T < 0 || H <= 0 || !float_type(a->type)) return COLI_EINVAL;
+  if (H > COLI_NORM_MAX_H) return COLI_EUNSUPPORTED;
+  if (a->n_out && a->n_type != a->type && a->n_type != COLI_F32) return COLI_EINVAL;
+  if (!a->codes != !a->scales) return COLI_EINVAL;
+  if (a->codes && H % MXB) return COLI_EINVAL;
+  if ((a->post_w || a->gate) && !a->y) return COLI_EINVAL;
+  if (!(a->eps >= 0.f) || a->ldx < H || (a->y && a->ldy < H) || (a->gate && a->ld_gate != 0 && a->ld_gate < H) ||
+      (a->x_out && a->ld_x_out < H) || (a->n_out && a->ld_n_out < H))
+    return COLI_EINVAL;
+  if (T == 0) return COLI_OK;
+  if (!a->x || (!a->x_out && !a->n_out && !a->codes)) return COLI_EINVAL;
+  const void* ptrs[] = {a->x, a->y, a->post_w, a->gate, a->pre_w, a->x_out, a->n_out, a->codes, a->scales};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return COLI_EALIGN;
+  const int32_t nt = a->n_out ? a->n_type : a->type;
+  const bool vec = H % 8 == 0 && rows_aligned(a->x, a->ldx, a->type) && (!a->y || rows_aligned(a->y, a->ldy, a->type)) &&
+                   (!a->gate || rows_aligned(a->gate, a->ld_gate, a->type)) &&
+                   (!a->x_out || rows_aligned(a->x_out, a->ld_x_out, a->type)) &&
+                   (!a->n_out || rows_aligned(a->n_out, a->ld_n_out, nt));
+  NormParams P{a->x, a->y, a->gate, a->post_w, a->pre_w, a->x_out, a->n_out, a->codes, a->scales,
+               a->ldx, a->ldy, a->ld_gate, a->ld_x_out, a->ld_n_out, T, H, a->res_scale, a->eps};
+  if (a->type == COLI_F32) return rc_of(launch<float, float>(P, vec, stream));
+  if (a->type == COLI_BF16)
+    return rc_of(nt == COLI_F32 ? launch<__nv_bfloat16, float>(P, vec, stream) : launch<__nv_bfloat16, __nv_bfloat16>(P, vec, stream));
+  return rc_of(nt == COLI_F32 ? launch<__half, float>(P, vec, stream) : launch<__half, __half>(P, vec, stream));
+}
