@@ -285,56 +285,79 @@ def capture_stack_step(layers, xs, residual, topk_idx, topk_w, y, ws, add_output
 
 
 # ------------------------------------------------------------------ MX4 experts
-# These entry points are called many times a token with few bytes each, so the
-# bindings below pass plain integers (ctypes converts them in place).
+# Single-position calls take a few microseconds on the GPU, so these bindings
+# keep their own cost to about that: one look at each tensor, plain integers
+# to ctypes, the raw handle of the current stream.
 _TYPES = {}
+_raw_stream = None
+
+
+def _torch_names():
+    global _raw_stream
+    import torch
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _TYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float16: COLI_F16})
 
 
 def _type(t) -> int:
     if not _TYPES:
-        import torch
-        _TYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float16: COLI_F16})
+        _torch_names()
     code = _TYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"values are float32, bfloat16 or float16, not {t.dtype}")
     return code
 
 
-def _rows(t, name: str):
-    """A [T, K] tensor with consecutive elements in each row, and its row stride."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, columns] with consecutive columns")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+def _on(t, stream) -> int:
+    """The stream to enqueue on: the given one, else the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        _torch_names()
+    return _raw_stream(t.get_device())
 
 
-def _bytes(t, shape, name: str):
-    """A contiguous uint8 tensor of `shape`."""
-    if t.element_size() != 1 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+def _rows(t, shape, name: str):
+    """The row stride of a GPU tensor of `shape` (two dimensions) whose rows have consecutive elements."""
+    if t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor of shape {tuple(shape)}, not {tuple(t.shape)} on {t.device}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have consecutive elements in each row")
+    return ld if shape[0] > 1 or ld > shape[1] else shape[1]
+
+
+def _bytes(t, shape, name: str) -> int:
+    """The address of a contiguous uint8 GPU tensor of `shape`."""
+    if t.shape != shape or t.element_size() != 1 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 GPU tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _stream_int(stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+def _flat(t, shape, size: int, name: str) -> int:
+    """The address of a contiguous GPU tensor of `shape` with elements of `size` bytes."""
+    if t.shape != shape or t.element_size() != size or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)} with {size}-byte elements, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def coli_mx4_quantize(x, codes, scales, stream=None):
     """MX4 of the rows of x [T, K] (any row stride) into codes [T, K/2] and scales [T, K/32]."""
-    T, K = x.shape
-    ld = _rows(x, "x")
-    _check(lib.coli_mx4_quantize(x.data_ptr(), _type(x), ld, T, K, _bytes(codes, (T, K // 2), "codes"),
-                                 _bytes(scales, (T, K // 32), "scales"), _stream_int(stream)), "coli_mx4_quantize")
+    T, K = shape = x.shape
+    rc = lib.coli_mx4_quantize(x.data_ptr(), _type(x), _rows(x, shape, "x"), T, K, _bytes(codes, (T, K // 2), "codes"),
+                               _bytes(scales, (T, K // 32), "scales"), _on(x, stream))
+    if rc:
+        _check(rc, "coli_mx4_quantize")
 
 
 def coli_mx4_dequantize(codes, scales, out, stream=None):
     """The values of codes [T, K/2] and scales [T, K/32] into out [T, K] (any row stride)."""
-    T, K = out.shape
-    ld = _rows(out, "out")
-    _check(lib.coli_mx4_dequantize(_bytes(codes, (T, K // 2), "codes"), _bytes(scales, (T, K // 32), "scales"), T, K,
-                                   out.data_ptr(), _type(out), ld, _stream_int(stream)), "coli_mx4_dequantize")
+    T, K = shape = out.shape
+    rc = lib.coli_mx4_dequantize(_bytes(codes, (T, K // 2), "codes"), _bytes(scales, (T, K // 32), "scales"), T, K,
+                                 out.data_ptr(), _type(out), _rows(out, shape, "out"), _on(out, stream))
+    if rc:
+        _check(rc, "coli_mx4_dequantize")
 
 
 def new_mx4_product_workspace(device="cuda"):
@@ -348,19 +371,16 @@ def new_mx4_product_workspace(device="cuda"):
 def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, stream=None):
     """y[p] = w[group of p] x[p] for x_codes [P, K/2], w_codes [G, N, K/2] (or [N, K/2]) with their
     scales; ``offsets`` [G + 1] int32 on the device gives each group's first row (None: one group)."""
-    P, K = x_codes.shape[0], 2 * x_codes.shape[1]
-    G, N = (w_codes.shape[0], w_codes.shape[1]) if w_codes.dim() == 3 else (1, w_codes.shape[0])
-    lead = tuple(w_codes.shape[:-1])
-    if tuple(y.shape) != (P, N):
-        raise ValueError(f"y must be {(P, N)}, not {tuple(y.shape)}")
-    if offsets is not None and (tuple(offsets.shape) != (G + 1,) or offsets.element_size() != 4 or offsets.is_floating_point()
-                                or not offsets.is_contiguous()):
-        raise ValueError("offsets must be a contiguous int32 tensor of one entry more than groups")
-    ld = _rows(y, "y")
-    _check(lib.coli_mx4_product(_bytes(x_codes, (P, K // 2), "x_codes"), _bytes(x_scales, (P, K // 32), "x_scales"), P,
-                                _bytes(w_codes, lead + (K // 2,), "w_codes"), _bytes(w_scales, lead + (K // 32,), "w_scales"),
-                                G, N, K, None if offsets is None else offsets.data_ptr(), y.data_ptr(), _type(y), ld,
-                                ws.data_ptr(), ws.numel(), _stream_int(stream)), "coli_mx4_product")
+    P, k2 = shape = x_codes.shape
+    K = 2 * k2
+    ws_shape = w_codes.shape
+    G, N = (ws_shape[0], ws_shape[1]) if len(ws_shape) == 3 else (1, ws_shape[0])
+    off = None if offsets is None else _flat(offsets, (G + 1,), 4, "offsets")
+    rc = lib.coli_mx4_product(_bytes(x_codes, shape, "x_codes"), _bytes(x_scales, (P, K // 32), "x_scales"), P,
+                              _bytes(w_codes, (*ws_shape[:-1], k2), "w_codes"), _bytes(w_scales, (*ws_shape[:-1], K // 32), "w_scales"),
+                              G, N, K, off, y.data_ptr(), _type(y), _rows(y, (P, N), "y"), ws.data_ptr(), ws.numel(), _on(y, stream))
+    if rc:
+        _check(rc, "coli_mx4_product")
 
 
 def make_mx4_weights(experts, expert_scales, shared=None, shared_scales=None) -> Mx4Weights:
@@ -389,20 +409,19 @@ def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_sca
     """The MX4 expert layer: x [T, H] values, or codes [T, H/2] with ``x_scales`` [T, H/32]; y [T, H]."""
     c = _cfg(cfg)
     T, H = y.shape
-    if H != c.hidden or not y.is_contiguous():
-        raise ValueError(f"y must be contiguous [positions, {c.hidden}]")
-    if tuple(topk_idx.shape) != (T, c.top_k) or tuple(topk_w.shape) != (T, c.top_k):
-        raise ValueError(f"topk_idx and topk_w must be {(T, c.top_k)}")
-    if not topk_idx.is_contiguous() or not topk_w.is_contiguous():
-        raise ValueError("topk_idx and topk_w must be contiguous")
+    if H != c.hidden:
+        raise ValueError(f"y must be [positions, {c.hidden}], not {tuple(y.shape)}")
     if x_scales is None:
-        if tuple(x.shape) != (T, H) or not x.is_contiguous():
-            raise ValueError(f"x must be contiguous {(T, H)}")
-        xp, xt, sp = x.data_ptr(), _type(x), None
+        xt, sp = _type(x), None
+        xp = _flat(x, (T, H), x.element_size(), "x")
     else:
         xp, xt, sp = _bytes(x, (T, H // 2), "x"), COLI_MX4, _bytes(x_scales, (T, H // 32), "x_scales")
-    _check(lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, topk_idx.data_ptr(), topk_w.data_ptr(),
-                                y.data_ptr(), _type(y), ws.data_ptr(), ws.numel(), _stream_int(stream)), "coli_mx4_forward")
+    k = c.top_k
+    rc = lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, _flat(topk_idx, (T, k), 4, "topk_idx"),
+                              _flat(topk_w, (T, k), 4, "topk_w"), _flat(y, (T, H), y.element_size(), "y"), _type(y),
+                              ws.data_ptr(), ws.numel(), _on(y, stream))
+    if rc:
+        _check(rc, "coli_mx4_forward")
 
 
 def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=None, eps=1e-6, x_out=None, n_out=None,
@@ -410,37 +429,31 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
     """x' = x + res_scale * gate * (y, normed with post_w) and n = x' normed with pre_w, for rows of
     x [T, H]: writes whichever of x_out (may be x), n_out, codes + scales (MX4 of n) are given.
     ``gate`` is [H] or [T, H]."""
-    T, H = x.shape
-
-    def rows(t, name):
-        if t is None:
-            return None, 0
-        if tuple(t.shape) != (T, H):
-            raise ValueError(f"{name} must be {(T, H)}, not {tuple(t.shape)}")
-        if t.dtype != x.dtype and name != "n_out":
-            raise TypeError(f"{name} must have x's type")
-        return t.data_ptr(), _rows(t, name)
-
-    def vec(t, name):
-        if t is None:
-            return None
-        if tuple(t.shape) != (H,) or t.element_size() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor of {H}")
-        return t.data_ptr()
-
+    T, H = shape = x.shape
     ty = _type(x)
-    if gate is not None and gate.dim() == 1:
-        if gate.shape[0] != H or gate.dtype != x.dtype or not gate.is_contiguous():
-            raise ValueError(f"gate must be {H} or {(T, H)} values of x's type")
-        g, ldg = gate.data_ptr(), 0
-    else:
-        g, ldg = rows(gate, "gate")
-    xp, ldx = rows(x, "x")
-    yp, ldy = rows(y, "y")
-    xo, ldxo = rows(x_out, "x_out")
-    no, ldno = rows(n_out, "n_out")
-    a = NormArgs(xp, ldx, yp, ldy, g, ldg, xo, ldxo, no, ldno, vec(post_w, "post_w"), vec(pre_w, "pre_w"),
-                 None if codes is None else _bytes(codes, (T, H // 2), "codes"),
-                 None if scales is None else _bytes(scales, (T, H // 32), "scales"),
-                 res_scale, eps, ty, ty if n_out is None else _type(n_out))
-    _check(lib.coli_moe_block_norm(ctypes.byref(a), T, H, _stream_int(stream)), "coli_moe_block_norm")
+    a = NormArgs(x.data_ptr(), _rows(x, shape, "x"), res_scale=res_scale, eps=eps, type=ty, n_type=ty)
+    if y is not None:
+        a.y, a.ldy = y.data_ptr(), _rows(y, shape, "y")
+    if gate is not None:
+        if gate.dim() == 1:
+            a.gate = _flat(gate, (H,), gate.element_size(), "gate")
+        else:
+            a.gate, a.ld_gate = gate.data_ptr(), _rows(gate, shape, "gate")
+    if x_out is not None:
+        a.x_out, a.ld_x_out = x_out.data_ptr(), _rows(x_out, shape, "x_out")
+    if n_out is not None:
+        a.n_out, a.ld_n_out, a.n_type = n_out.data_ptr(), _rows(n_out, shape, "n_out"), _type(n_out)
+    for t in (y, gate, x_out):
+        if t is not None and t.dtype is not x.dtype:
+            raise TypeError(f"y, gate and x_out must have x's type {x.dtype}, not {t.dtype}")
+    if post_w is not None:
+        a.post_w = _flat(post_w, (H,), 4, "post_w")
+    if pre_w is not None:
+        a.pre_w = _flat(pre_w, (H,), 4, "pre_w")
+    if codes is not None:
+        a.codes = _bytes(codes, (T, H // 2), "codes")
+    if scales is not None:
+        a.scales = _bytes(scales, (T, H // 32), "scales")
+    rc = lib.coli_moe_block_norm(ctypes.byref(a), T, H, _on(x, stream))
+    if rc:
+        _check(rc, "coli_moe_block_norm")

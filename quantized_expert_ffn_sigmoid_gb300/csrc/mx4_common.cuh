@@ -13,6 +13,7 @@
 // power of two (exact), rounded to the nearest code (ties to the even code)
 // and saturated at 6.  A block with an infinity or NaN gets b = 255, codes 0.
 #pragma once
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "colimoe_internal.cuh"
@@ -131,10 +132,14 @@ __device__ __forceinline__ void store8(T* p, int n, const float* v) {
 inline bool rows_aligned(const void* p, int64_t ld, int32_t t) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ((uint64_t)ld * type_bytes(t)) % 16 == 0;
 }
+// SMs of the current device (0 on failure), looked up once per device
 inline int device_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 // launch with programmatic dependent launch (every kernel here begins with

@@ -39,6 +39,7 @@ constexpr int GW_EPI = 4, GW_TMA = 8, GW_MMA = 9;
 constexpr int GEC = 8;                   // columns exchanged at a time between gate and up lanes
 constexpr int GMAXENT = MAX_E + MAX_SHARED;
 constexpr uint32_t GTMEM = 512;
+constexpr int G_MAX_SMEM = 227 * 1024;   // dynamic shared memory of a CTA
 
 struct Mx4Maps {
   CUtensorMap w, w_sh;   // 64 rows x 128 bytes of weight codes (routed or grouped, shared)
@@ -481,6 +482,7 @@ cudaError_t launch_mode(const Mx4Gemm& A, cudaStream_t st) {
   T.n = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
   T.stages = T.n == 128 ? 3 : T.n == 64 ? 4 : 5;
   const Mx4Smem S = g_smem(T);
+  if (S.total > (uint32_t)G_MAX_SMEM) return cudaErrorInvalidConfiguration;
   Mx4Maps maps{};
   const coli_moe_cfg& c = A.cfg;
   const size_t pitch = MODE == MX4_PRODUCT ? A.K : MODE == MX4_GATE_UP ? c.hidden : c.inter;
@@ -492,8 +494,15 @@ cudaError_t launch_mode(const Mx4Gemm& A, cudaStream_t st) {
     ok = encode_bytes(&maps.w_sh, A.shc, (MODE == MX4_GATE_UP ? c.hidden : c.shared_inter) / 2,
                       (size_t)c.n_shared * 3 * (MODE == MX4_GATE_UP ? c.shared_inter : c.hidden), 64);
   if (!ok) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(mx4_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S.total);
-  if (e != cudaSuccess) return e;
+  // the kernel's shared-memory limit is raised once per device, to the most any tile needs
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!(raised.load(std::memory_order_acquire) >> dev & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(mx4_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, G_MAX_SMEM);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(1ull << dev, std::memory_order_release);
+  }
   return launch_pdl(mx4_gemm<MODE>, (unsigned)sms, GTHREADS, S.total, st, maps, A, T);
 }
 
