@@ -48,6 +48,11 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 template <bool VEC>
 __device__ __forceinline__ void load_w(const float* p, int n, float* v) {
   if (VEC) {
+    if (n <= 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      return;
+    }
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   } else {
@@ -56,138 +61,116 @@ __device__ __forceinline__ void load_w(const float* p, int n, float* v) {
   }
 }
 
-// U units of 8 elements per thread; WARP: one row per warp, else per CTA
+// U units of 8 elements per thread; WARP: one row per warp, else per CTA.
+// Every load of the row (x, y and gate) is issued before the first reduction.
 template <typename T, typename TN, int U, bool VEC, bool WARP>
-__global__ void __launch_bounds__(U == 4 ? 512 : 1024) norm_kernel(const NormParams P) {
+__global__ void __launch_bounds__(U <= 2 ? 1024 : 512) norm_kernel(const NormParams P) {
   __shared__ float red[2][32];
   const int H = P.H;
   const int nthr = WARP ? 32 : (int)blockDim.x, t = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-  const int per_cta = WARP ? (int)(blockDim.x >> 5) : 1;
-  const long long first = (long long)blockIdx.x * per_cta + (WARP ? (threadIdx.x >> 5) : 0);
+  const long long row = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (long long)blockIdx.x;
   pdl_wait();
   pdl_trigger();
-  for (long long row = first; row < P.rows; row += (long long)gridDim.x * per_cta) {
-    const T* xr = static_cast<const T*>(P.x) + row * P.ldx;
-    const T* yr = P.y ? static_cast<const T*>(P.y) + row * P.ldy : nullptr;
-    const T* gr = P.gate ? static_cast<const T*>(P.gate) + row * P.ldg : nullptr;
-    float x[U][8], y[U][8];
-    float ss = 0.f;
+  if (row >= P.rows) return;  // (whole warps; a CTA's row always exists)
+  Raw8<T> xr[U], yr[U], gr[U];
+  const bool with_y = P.y != nullptr, gated = P.gate != nullptr;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int k = (u * nthr + t) * 8;
+    xr[u] = load8<T, VEC>(static_cast<const T*>(P.x) + row * P.ldx + k, H - k);
+    if (with_y) yr[u] = load8<T, VEC>(static_cast<const T*>(P.y) + row * P.ldy + k, H - k);
+    if (gated) gr[u] = load8<T, VEC>(static_cast<const T*>(P.gate) + row * P.ldg + k, H - k);
+  }
+  float c = P.res_scale, ss = 0.f;
+  if (P.post_w) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = (u * nthr + t) * 8;
-      const int n = H - k;
-      if (n > 0) {
-        load8<T, VEC>(xr + k, n, x[u]);
-        if (yr) load8<T, VEC>(yr + k, n, y[u]);
-      } else {
+      float y[8];
+      floats8(yr[u], y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] = y[u][i] = 0.f;
-      }
+      for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
     }
-    if (yr) {
-      float c = P.res_scale;
+    c *= rsqrtf(row_sum<WARP>(ss, red[0]) / (float)H + P.eps);
+  }
+  float x[U][8];
+  ss = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int k = (u * nthr + t) * 8, n = H - k;
+    floats8(xr[u], x[u]);
+    if (with_y) {
+      float y[8], w[8];
+      floats8(yr[u], y);
       if (P.post_w) {
+        load_w<VEC>(P.post_w + k, n, w);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int i = 0; i < 8; ++i) y[i] *= w[i];
+      }
+      if (gated) {
+        floats8(gr[u], w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss += y[u][i] * y[u][i];
-        c *= rsqrtf(row_sum<WARP>(ss, red[0]) / (float)H + P.eps);
+        for (int i = 0; i < 8; ++i) y[i] *= w[i];
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (u * nthr + t) * 8;
-        const int n = H - k;
-        if (n <= 0) continue;
-        float w[8];
-        if (P.post_w) {
-          load_w<VEC>(P.post_w + k, n, w);
+      for (int i = 0; i < 8; ++i) x[u][i] += c * y[i];
+    }
+    if (P.x_out && n > 0) store8<T, VEC>(static_cast<T*>(P.x_out) + row * P.ldxo + k, n, x[u]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[u][i] *= w[i];
-        }
-        if (gr) {
-          load8<T, VEC>(gr + k, n, w);
+    for (int i = 0; i < 8; ++i) ss += x[u][i] * x[u][i];
+  }
+  if (!P.n_out && !P.codes) return;
+  c = rsqrtf(row_sum<WARP>(ss, red[1]) / (float)H + P.eps);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[u][i] *= w[i];
-        }
+  for (int u = 0; u < U; ++u) {
+    const int k = (u * nthr + t) * 8, n = H - k;
+    float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] += c * y[u][i];
-        if (P.x_out) store8<T, VEC>(static_cast<T*>(P.x_out) + row * P.ldxo + k, n, x[u]);
-      }
-    } else if (P.x_out) {
+    for (int i = 0; i < 8; ++i) v[i] = x[u][i] * c;
+    if (P.pre_w) {
+      float w[8];
+      load_w<VEC>(P.pre_w + k, n, w);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (u * nthr + t) * 8;
-        if (k < H) store8<T, VEC>(static_cast<T*>(P.x_out) + row * P.ldxo + k, H - k, x[u]);
+      for (int i = 0; i < 8; ++i) v[i] *= w[i];
+    }
+    if (P.n_out && n > 0) store8<TN, VEC>(static_cast<TN*>(P.n_out) + row * P.ldno + k, n, v);
+    if (P.codes) {  // H % 32 == 0: a block's four lanes are in or out together
+      uint32_t b;
+      const uint32_t q = mx4_quant8(v, &b);
+      if (n > 0) {
+        reinterpret_cast<uint32_t*>(P.codes)[(row * H + k) / 8] = q;
+        if ((t & 3) == 0) P.scales[(row * H + k) / MXB] = (uint8_t)b;
       }
     }
-    if (!P.n_out && !P.codes) {
-      if (!WARP) __syncthreads();
-      continue;
-    }
-    ss = 0.f;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[u][i] * x[u][i];
-    const float c = rsqrtf(row_sum<WARP>(ss, red[1]) / (float)H + P.eps);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = (u * nthr + t) * 8;
-      const int n = H - k;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = x[u][i] * c;
-      if (P.pre_w && n > 0) {
-        float w[8];
-        load_w<VEC>(P.pre_w + k, n, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= w[i];
-      }
-      if (P.n_out && n > 0) store8<TN, VEC>(static_cast<TN*>(P.n_out) + row * P.ldno + k, n, v);
-      if (P.codes) {  // H % 32 == 0: a block's four lanes are in or out together
-        uint32_t b;
-        const uint32_t q = mx4_quant8(v, &b);
-        if (n > 0) {
-          reinterpret_cast<uint32_t*>(P.codes)[(row * H + k) / 8] = q;
-          if ((t & 3) == 0) P.scales[(row * H + k) / MXB] = (uint8_t)b;
-        }
-      }
-    }
-    if (!WARP) __syncthreads();  // both partial arrays are free for the next row
   }
 }
 
 template <typename T, typename TN, int U>
-cudaError_t launch_u(const NormParams& P, bool vec, bool warp, unsigned grid, unsigned block, cudaStream_t st) {
-  if (warp)
-    return vec ? launch_pdl(norm_kernel<T, TN, U, true, true>, grid, block, 0, st, P)
-               : launch_pdl(norm_kernel<T, TN, U, false, true>, grid, block, 0, st, P);
+cudaError_t launch_u(const NormParams& P, bool vec, unsigned block, cudaStream_t st) {
+  const unsigned grid = (unsigned)P.rows;
   return vec ? launch_pdl(norm_kernel<T, TN, U, true, false>, grid, block, 0, st, P)
              : launch_pdl(norm_kernel<T, TN, U, false, false>, grid, block, 0, st, P);
 }
 
 // Threads of a row: one warp up to 512 elements (no barrier); else a CTA with
 // one unit per thread, which is the shortest chain for few rows, or with more
-// rows than SMs up to four units per thread, so that several small CTAs share
-// an SM and their loads cover each other's reductions.
+// rows than SMs 256 threads of up to four units (512 beyond 8192 elements),
+// so that several CTAs share an SM and cover each other's reductions.
 template <typename T, typename TN>
 cudaError_t launch(const NormParams& P, bool vec, cudaStream_t st) {
   const int units = (P.H + 7) / 8;
-  const int sms = device_sms() > 0 ? device_sms() : 152;
+  const int sms = device_sms();
   if (units <= 64) {
-    const long long blocks = ((long long)P.rows + 7) / 8;
-    const long long cap = 8LL * sms;
-    const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
-    return units <= 32 ? launch_u<T, TN, 1>(P, vec, true, grid, 256, st) : launch_u<T, TN, 2>(P, vec, true, grid, 256, st);
+    const unsigned grid = (unsigned)(((long long)P.rows + 7) / 8);
+    return vec ? launch_pdl(norm_kernel<T, TN, 2, true, true>, grid, 256, 0, st, P)
+               : launch_pdl(norm_kernel<T, TN, 2, false, true>, grid, 256, 0, st, P);
   }
-  int u = units > 1024 ? 2 : 1;
-  while (u < 4 && P.rows > sms && (units + u - 1) / u > 256) u *= 2;
+  const int most = P.rows <= sms ? 1024 : units <= 1024 ? 256 : 512;
+  const int u = (units + most - 1) / most;
   const unsigned block = (unsigned)(((units + u - 1) / u + 31) / 32 * 32);
-  const long long cap = (2048 / block) * (long long)sms;
-  const unsigned grid = (unsigned)(P.rows < cap ? P.rows : cap);
-  if (u == 1) return launch_u<T, TN, 1>(P, vec, false, grid, block, st);
-  if (u == 2) return launch_u<T, TN, 2>(P, vec, false, grid, block, st);
-  return launch_u<T, TN, 4>(P, vec, false, grid, block, st);
+  if (u == 1) return launch_u<T, TN, 1>(P, vec, block, st);
+  if (u == 2) return launch_u<T, TN, 2>(P, vec, block, st);
+  if (u == 3) return launch_u<T, TN, 3>(P, vec, block, st);
+  return launch_u<T, TN, 4>(P, vec, block, st);
 }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }

@@ -83,27 +83,49 @@ __device__ __forceinline__ uint32_t mx4_quant8(const float* v, uint32_t* byte) {
   return w;
 }
 
-// 8 consecutive elements as floats: one or two 16-byte loads (VEC: the address
-// is 16-byte aligned and all 8 exist) or n guarded single loads (zero beyond)
+// 8 consecutive elements as they are in memory, so that a thread can have many
+// loads in flight in few registers.  VEC: the address is 16-byte aligned and
+// all 8 exist (one or two 16-byte loads); otherwise n guarded single loads,
+// zero beyond.
+template <typename T>
+struct Raw8 {
+  uint4 q[sizeof(T) / 2];
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, float* v) {
+__device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
+  Raw8<T> r;
   if (VEC) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const T* h = reinterpret_cast<const T*>(&w[i]);
-        v[2 * i] = to_f32(h[0]);
-        v[2 * i + 1] = to_f32(h[1]);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = n > 0 ? __ldcs(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+  } else {
+    constexpr int PER = 4 / sizeof(T);  // elements in a 32-bit word
+    uint32_t w[2 * sizeof(T)] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= n) continue;
+      if constexpr (PER == 1) w[i] = __float_as_uint(p[i]);
+      else w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+    }
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void floats8(const Raw8<T>& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+    const uint32_t w[4] = {r.q[i].x, r.q[i].y, r.q[i].z, r.q[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        v[4 * i + j] = __uint_as_float(w[j]);
+      } else {
+        const T* h = reinterpret_cast<const T*>(&w[j]);
+        v[2 * j] = to_f32(h[0]);
+        v[2 * j + 1] = to_f32(h[1]);
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
   }
 }
 template <typename T, bool VEC>

@@ -95,127 +95,215 @@ __global__ void __launch_bounds__(TT) mx4_tables(const coli_moe_cfg c, const Mx4
   }
 }
 
-// MX4 of each token's row (or the caller's codes), written to every row of
-// the token's experts.  A warp takes 1024 elements of one token.
-template <typename T, int TYPE>
+// MX4 of one unit (8 elements a lane, 256 a warp) of a token's row, or the
+// caller's codes: the lane's codes and its block's scale byte.
+template <typename T>
+__device__ __forceinline__ uint32_t unit_codes(const T* x, const uint8_t* x_scales, long long at, bool in, uint32_t* b) {
+  if constexpr (sizeof(T) == 1) {  // codes
+    *b = in ? x_scales[at / MXB] : 0u;
+    return in ? reinterpret_cast<const uint32_t*>(x)[at / 8] : 0u;
+  } else {
+    float v[8];
+    floats8(load8<T, true>(x + at, in ? 8 : 0), v);
+    return mx4_quant8(v, b);
+  }
+}
+
+// Writes a lane's U units (codes w, scale bytes b, elements k0 + 256 u) to the
+// rows that lanes 0 .. n-1 hold in `row` (-1: none).
+template <int U>
+__device__ __forceinline__ void scatter_units(uint8_t* ws, const Mx4Layout& L, int H, const uint32_t* w, const uint32_t* b, int k0,
+                                              int row, int n) {
+  const int lane = threadIdx.x & 31;
+  uint32_t* xq = reinterpret_cast<uint32_t*>(ws + L.xq);
+  uint8_t* xs = ws + L.xs;
+  bool bad = false;
+  for (int j = 0; j < n; ++j) {
+    const int r = __shfl_sync(0xffffffffu, row, j);
+    if (r < 0) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u * 256 < H) {
+        const long long at = (long long)r * H + k0 + u * 256;
+        xq[at / 8] = w[u];
+        if ((lane & 3) == 0) xs[at / MXB] = (uint8_t)b[u];
+        bad |= b[u] == 255u;
+      }
+  }
+  if (bad) atomicOr(reinterpret_cast<uint32_t*>(ws), COLI_STATUS_NONFINITE);
+}
+
+// MX4 of each token's row, written to every row of the token's experts.  A
+// warp takes 1024 elements of one token.
+template <typename T>
 __global__ void __launch_bounds__(256) mx4_gather(const coli_moe_cfg c, const Mx4Layout L, const T* __restrict__ x,
                                                   const uint8_t* __restrict__ x_scales, int rows, uint8_t* __restrict__ ws) {
   const int lane = threadIdx.x & 31, H = c.hidden, k = c.top_k, ns = c.n_shared;
   const int per_row = (H + 1023) / 1024;
-  const long long tasks = (long long)rows * per_row, step = (long long)gridDim.x * 8;
+  const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   pdl_wait();
   pdl_trigger();
-  const int32_t* hdr = reinterpret_cast<const int32_t*>(ws + L.hdr);
+  if (task >= (long long)rows * per_row) return;
+  const int t = (int)(task / per_row), k0 = (int)(task - (long long)t * per_row) * 1024 + lane * 8;
   const int32_t* slot = reinterpret_cast<const int32_t*>(ws + L.slot);
-  const int shared0 = __ldcg(hdr + MH_NPAIRS) - ns * rows;
-  uint32_t* xq = reinterpret_cast<uint32_t*>(ws + L.xq);
-  uint8_t* xs = ws + L.xs;
-  for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < tasks; task += step) {
-    const int t = (int)(task / per_row);
-    const int k0 = (int)(task - (long long)t * per_row) * 1024 + lane * 8;
-    uint32_t w[4] = {}, b[4] = {};
-    if constexpr (TYPE == COLI_MX4) {
+  const int shared0 = __ldcg(reinterpret_cast<const int32_t*>(ws + L.hdr) + MH_NPAIRS) - ns * rows;
+  uint32_t w[4], b[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (k0 + u * 256 < H) {
-          const long long at = (long long)t * H + k0 + u * 256;
-          w[u] = reinterpret_cast<const uint32_t*>(x)[at / 8];
-          b[u] = x_scales[at / MXB];
-        }
-    } else {
-      float v[4][8];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (k0 + u * 256 < H) {
-          load8<T, true>(x + (long long)t * H + k0 + u * 256, 8, v[u]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = mx4_quant8(v[u], &b[u]);
-    }
-    bool bad = false;
-    for (int j = 0; j < k + ns; ++j) {
-      const int r = j < k ? __ldcg(slot + (long long)t * k + j) : shared0 + (j - k) * rows + t;
-      if (r < 0) continue;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (k0 + u * 256 < H) {
-          const long long at = (long long)r * H + k0 + u * 256;
-          xq[at / 8] = w[u];
-          if ((lane & 3) == 0) xs[at / MXB] = (uint8_t)b[u];
-          bad |= b[u] == 255u;
-        }
-    }
-    if (bad) atomicOr(reinterpret_cast<uint32_t*>(ws), COLI_STATUS_NONFINITE);
+  for (int u = 0; u < 4; ++u) w[u] = unit_codes(x, x_scales, (long long)t * H + k0 + u * 256, k0 + u * 256 < H, &b[u]);
+  for (int j0 = 0; j0 < k + ns; j0 += 32) {
+    const int j = j0 + lane;
+    const int row = j < k ? __ldcg(slot + (long long)t * k + j) : shared0 + (j - k) * rows + t;
+    scatter_units<4>(ws, L, H, w, b, k0, row, min(32, k + ns - j0));
   }
 }
 
-// y[t] = sum_j w[t][j] o[row(t, j)] + sum_s o[shared row of t], in this order
+// Tables and activations of calls of few pairs in one launch: every CTA works
+// out all pairs' rows by itself (in the order of (expert, pair), from the at
+// most PREP_PAIRS ids in shared memory), CTA 0 writes the tables, and each
+// warp quantises 256 elements of one token.
+constexpr int PREP_PAIRS = 256;
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_prep_small(const coli_moe_cfg c, const Mx4Layout L, const T* __restrict__ x,
+                                                      const uint8_t* __restrict__ x_scales, int rows, const int32_t* __restrict__ idx,
+                                                      uint8_t* __restrict__ ws) {
+  __shared__ int s_id[PREP_PAIRS], s_row[PREP_PAIRS];
+  const int tid = threadIdx.x, lane = tid & 31, H = c.hidden, E = c.n_experts, k = c.top_k, ns = c.n_shared, np = rows * k;
+  constexpr int NONE = 0x7fffffff;
+  pdl_wait();
+  pdl_trigger();
+  // this warp's activations are on their way while the pairs are sorted
+  const int per_row = H / 256 + (H % 256 ? 1 : 0);
+  const int task = blockIdx.x * 8 + (tid >> 5);
+  const int t = task / per_row, k0 = (task - t * per_row) * 256 + lane * 8;
+  uint32_t w[1], b[1];
+  w[0] = unit_codes(x, x_scales, (long long)t * H + k0, t < rows && k0 < H, &b[0]);
+  bool bad = false;
+  int id = NONE;
+  if (tid < np) {
+    const int e = idx[tid];
+    const bool in = e >= 0 && e < E;
+    bad = !in && e != -1;
+    id = in && ep_owned(c, e) ? e : NONE;
+  }
+  s_id[tid] = id;
+  if (bad && blockIdx.x == 0) atomicOr(reinterpret_cast<uint32_t*>(ws), COLI_STATUS_BADIDX);
+  __syncthreads();
+  // row = pairs of lower experts + earlier pairs of the same one
+  int row = 0, before = 0, same = 0, firsts = 0;
+  for (int q = 0; q < np; ++q) {
+    const int o = s_id[q];
+    row += o < id || (o == id && q < tid);
+    before += o == id && q < tid;
+    same += o == id;
+  }
+  const bool first = id != NONE && before == 0;
+  s_row[tid] = id == NONE ? -1 : row;
+  const int pairs = __syncthreads_count(id != NONE);
+  if (blockIdx.x == 0) {
+    // entry number: first pairs of lower experts
+    int32_t* ent_expert = reinterpret_cast<int32_t*>(ws + L.ent_expert);
+    int32_t* ent_count = reinterpret_cast<int32_t*>(ws + L.ent_count);
+    int32_t* ent_offset = reinterpret_cast<int32_t*>(ws + L.ent_offset);
+    int32_t* hdr = reinterpret_cast<int32_t*>(ws + L.hdr);
+    s_id[tid] = first ? id : NONE;
+    const int uniq = __syncthreads_count(first);
+    for (int q = 0; q < np; ++q) firsts += s_id[q] < id;
+    if (first) {
+      ent_expert[firsts] = id;
+      ent_count[firsts] = same;
+      ent_offset[firsts] = row;
+    }
+    if (tid < ns) {
+      ent_expert[uniq + tid] = E + tid;
+      ent_count[uniq + tid] = rows;
+      ent_offset[uniq + tid] = pairs + tid * rows;
+    }
+    if (tid == 0) {
+      ent_offset[uniq + ns] = pairs + ns * rows;
+      hdr[MH_NENT] = uniq + ns;
+      hdr[MH_NUNIQ] = uniq;
+      hdr[MH_NPAIRS] = pairs + ns * rows;
+    }
+    if (tid < np) reinterpret_cast<int32_t*>(ws + L.slot)[tid] = s_row[tid];
+  }
+  if (t >= rows) return;  // (whole warps)
+  for (int j0 = 0; j0 < k + ns; j0 += 32) {
+    const int j = j0 + lane;
+    const int r = j < k ? s_row[t * k + j] : pairs + (j - k) * rows + t;
+    scatter_units<1>(ws, L, H, w, b, k0, r, min(32, k + ns - j0));
+  }
+}
+
+// y[t] = sum_j w[t][j] o[row(t, j)] + sum_s o[shared row of t], in this order;
+// eight rows' loads in flight at a time
 __global__ void __launch_bounds__(256) mx4_combine(const coli_moe_cfg c, const Mx4Layout L, const uint8_t* __restrict__ ws, int T,
                                                    const float* __restrict__ topk_w, void* __restrict__ y, int32_t y_type) {
   const int H = c.hidden, k = c.top_k, ns = c.n_shared, h4 = H / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(i / h4), c4 = (int)(i - (long long)t * h4);
   pdl_wait();
   pdl_trigger();
-  const int32_t* slot = reinterpret_cast<const int32_t*>(ws + L.slot);
+  if (t >= T) return;
+  const int32_t* slot = reinterpret_cast<const int32_t*>(ws + L.slot) + (long long)t * k;
   const int shared0 = __ldcg(reinterpret_cast<const int32_t*>(ws + L.hdr) + MH_NPAIRS) - ns * T;
   const float* o = reinterpret_cast<const float*>(ws + L.o);
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)T * h4; i += (long long)gridDim.x * 256) {
-    const int t = (int)(i / h4), c4 = (int)(i - (long long)t * h4);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < k + ns; ++j) {
-      const int r = j < k ? __ldcg(slot + (long long)t * k + j) : shared0 + (j - k) * T + t;
-      if (r < 0) continue;
-      const float w = j < k ? topk_w[(long long)t * k + j] : 1.f;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(o + (long long)r * H) + c4);
-      a.x += w * v.x; a.y += w * v.y; a.z += w * v.z; a.w += w * v.w;
-    }
-    if (y_type == COLI_F32) {
-      reinterpret_cast<float4*>(y)[i] = a;
-    } else {
-      const float v[4] = {a.x, a.y, a.z, a.w};
-      uint32_t p[2];
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int B = 8;
+  for (int j0 = 0; j0 < k + ns; j0 += B) {
+    int r[B];
+    float w[B];
+    float4 v[B];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (y_type == COLI_BF16) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
-          p[q] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-          const __half2 h = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
-          p[q] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      }
-      reinterpret_cast<uint2*>(y)[i] = make_uint2(p[0], p[1]);
+    for (int q = 0; q < B; ++q) {
+      const int j = j0 + q;
+      r[q] = j < k ? __ldcg(slot + j) : j < k + ns ? shared0 + (j - k) * T + t : -1;
+      w[q] = j < k ? __ldg(topk_w + (long long)t * k + j) : 1.f;
     }
+#pragma unroll
+    for (int q = 0; q < B; ++q)
+      if (r[q] >= 0) v[q] = __ldcs(reinterpret_cast<const float4*>(o + (long long)r[q] * H) + c4);
+#pragma unroll
+    for (int q = 0; q < B; ++q)
+      if (r[q] >= 0) {
+        a.x += w[q] * v[q].x; a.y += w[q] * v[q].y; a.z += w[q] * v[q].z; a.w += w[q] * v[q].w;
+      }
   }
+  if (y_type == COLI_F32) {
+    reinterpret_cast<float4*>(y)[i] = a;
+  } else if (y_type == COLI_BF16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a.x, a.y), q = __floats2bfloat162_rn(a.z, a.w);
+    reinterpret_cast<uint2*>(y)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+  } else {
+    const __half2 p = __floats2half2_rn(a.x, a.y), q = __floats2half2_rn(a.z, a.w);
+    reinterpret_cast<uint2*>(y)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+  }
+}
+
+template <typename T>
+cudaError_t dispatch(const coli_moe_cfg& c, const Mx4Layout& L, const T* x, const uint8_t* x_scales, int rows, const int32_t* idx,
+                     uint8_t* ws, cudaStream_t st) {
+  if (rows * c.top_k <= PREP_PAIRS && rows <= PREP_PAIRS) {
+    const unsigned tasks = (unsigned)rows * (unsigned)((c.hidden + 255) / 256);
+    return launch_pdl(mx4_prep_small<T>, (tasks + 7) / 8, 256, 0, st, c, L, x, x_scales, rows, idx, ws);
+  }
+  const cudaError_t e = launch_pdl(mx4_tables, 1, TT, 0, st, c, L, idx, rows, ws);
+  if (e != cudaSuccess) return e;
+  const long long tasks = (long long)rows * ((c.hidden + 1023) / 1024);
+  return launch_pdl(mx4_gather<T>, (unsigned)((tasks + 7) / 8), 256, 0, st, c, L, x, x_scales, rows, ws);
 }
 
 cudaError_t launch_mx4_dispatch(const coli_moe_cfg& c, const Mx4Layout& L, const void* x, int32_t x_type, const uint8_t* x_scales,
                                 int T, const int32_t* idx, uint8_t* ws, cudaStream_t st) {
-  const cudaError_t e = launch_pdl(mx4_tables, 1, TT, 0, st, c, L, idx, T, ws);
-  if (e != cudaSuccess) return e;
-  const int sms = device_sms() > 0 ? device_sms() : 152;
-  const long long tasks = (long long)T * ((c.hidden + 1023) / 1024);
-  long long blocks = (tasks + 7) / 8;
-  if (blocks > 8LL * sms) blocks = 8LL * sms;
-  const unsigned grid = (unsigned)blocks;
-  if (x_type == COLI_F32)
-    return launch_pdl(mx4_gather<float, COLI_F32>, grid, 256, 0, st, c, L, static_cast<const float*>(x), x_scales, T, ws);
-  if (x_type == COLI_BF16)
-    return launch_pdl(mx4_gather<__nv_bfloat16, COLI_BF16>, grid, 256, 0, st, c, L, static_cast<const __nv_bfloat16*>(x), x_scales, T, ws);
-  if (x_type == COLI_F16)
-    return launch_pdl(mx4_gather<__half, COLI_F16>, grid, 256, 0, st, c, L, static_cast<const __half*>(x), x_scales, T, ws);
-  return launch_pdl(mx4_gather<uint8_t, COLI_MX4>, grid, 256, 0, st, c, L, static_cast<const uint8_t*>(x), x_scales, T, ws);
+  if (x_type == COLI_F32) return dispatch(c, L, static_cast<const float*>(x), x_scales, T, idx, ws, st);
+  if (x_type == COLI_BF16) return dispatch(c, L, static_cast<const __nv_bfloat16*>(x), x_scales, T, idx, ws, st);
+  if (x_type == COLI_F16) return dispatch(c, L, static_cast<const __half*>(x), x_scales, T, idx, ws, st);
+  return dispatch(c, L, static_cast<const uint8_t*>(x), x_scales, T, idx, ws, st);
 }
 
 cudaError_t launch_mx4_combine(const coli_moe_cfg& c, const Mx4Layout& L, const uint8_t* ws, int T, const float* topk_w, void* y,
                                int32_t y_type, cudaStream_t st) {
-  const long long n4 = (long long)T * (c.hidden / 4);
-  const int sms = device_sms() > 0 ? device_sms() : 152;
-  long long blocks = (n4 + 255) / 256;
-  if (blocks > 8LL * sms) blocks = 8LL * sms;
+  const long long blocks = ((long long)T * (c.hidden / 4) + 255) / 256;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return launch_pdl(mx4_combine, (unsigned)blocks, 256, 0, st, c, L, ws, T, topk_w, y, y_type);
 }
 

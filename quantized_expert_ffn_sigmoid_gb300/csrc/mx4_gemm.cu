@@ -14,16 +14,20 @@
 // Gate/up tiles pair 64 gate rows with the same 64 up rows.  K runs in stages
 // of 512 (256 bytes of a row: two 128-byte swizzled boxes per operand).
 //
-// One persistent CTA per SM, ten warps:
+// One persistent CTA per SM, thirteen warps:
 //   warps 0-3  scales: bytes of the stage's rows by cp.async two stages ahead,
 //              then into tensor memory.  Row r of a 128-row tile is lane r % 32,
 //              column r / 32 (the four bytes of K / 128 in one 32-bit column),
 //              repeated in all four lane quarters, one quarter per warp;
 //   warps 4-7  epilogue: accumulators to y, or SwiGLU and MX4 of h;
-//   warp 8     TMA producer (codes);  warp 9  MMA issuer.
+//   warp 8     MMA issuer;
+//   warps 9-12 TMA producers of the codes, one for each 128-byte half of a
+//              stage of each operand (one thread issues a box of 8 KB every
+//              190 cycles, which alone held a stage back to 1150 cycles).
 // Two accumulators, so a tile's epilogue overlaps the next tile's products.
 // Every wait is bounded; an expired one sets COLI_STATUS_TIMEOUT and the rest
 // of the launch drains.
+#include <cstdlib>
 #include "mx4_layer.cuh"
 #include "tcgen05.cuh"
 #include "tensormap.cuh"
@@ -34,16 +38,16 @@ constexpr int GM = 128;                  // weight rows of a tile
 constexpr int GK = 512;                  // K of a stage
 constexpr uint32_t GABYTES = GM * GK / 2;  // 32 KB of weight codes per stage
 constexpr int GSR = 4;                   // ring of scale bytes in shared memory (two stages ahead + two)
-constexpr int GTHREADS = 320;
-constexpr int GW_EPI = 4, GW_TMA = 8, GW_MMA = 9;
+constexpr int GTHREADS = 416;
+constexpr int GW_EPI = 4, GW_MMA = 8, GW_TMA = 9;
 constexpr int GEC = 8;                   // columns exchanged at a time between gate and up lanes
 constexpr int GMAXENT = MAX_E + MAX_SHARED;
 constexpr uint32_t GTMEM = 512;
 constexpr int G_MAX_SMEM = 227 * 1024;   // dynamic shared memory of a CTA
 
 struct Mx4Maps {
-  CUtensorMap w, w_sh;   // 64 rows x 128 bytes of weight codes (routed or grouped, shared)
-  CUtensorMap x16, xn;   // 16 and n_tile rows x 128 bytes of activation codes
+  CUtensorMap w, w_sh;   // 128 bytes x 128 rows (gate/up: 64) of weight codes (routed or grouped, shared)
+  CUtensorMap x[4];      // 128 bytes x 16, 32, 64, 128 rows of activation codes, up to the tile's
 };
 
 // tile capacity on the N side and what follows from it
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], 1 + 4);
+      mbar_init(&full[i], 4 + 4);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -329,37 +333,53 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       }
     }
     cp_async_wait<0>();
-  } else if (warp == GW_TMA) {
+  } else if (warp >= GW_TMA) {
     if (lane == 0) {
-      // ------------------------------------------------------------ TMA producer
+      // ------------------------------------------------------------ TMA producers
+      const int h = (warp - GW_TMA) & 1;         // 128-byte half of the stage
+      const bool weights = warp - GW_TMA < 2;
+      const uint64_t stream = policy_evict_first();
       uint32_t gs = 0;
       bool go = true;
       for (int item = blockIdx.x; item < n_items && go; item += gridDim.x) {
         const Item it = item_at(item);
         const CUtensorMap* wm = it.shared ? &maps.w_sh : &maps.w;
-        const int w0 = (int)it.wrow, w1 = MODE == MX4_GATE_UP ? w0 + it.rows : w0 + 64;
-        const int n16 = (it.ntok + 15) / 16;
+        const int w0 = (int)it.wrow, n16 = (it.ntok + 15) / 16;
         for (int st = 0; st < it.nst; ++st, ++gs) {
           const uint32_t s = gs % NST;
           if (!pf_wait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
+          const int x = st * (GK / 2) + h * 128;
+          if (x >= it.K / 2) {  // nothing of the row in this half: no products either
+            mbar_arrive(&full[s]);
+            continue;
+          }
           uint8_t* dst = sm + (size_t)s * STAGE;
-          uint8_t* bdst = dst + GABYTES;
-          const int halves = it.K - st * GK > GK / 2 ? 2 : 1;  // 128-byte boxes that hold any of the row
-          mbar_arrive_expect_tx(&full[s], (uint32_t)halves * (GABYTES / 2 + (uint32_t)n16 * 2048));
-          for (int h = 0; h < halves; ++h) {
-            const int x = st * (GK / 2) + h * 128;
-            tma_load_2d(dst + h * (GABYTES / 2), wm, x, w0, &full[s]);
-            tma_load_2d(dst + h * (GABYTES / 2) + GABYTES / 4, wm, x, w1, &full[s]);
-            if (n16 * 16 == T.n) {
-              tma_load_2d(bdst + h * T.n * 128, &maps.xn, x, it.row0, &full[s]);
+          if (weights) {
+            dst += h * (GABYTES / 2);
+            mbar_arrive_expect_tx(&full[s], GABYTES / 2);
+            if (MODE == MX4_GATE_UP) {
+              tma_load_2d_hint(dst, wm, x, w0, &full[s], stream);
+              tma_load_2d_hint(dst + GABYTES / 4, wm, x, w0 + it.rows, &full[s], stream);
+            } else if (MODE == MX4_DOWN) {
+              tma_load_2d_hint(dst, wm, x, w0, &full[s], stream);
             } else {
-              for (int i = 0; i < n16; ++i) tma_load_2d(bdst + h * T.n * 128 + i * 2048, &maps.x16, x, it.row0 + 16 * i, &full[s]);
+              tma_load_2d(dst, wm, x, w0, &full[s]);
             }
+          } else {
+            dst += GABYTES + h * T.n * 128;
+            mbar_arrive_expect_tx(&full[s], (uint32_t)n16 * 2048);
+            int row = 0;
+#pragma unroll
+            for (int i = 3; i >= 0; --i)  // the rows in boxes of 128, 64, 32, 16
+              if (n16 >> i & 1) {
+                tma_load_2d(dst + row * 128, &maps.x[i], x, it.row0 + row, &full[s]);
+                row += 16 << i;
+              }
           }
         }
       }
       // every copy issued has landed before the CTA can exit; a stage's phase
-      // also needs the scale warps, so after an abort this wait is bounded
+      // also needs the other warps, so after an abort this wait is bounded
       for (uint32_t k = gs > (uint32_t)NST ? gs - NST : 0; k < gs; ++k)
         for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full[k % NST], (k / NST) & 1u); ++i) {
         }
@@ -380,11 +400,19 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
             tmem_fence_after();
             const uint32_t a0 = smem_u32(sm + (size_t)s * STAGE), b0 = a0 + GABYTES;
             const uint32_t sa = taddr + sc_col0 + s * GSCOLS, sb = sa + 16;
+            // kept short: this thread's instructions are on the pipeline's critical path
+            const uint64_t da = umma_desc_sw128(a0), db = umma_desc_sw128(b0);
+            const uint32_t bh = (uint32_t)T.n * 8;  // second box of B, in descriptor units of 16 bytes
             const int steps = min(GK / 64, (it.K - st * GK + 63) / 64);
-            for (int k = 0; k < steps; ++k) {
-              const uint32_t h = (uint32_t)k >> 2, o = ((uint32_t)k & 3u) * 32, j = (uint32_t)k >> 1, id = ((uint32_t)k & 1u) * 2;
-              umma_mx4(d, umma_desc_sw128(a0 + h * (GABYTES / 2) + o), umma_desc_sw128(b0 + h * (uint32_t)T.n * 128 + o),
-                       idesc | (id << 4) | (id << 29), sa + 4 * j, sb + 4 * j, (st | k) != 0);
+            if (steps == GK / 64) {
+#pragma unroll
+              for (int k = 0; k < GK / 64; ++k)
+                umma_mx4(d, da + (k >> 2) * (GABYTES / 32) + (k & 3) * 2, db + (k >> 2) * bh + (k & 3) * 2,
+                         idesc | ((k & 1) * ((2u << 4) | (2u << 29))), sa + 4 * (k >> 1), sb + 4 * (k >> 1), k ? 1u : (uint32_t)(st != 0));
+            } else {
+              for (int k = 0; k < steps; ++k)
+                umma_mx4(d, da + (k >> 2) * (GABYTES / 32) + (k & 3) * 2, db + (k >> 2) * bh + (k & 3) * 2,
+                         idesc | ((k & 1) * ((2u << 4) | (2u << 29))), sa + 4 * (k >> 1), sb + 4 * (k >> 1), (st | k) != 0);
             }
           }
           umma_commit(&empty[s]);
@@ -479,7 +507,9 @@ cudaError_t launch_mode(const Mx4Gemm& A, cudaStream_t st) {
   // most rows an entry can hold
   const int most = MODE == MX4_PRODUCT ? A.P : A.L.T;
   Mx4Tile T;
+  const int n_env = getenv("MXN") ? atoi(getenv("MXN")) : 0;
   T.n = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
+  if (n_env && n_env < T.n) T.n = n_env;
   T.stages = T.n == 128 ? 3 : T.n == 64 ? 4 : 5;
   const Mx4Smem S = g_smem(T);
   if (S.total > (uint32_t)G_MAX_SMEM) return cudaErrorInvalidConfiguration;
@@ -487,12 +517,13 @@ cudaError_t launch_mode(const Mx4Gemm& A, cudaStream_t st) {
   const coli_moe_cfg& c = A.cfg;
   const size_t pitch = MODE == MX4_PRODUCT ? A.K : MODE == MX4_GATE_UP ? c.hidden : c.inter;
   const size_t rows = MODE == MX4_PRODUCT ? (size_t)A.G * A.N : (size_t)ep_records(c) * 3 * (MODE == MX4_GATE_UP ? c.inter : c.hidden);
-  bool ok = encode_bytes(&maps.w, A.wc, pitch / 2, rows, 64) && encode_bytes(&maps.x16, A.xc, A.xpitch / 2, A.P, 16) &&
-            encode_bytes(&maps.xn, A.xc, A.xpitch / 2, A.P, T.n);
+  const uint32_t box = MODE == MX4_GATE_UP ? 64 : 128;
+  bool ok = encode_bytes(&maps.w, A.wc, pitch / 2, rows, box);
+  for (int i = 0; ok && 16 << i <= T.n; ++i) ok = encode_bytes(&maps.x[i], A.xc, A.xpitch / 2, A.P, 16u << i);
   maps.w_sh = maps.w;
   if (ok && MODE != MX4_PRODUCT && c.n_shared > 0)
     ok = encode_bytes(&maps.w_sh, A.shc, (MODE == MX4_GATE_UP ? c.hidden : c.shared_inter) / 2,
-                      (size_t)c.n_shared * 3 * (MODE == MX4_GATE_UP ? c.shared_inter : c.hidden), 64);
+                      (size_t)c.n_shared * 3 * (MODE == MX4_GATE_UP ? c.shared_inter : c.hidden), box);
   if (!ok) return cudaErrorInvalidValue;
   // the kernel's shared-memory limit is raised once per device, to the most any tile needs
   static std::atomic<uint64_t> raised{0};

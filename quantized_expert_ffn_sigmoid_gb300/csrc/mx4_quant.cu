@@ -28,22 +28,16 @@ __global__ void __launch_bounds__(QT) quantize_kernel(const T* __restrict__ x, l
     const long long row = task / per_row;
     const int k0 = (int)(task - row * per_row) * QW + lane * 8;
     const T* src = x + row * ldx;
-    float v[QU][8];
+    Raw8<T> r[QU];
+#pragma unroll
+    for (int u = 0; u < QU; ++u) r[u] = load8<T, VEC>(src + k0 + u * 256, K - (k0 + u * 256));
 #pragma unroll
     for (int u = 0; u < QU; ++u) {
       const int k = k0 + u * 256;
-      if (k < K) {
-        load8<T, VEC>(src + k, 8, v[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < QU; ++u) {
-      const int k = k0 + u * 256;
+      float v[8];
+      floats8(r[u], v);
       uint32_t b;
-      const uint32_t w = mx4_quant8(v[u], &b);
+      const uint32_t w = mx4_quant8(v, &b);
       if (k < K) {  // K % 32 == 0: a block's four lanes are in or out together
         reinterpret_cast<uint32_t*>(codes)[(row * K + k) / 8] = w;
         if ((lane & 3) == 0) scales[(row * K + k) / MXB] = (uint8_t)b;
@@ -86,12 +80,13 @@ __global__ void __launch_bounds__(QT) dequantize_kernel(const uint8_t* __restric
   }
 }
 
+// A CTA per 8 warp tasks: the hardware deals them out as CTAs end (a grid of
+// resident CTAs that stride over the tasks left a sixth of the last round
+// idle: 27.7 instead of XX us for 8192 x 6144 bf16).
 unsigned grid_for(long long rows, int K) {
   const long long tasks = rows * ((K + QW - 1) / QW);
-  long long blocks = (tasks + QT / 32 - 1) / (QT / 32);
-  const int sms = device_sms();
-  const long long cap = 8LL * (sms > 0 ? sms : 152);
-  return (unsigned)(blocks < cap ? blocks : cap);
+  const long long blocks = (tasks + QT / 32 - 1) / (QT / 32);
+  return (unsigned)(blocks < 0x7fffffffLL ? blocks : 0x7fffffffLL);
 }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }
