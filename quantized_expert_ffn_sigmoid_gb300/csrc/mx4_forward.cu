@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(TT) mx4_tables(const coli_moe_cfg c, const Mx4
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  for (int u = tid; u < L.n_ent_max; u += TT) reinterpret_cast<uint32_t*>(ws + L.ready)[u] = 0u;
+  if (tid == 0) *reinterpret_cast<uint32_t*>(ws + L.claim) = 0u;
   bool bad = false;
   for (int p = tid; p < np; p += TT) {
     const int e = idx[p];
@@ -200,6 +202,8 @@ __global__ void __launch_bounds__(256) mx4_prep_small(const coli_moe_cfg c, cons
   s_row[tid] = id == NONE ? -1 : row;
   const int pairs = __syncthreads_count(id != NONE);
   if (blockIdx.x == 0) {
+    for (int u = tid; u < L.n_ent_max; u += 256) reinterpret_cast<uint32_t*>(ws + L.ready)[u] = 0u;
+    if (tid == 0) *reinterpret_cast<uint32_t*>(ws + L.claim) = 0u;
     // entry number: first pairs of lower experts
     int32_t* ent_expert = reinterpret_cast<int32_t*>(ws + L.ent_expert);
     int32_t* ent_count = reinterpret_cast<int32_t*>(ws + L.ent_count);
@@ -358,7 +362,7 @@ extern "C" int coli_mx4_product(const uint8_t* x_codes, const uint8_t* x_scales,
   A.y_type = y_type;
   A.ldy = ldy;
   A.ws = static_cast<uint8_t*>(ws);
-  return rc_of(launch_mx4_gemm(A, MX4_PRODUCT, stream));
+  return rc_of(launch_mx4_product(A, stream));
 }
 
 extern "C" size_t coli_mx4_workspace_size(const coli_moe_cfg* cfg, int32_t max_T) {
@@ -401,13 +405,9 @@ extern "C" int coli_mx4_forward(const coli_moe_cfg* cfg, const coli_mx4_weights*
   A.xc = w8 + L.xq;
   A.xs = w8 + L.xs;
   A.xpitch = c.hidden;
-  if ((rc = rc_of(launch_mx4_gemm(A, MX4_GATE_UP, stream)))) return rc;
-  A.xc = w8 + L.hq;
-  A.xs = w8 + L.hs;
-  A.xpitch = L.imax;
   A.y = w8 + L.o;
   A.y_type = COLI_F32;
   A.ldy = c.hidden;
-  if ((rc = rc_of(launch_mx4_gemm(A, MX4_DOWN, stream)))) return rc;
+  if ((rc = rc_of(launch_mx4_layer(A, stream)))) return rc;
   return rc_of(launch_mx4_combine(c, L, w8, T, topk_w, y, y_type, stream));
 }

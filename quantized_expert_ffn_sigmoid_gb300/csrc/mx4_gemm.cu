@@ -1,6 +1,6 @@
 // Products of MX4 rows, grouped by expert, on the block-scaled 4-bit tensor
-// core instruction (tcgen05.mma kind::mxf4): the grouped product and the two
-// passes of the MX4 expert layer.
+// core instruction (tcgen05.mma kind::mxf4): the grouped product, and both
+// passes of the MX4 expert layer in one launch.
 //
 // Mathematics.  y[p][n] = sum_b 2^(sx[p][b] + sw[n][b] - 254) * sum_{k in b}
 // x[p][k] w[n][k] with b the blocks of 32.  The instruction takes 4-bit codes
@@ -14,16 +14,28 @@
 // Gate/up tiles pair 64 gate rows with the same 64 up rows.  K runs in stages
 // of 512 (256 bytes of a row: two 128-byte swizzled boxes per operand).
 //
-// One persistent CTA per SM, thirteen warps:
-//   warps 0-3  scales: bytes of the stage's rows by cp.async two stages ahead,
-//              then into tensor memory.  Row r of a 128-row tile is lane r % 32,
-//              column r / 32 (the four bytes of K / 128 in one 32-bit column),
-//              repeated in all four lane quarters, one quarter per warp;
-//   warps 4-7  epilogue: accumulators to y, or SwiGLU and MX4 of h;
-//   warp 8     MMA issuer;
-//   warps 9-12 TMA producers of the codes, one for each 128-byte half of a
-//              stage of each operand (one thread issues a box of 8 KB every
-//              190 cycles, which alone held a stage back to 1150 cycles).
+// Items are (entry, row tile, tile of activation rows), the last fastest, so
+// that neighbouring items share weight rows, which L2 then serves once.  The
+// layer's items are all gate/up items, then all down items, claimed in order
+// from a counter: a CTA that claims a down item knows that every gate/up item
+// is claimed by a running CTA, so its wait for the entry's h (a counter per
+// entry) ends however many CTAs are resident; meanwhile the down weights
+// already stream into the ring.
+//
+// One persistent CTA per SM, eighteen warps meeting at mbarriers:
+//   warps 0-3   scales into tensor memory.  Row r of a 128-row tile is lane
+//               r % 32, column r / 32 (the four bytes of K / 128 in one 32-bit
+//               column), repeated in all four lane quarters, one per warp;
+//   warps 4-7   epilogue: accumulators to y, or SwiGLU and MX4 of h;
+//   warp 8      MMA issuer;
+//   warps 9-12  TMA producers of the codes, one for each 128-byte half of a
+//               stage of each operand (one thread issues a box of 8 KB every
+//               190 cycles, which alone held a stage back to 1150 cycles);
+//   warp 13     schedule: claims and decodes items ahead of their use;
+//   warps 14-17 copy the stage's scale bytes, one row of each operand per
+//               thread, with cp.async (16 bytes where the rows allow it).
+//               Apart from the warps that use them, or a stage takes the sum
+//               of both latencies (1650 cycles).
 // Two accumulators, so a tile's epilogue overlaps the next tile's products.
 // Every wait is bounded; an expired one sets COLI_STATUS_TIMEOUT and the rest
 // of the launch drains.
@@ -37,17 +49,21 @@ namespace colimoe {
 constexpr int GM = 128;                  // weight rows of a tile
 constexpr int GK = 512;                  // K of a stage
 constexpr uint32_t GABYTES = GM * GK / 2;  // 32 KB of weight codes per stage
-constexpr int GSR = 4;                   // ring of scale bytes in shared memory (two stages ahead + two)
-constexpr int GTHREADS = 416;
-constexpr int GW_EPI = 4, GW_MMA = 8, GW_TMA = 9;
+constexpr int GIR = 4;                   // ring of items
+constexpr int GTHREADS = 576;
+constexpr int GW_EPI = 4, GW_MMA = 8, GW_TMA = 9, GW_SCHED = 13, GW_COPY = 14;
+constexpr int GROLES = 17;               // warps that read an item
 constexpr int GEC = 8;                   // columns exchanged at a time between gate and up lanes
 constexpr int GMAXENT = MAX_E + MAX_SHARED;
+constexpr uint32_t GSCOLS = 32;          // TMEM columns of one stage's scales: 4 x K / 128 x 4 for each operand
 constexpr uint32_t GTMEM = 512;
 constexpr int G_MAX_SMEM = 227 * 1024;   // dynamic shared memory of a CTA
 
 struct Mx4Maps {
-  CUtensorMap w, w_sh;   // 128 bytes x 128 rows (gate/up: 64) of weight codes (routed or grouped, shared)
-  CUtensorMap x[4];      // 128 bytes x 16, 32, 64, 128 rows of activation codes, up to the tile's
+  // 128 bytes x 128 rows (gate/up: 64) of weight codes; [1]: of the shared experts
+  CUtensorMap w[2], wd[2];
+  // 128 bytes x 16, 32, 64, 128 rows of activation codes, up to the tile's: x, and h for the down items
+  CUtensorMap x[4], h[4];
 };
 
 // tile capacity on the N side and what follows from it
@@ -55,21 +71,33 @@ struct Mx4Tile {
   int n;          // activation rows per tile: 16, 32, 64 or 128
   int stages;
 };
+
+// one item, as the schedule warp leaves it for the others
+struct __align__(16) Mx4Item {
+  int row0, ntok;     // activation rows
+  int r0, rows;       // first result row of the tile, result rows of the matrix
+  int K, nst;         // reduction length, stages (0: no more items)
+  int wrow;           // weight row (of pitch K) of result row r0; gate/up: up rows `rows` later
+  int shared, down;
+  int entry, ready;   // down: entry whose h must be complete, gate/up items that complete it
+  int pad;
+};
+
 __host__ __device__ inline uint32_t g_stage(int n) { return GABYTES + (uint32_t)n * (GK / 2); }
-__host__ __device__ inline uint32_t g_scale_slot(int n) { return (uint32_t)(GM + (n <= 32 ? 32 : GM)) * (GK / MXB); }
-constexpr uint32_t GSCOLS = 32;  // TMEM columns of one stage's scales: 4 x K / 128 x 4 for each operand
+// scale bytes of a stage: 16 per row, the activation rows up to a multiple of 32
+__host__ __device__ inline uint32_t g_scale_slot(int n) { return (uint32_t)(GM + (n <= 32 ? 32 : n)) * (GK / MXB); }
 struct Mx4Smem {
-  uint32_t scales, pre, row0, ent, ex, bars, total;
+  uint32_t scales, ex, bars, items, tiles, row0, total;
 };
 __host__ __device__ inline Mx4Smem g_smem(const Mx4Tile& t) {
   Mx4Smem s;
   uint32_t at = g_stage(t.n) * (uint32_t)t.stages;
-  s.scales = at;  at += g_scale_slot(t.n) * GSR;
+  s.scales = at;  at += g_scale_slot(t.n) * (uint32_t)t.stages;
   s.ex = at;      at += GM * (GEC + 1) * 4;
-  s.bars = at;    at += 256;
-  s.pre = at;     at += (GMAXENT + 1) * 4;
+  s.bars = at;    at += 320;
+  s.items = at;   at += GIR * sizeof(Mx4Item);
+  s.tiles = at;   at += (GMAXENT + 1) * 4;
   s.row0 = at;    at += (GMAXENT + 1) * 4;
-  s.ent = at;     at += GMAXENT * 2;
   s.total = at + 1024;  // alignment slack
   return s;
 }
@@ -94,11 +122,12 @@ __device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t* r) {
 
 // 16 scale bytes of a row from byte `at` on, of which the first `valid` exist
 // (the rest become 0, the scale of codes that are 0), to shared memory.
-// unit: the alignment that the rows' pitch allows for the copies.
-__device__ __forceinline__ void copy_scales(uint8_t* dst, const uint8_t* row, int at, int valid, int unit) {
-  if (unit == 16) {
+// The copies are as wide as the row's address allows.
+__device__ __forceinline__ void copy_scales(uint8_t* dst, const uint8_t* row, int at, int valid) {
+  const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(row + at) & 15u;
+  if (low == 0 && (valid >= 16 || valid <= 0)) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(valid > 0 ? row + at : row), "r"(valid > 0 ? 16 : 0) : "memory");
-  } else if (unit == 4) {
+  } else if ((low & 3u) == 0 && (valid & 3) == 0) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst + i)), "l"(valid > i ? row + at + i : row), "r"(valid > i ? 4 : 0) : "memory");
@@ -120,31 +149,69 @@ __device__ __forceinline__ void store_cols(T* y, long long ldy, const uint32_t* 
     if (i < n) y[i * ldy] = from_f32<T>(__uint_as_float(v[i]));
 }
 
-template <int MODE>
+// Waits until the entry's gate/up items are complete (bounded, as pf_wait).
+__device__ __forceinline__ void wait_ready(const uint32_t* ready, int target, uint32_t* status, volatile int* abort) {
+  for (uint32_t i = 0; i < SPIN_LIMIT; ++i) {
+    if (ld_acquire_u32(ready) >= (uint32_t)target) return;
+    if (*abort) return;
+    if (i > 64) __nanosleep(64);
+  }
+  *abort = 1;
+  atomicOr(status, COLI_STATUS_TIMEOUT);
+}
+
+// An arrival of this thread at `bar` once all its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Named barrier of `threads` threads that also ANDs a predicate over them.
+__device__ __forceinline__ bool named_bar_and(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"((uint32_t)v), "r"(id), "r"(threads) : "memory");
+  return r != 0;
+}
+
+// LAYER: both passes of the expert layer; otherwise a grouped product
+template <bool LAYER>
 __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ Mx4Maps maps, const Mx4Gemm A, const Mx4Tile T) {
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<size_t>(sm_raw), 1024));
   const Mx4Smem S = g_smem(T);
   const uint32_t STAGE = g_stage(T.n);
   const int NST = T.stages;
-  int* s_pre = reinterpret_cast<int*>(sm + S.pre);        // [entries + 1] first item of an entry
+  int* s_tiles = reinterpret_cast<int*>(sm + S.tiles);    // [entries + 1] tiles of activation rows before an entry
   int* s_row0 = reinterpret_cast<int*>(sm + S.row0);      // [entries + 1] first activation row
-  uint16_t* s_ent = reinterpret_cast<uint16_t*>(sm + S.ent);
+  Mx4Item* s_items = reinterpret_cast<Mx4Item*>(sm + S.items);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + S.bars);  // [NST] codes landed, scales in TMEM
   uint64_t* empty = full + 8;                                 // [NST] the stage's products are done
-  uint64_t* acc_full = empty + 8;                             // [2]
+  uint64_t* sc_full = empty + 8;                              // [NST] scale bytes landed
+  uint64_t* item_full = sc_full + 8;                          // [GIR]
+  uint64_t* item_empty = item_full + GIR;                     // [GIR]
+  uint64_t* acc_full = item_empty + GIR;                      // [2]
   uint64_t* acc_empty = acc_full + 2;                         // [2]
   uint64_t* fin = acc_empty + 2;
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_taddr + 1);
   uint32_t* status = reinterpret_cast<uint32_t*>(A.ws);
+  uint32_t* ready = reinterpret_cast<uint32_t*>(A.ws + A.L.ready);
+  uint32_t* claim = reinterpret_cast<uint32_t*>(A.ws + A.L.claim);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int RT = MODE == MX4_GATE_UP ? GM / 2 : GM;   // result rows of a tile
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 4 + 4);
       mbar_init(&empty[i], 1);
+      mbar_init(&sc_full[i], 128);
+    }
+    for (int i = 0; i < GIR; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], GROLES);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -160,20 +227,38 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
   }
   pdl_wait();
   pdl_trigger();
-  // items: (entry, row tile, tile of activation rows), the last fastest, so
-  // that neighbouring items share weight rows, which L2 then serves once
-  const int n_ent = mx4_entries<MODE>(A);
-  const int n_uniq = MODE == MX4_PRODUCT ? n_ent : __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.hdr) + MH_NUNIQ);
+  int first = blockIdx.x;
+  if (LAYER && warp == GW_SCHED && lane == 0) first = (int)atomicAdd(claim, 1u);  // under way while the tables load
+  const int n_ent = LAYER ? __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.hdr) + MH_NENT) : A.G;
+  const int n_uniq = LAYER ? __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.hdr) + MH_NUNIQ) : n_ent;
   for (int u = tid; u <= n_ent; u += GTHREADS) {
-    if (MODE == MX4_PRODUCT) {
-      s_row0[u] = A.offsets ? min(max(__ldcg(A.offsets + u), 0), A.P) : u * A.P;
-    } else {
-      s_row0[u] = __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_offset) + u);
-      if (u < n_ent) s_ent[u] = (uint16_t)__ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_expert) + u);
-    }
+    if (LAYER) s_row0[u] = __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_offset) + u);
+    else s_row0[u] = A.offsets ? min(max(__ldcg(A.offsets + u), 0), A.P) : u * A.P;
   }
+  tmem_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  tmem_fence_after();
+  const uint32_t taddr = *s_taddr;
+  const uint32_t acc_cols = T.n < 32 ? 32 : T.n;
+  const uint32_t sc_col0 = 2 * acc_cols;
+
+  // The roles' view of the ring of items.  Warps that meet at named barriers
+  // agree on its answer first, so that after an expired wait none of them
+  // waits at a barrier for one that has given up.
+  uint32_t n_item = 0;
+  auto next_item = [&](Mx4Item& it) {  // waits for item n_item and reads it; false: no more
+    if (!pf_wait(&item_full[n_item % GIR], (n_item / GIR) & 1u, status, s_abort)) return false;
+    it = s_items[n_item % GIR];
+    return it.nst > 0;
+  };
+  auto done_item = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[n_item % GIR]);
+    ++n_item;
+  };
+
+  if (warp == GW_SCHED) {
+    // -------------------------------------------------------------- schedule
     int run = 0, top = 0;
     for (int base = 0; base <= n_ent; base += 32) {
       const int u = base + lane;
@@ -187,12 +272,8 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       }
       top = __shfl_sync(0xffffffffu, a, 31);
       const int next = u + 1 <= n_ent ? max(s_row0[u + 1], a) : a;
-      int items = 0;
-      if (u < n_ent) {
-        const int rows = MODE == MX4_PRODUCT ? A.N : MODE == MX4_DOWN ? A.cfg.hidden : u >= n_uniq ? A.cfg.shared_inter : A.cfg.inter;
-        items = ((rows + RT - 1) / RT) * ((next - a + T.n - 1) / T.n);
-      }
-      int inc = items;
+      const int tiles = (next - a + T.n - 1) / T.n;
+      int inc = tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -200,128 +281,90 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       }
       __syncwarp();
       if (u <= n_ent) {
-        s_pre[u] = run + inc - items;
+        s_tiles[u] = run + inc - tiles;
         s_row0[u] = a;
       }
       run += __shfl_sync(0xffffffffu, inc, 31);
       __syncwarp();
     }
-  }
-  tmem_fence_before();
-  __syncthreads();
-  tmem_fence_after();
-  const uint32_t taddr = *s_taddr;
-  const uint32_t acc_cols = T.n < 32 ? 32 : T.n;
-  const uint32_t sc_col0 = 2 * acc_cols;
-  const int n_items = s_pre[n_ent];
-
-  struct Item {
-    int row0, ntok;     // activation rows
-    int r0, rows;       // first result row of the tile, result rows of the matrix
-    int K, nst, shared;
-    long long wrow;     // weight row (of pitch K) of result row r0; gate/up: up rows `rows` later
-  };
-  auto item_at = [&](int item) {
-    int lo = 0, hi = n_ent - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_pre[mid] <= item) lo = mid; else hi = mid - 1;
-    }
-    Item it;
-    const int cnt = s_row0[lo + 1] - s_row0[lo];
-    const int ntn = (cnt + T.n - 1) / T.n;
-    const int local = item - s_pre[lo], m = local / ntn, nt = local - m * ntn;
-    it.row0 = s_row0[lo] + nt * T.n;
-    it.ntok = min(T.n, cnt - nt * T.n);
-    it.r0 = m * RT;
-    Mx4Entry e;
-    if (MODE == MX4_PRODUCT) {
-      it.shared = 0;
-      it.K = A.K;
-      it.rows = A.N;
-      e.rec = lo;
-    } else {
-      it.shared = lo >= n_uniq;
-      const int inter = it.shared ? A.cfg.shared_inter : A.cfg.inter;
-      it.K = MODE == MX4_GATE_UP ? A.cfg.hidden : inter;
-      it.rows = MODE == MX4_GATE_UP ? inter : A.cfg.hidden;
-      e.rec = it.shared ? s_ent[lo] - A.cfg.n_experts : ep_local(A.cfg, s_ent[lo]);
-    }
-    e.rows = it.rows;
-    it.wrow = mx4_weight_row<MODE>(e) + it.r0;
-    it.nst = (it.K + GK - 1) / GK;
-    return it;
-  };
-
-  if (warp < GW_EPI) {
-    // ---------------------------------------------------------------- scales
-    const int unit = A.K % 512 == 0 && A.cfg.hidden % 512 == 0 && A.cfg.inter % 512 == 0 && A.cfg.shared_inter % 512 == 0 ? 16
-                     : A.K % 128 == 0 ? 4 : 1;   // (the layer's sizes are multiples of 128; A.K is 0 there)
-    const uint32_t slot = g_scale_slot(T.n);
-    const bool wide = T.n > 32;
-    // copies run ahead of their use, over item boundaries
-    int p_item = blockIdx.x, p_st = 0;
-    uint32_t pc = 0;
-    Item pit;
-    if (p_item < n_items) pit = item_at(p_item);
-    auto fetch = [&]() {
-      if (p_item < n_items) {
-        uint8_t* dst = sm + S.scales + (pc % GSR) * slot;
-        const int at = p_st * (GK / MXB);
-        {
-          const int pitch = pit.K / MXB;
-          const uint8_t* base = pit.shared ? A.shs : A.wsc;
-          // gate/up: threads 64..127 hold the up rows of threads 0..63
-          const int r = MODE == MX4_GATE_UP ? tid & 63 : tid;
-          const bool live = pit.r0 + r < pit.rows;
-          const long long row = pit.wrow + r + (MODE == MX4_GATE_UP && tid >= 64 ? pit.rows : 0);
-          copy_scales(dst + tid * 16, live ? base + row * pitch : base, at, live ? pitch - at : 0, unit);
+    if (lane == 0) {
+      const coli_moe_cfg& c = A.cfg;
+      const int all = s_tiles[n_ent], routed = s_tiles[n_uniq];
+      const int mt = LAYER ? c.inter / 64 : (A.N + GM - 1) / GM, mts = LAYER ? c.shared_inter / 64 : 0, mtd = LAYER ? c.hidden / GM : 0;
+      const int n_gr = mt * routed, n_gu = n_gr + mts * (all - routed);  // gate/up items (or all items of a product)
+      const int n_items = n_gu + mtd * all;
+      int item = first;
+      for (uint32_t n = 0;; ++n) {
+        Mx4Item it;
+        it.nst = 0;
+        if (item < n_items) {
+          // position among the row tiles x token tiles of its part, then its entry
+          it.down = item >= n_gu;
+          const bool gs = LAYER && !it.down && item >= n_gr;
+          const int m_all = it.down ? mtd : gs ? mts : mt;
+          const int local = it.down ? item - n_gu : gs ? item - n_gr : item;
+          const int q = local / m_all + (gs ? routed : 0);
+          int lo = gs ? n_uniq : 0, hi = n_ent - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_tiles[mid] <= q) lo = mid; else hi = mid - 1;
+          }
+          const int ntn = s_tiles[lo + 1] - s_tiles[lo];
+          const int in = local - (s_tiles[lo] - (gs ? routed : 0)) * m_all, m = in / ntn, nt = in - m * ntn;
+          it.row0 = s_row0[lo] + nt * T.n;
+          it.ntok = min(T.n, s_row0[lo + 1] - it.row0);
+          it.shared = LAYER && lo >= n_uniq;
+          if (LAYER) {
+            const int inter = it.shared ? c.shared_inter : c.inter;
+            const int rec = it.shared ? lo - n_uniq : ep_local(c, __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_expert) + lo));
+            it.r0 = m * (it.down ? GM : 64);
+            it.rows = it.down ? c.hidden : inter;
+            it.K = it.down ? inter : c.hidden;
+            // a record is gate, up, down: 3 * inter rows of pitch hidden, or 3 * hidden
+            // rows of pitch inter of which the last third are the down rows
+            it.wrow = rec * 3 * it.rows + (it.down ? 2 * it.rows : 0) + it.r0;
+            it.ready = inter / 64 * ntn;
+          } else {
+            it.r0 = m * GM;
+            it.rows = A.N;
+            it.K = A.K;
+            it.wrow = lo * A.N + it.r0;
+            it.ready = 0;
+          }
+          it.entry = lo;
+          it.nst = (it.K + GK - 1) / GK;
         }
-        if (tid < (wide ? GM : 32)) {
-          const int pitch = A.xpitch / MXB, len = pit.K / MXB;
-          const bool live = tid < pit.ntok;
-          copy_scales(dst + (GM + tid) * 16, live ? A.xs + (long long)(pit.row0 + tid) * pitch : A.xs, at, live ? len - at : 0, unit);
-        }
-        if (++p_st == pit.nst) {
-          p_st = 0;
-          p_item += gridDim.x;
-          if (p_item < n_items) pit = item_at(p_item);
-        }
+        if (!pf_wait(&item_empty[n % GIR], ((n / GIR) & 1u) ^ 1u, status, s_abort)) break;
+        s_items[n % GIR] = it;
+        mbar_arrive(&item_full[n % GIR]);  // (release)
+        if (it.nst == 0) break;
+        item = LAYER ? (int)atomicAdd(claim, 1u) : item + (int)gridDim.x;
       }
-      ++pc;
-      cp_async_commit();
-    };
-    fetch();
-    fetch();
-    uint32_t gs = 0;
+    }
+  } else if (warp < GW_EPI) {
+    // ------------------------------------------------- scales into tensor memory
+    const uint32_t slot = g_scale_slot(T.n);
+    const int groups = T.n <= 32 ? 1 : T.n / 32;  // 32-row groups of the activations
     const uint32_t lane0 = taddr + ((uint32_t)(32 * warp) << 16) + sc_col0;
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-      const int nst = item_at(item).nst;
-      for (int st = 0; st < nst; ++st, ++gs) {
-        fetch();
-        cp_async_wait<2>();
-        named_bar(1, 128);  // the stage's bytes are there, and every thread is past the slot before it
-        const uint4* src = reinterpret_cast<const uint4*>(sm + S.scales + (gs % GSR) * slot);
+    uint32_t gs = 0;
+    Mx4Item it;
+    while (next_item(it)) {
+      for (int st = 0; st < it.nst; ++st, ++gs) {
+        const uint32_t s = gs % NST;
+        pf_wait_poll(&sc_full[s], (gs / NST) & 1u, status, s_abort);
+        const uint4* src = reinterpret_cast<const uint4*>(sm + S.scales + s * slot);
         uint32_t a[16], b[16];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // rows 32 c + lane: word j is K / 128 of the stage
           const uint4 v = src[32 * c + lane];
           a[c] = v.x; a[4 + c] = v.y; a[8 + c] = v.z; a[12 + c] = v.w;
         }
-        if (wide) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 v = src[GM + 32 * c + lane];
-            b[c] = v.x; b[4 + c] = v.y; b[8 + c] = v.z; b[12 + c] = v.w;
-          }
-        } else {
-          const uint4 v = src[GM + lane];  // at most 32 rows: one column of each four
-#pragma unroll
-          for (int c = 0; c < 16; ++c) b[c] = 0;
-          b[0] = v.x; b[4] = v.y; b[8] = v.z; b[12] = v.w;
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = c < groups ? src[GM + 32 * c + lane] : make_uint4(0, 0, 0, 0);
+          b[c] = v.x; b[4 + c] = v.y; b[8 + c] = v.z; b[12 + c] = v.w;
         }
-        const uint32_t s = gs % NST;
-        pf_wait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort);
+        // the copies waited for the stage, so its columns are free as well
         tmem_fence_after();
         __syncwarp();
         tmem_st16(lane0 + s * GSCOLS, a);
@@ -331,20 +374,55 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
       }
+      done_item();
+    }
+  } else if (warp >= GW_COPY) {
+    // ------------------------------------------------------- copies of scale bytes
+    const int t = tid - 32 * GW_COPY;
+    const uint32_t slot = g_scale_slot(T.n);
+    const bool has_row = t < (T.n <= 32 ? 32 : T.n);
+    uint32_t gs = 0;
+    Mx4Item it;
+    while (next_item(it)) {
+      const bool gate_up = LAYER && !it.down;
+      if (LAYER && it.down) wait_ready(ready + it.entry, it.ready, status, s_abort);
+      const int pitch = it.K / MXB, xpitch = (LAYER && it.down ? A.L.imax : A.xpitch) / MXB;
+      // gate/up: threads 64..127 hold the up rows of threads 0..63
+      const int r = gate_up ? t & 63 : t;
+      const bool wlive = it.r0 + r < it.rows, xlive = t < it.ntok;
+      const uint8_t* wp = it.shared ? A.shs : A.wsc;
+      if (wlive) wp += ((long long)it.wrow + r + (gate_up && t >= 64 ? it.rows : 0)) * pitch;
+      const uint8_t* xp = LAYER && it.down ? A.ws + A.L.hs : A.xs;
+      if (xlive) xp += (long long)(it.row0 + t) * xpitch;
+      for (int st = 0; st < it.nst; ++st, ++gs) {
+        const uint32_t s = gs % NST;
+        pf_wait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort);
+        uint8_t* dst = sm + S.scales + s * slot;
+        const int at = st * (GK / MXB);
+        copy_scales(dst + t * 16, wp, at, wlive ? pitch - at : 0);
+        if (has_row) copy_scales(dst + (GM + t) * 16, xp, at, xlive ? pitch - at : 0);
+        cp_async_arrive(&sc_full[s]);
+      }
+      done_item();
     }
     cp_async_wait<0>();
   } else if (warp >= GW_TMA) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ TMA producers
-      const int h = (warp - GW_TMA) & 1;         // 128-byte half of the stage
-      const bool weights = warp - GW_TMA < 2;
-      const uint64_t stream = policy_evict_first();
-      uint32_t gs = 0;
-      bool go = true;
-      for (int item = blockIdx.x; item < n_items && go; item += gridDim.x) {
-        const Item it = item_at(item);
-        const CUtensorMap* wm = it.shared ? &maps.w_sh : &maps.w;
-        const int w0 = (int)it.wrow, n16 = (it.ntok + 15) / 16;
+    // ------------------------------------------------------------ TMA producers
+    const int h = (warp - GW_TMA) & 1;         // 128-byte half of the stage
+    const bool weights = warp - GW_TMA < 2;
+    const uint64_t stream = policy_evict_first();
+    uint32_t gs = 0;
+    bool go = true;
+    Mx4Item it;
+    while (next_item(it)) {
+      if (lane == 0 && go) {
+        const bool down = LAYER && it.down;
+        const CUtensorMap* wm = down ? &maps.wd[it.shared] : &maps.w[it.shared];
+        const int n16 = (it.ntok + 15) / 16;
+        if (down && !weights) {  // h was written by ordinary stores
+          wait_ready(ready + it.entry, it.ready, status, s_abort);
+          fence_proxy_async_global();
+        }
         for (int st = 0; st < it.nst; ++st, ++gs) {
           const uint32_t s = gs % NST;
           if (!pf_wait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
@@ -357,42 +435,45 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
           if (weights) {
             dst += h * (GABYTES / 2);
             mbar_arrive_expect_tx(&full[s], GABYTES / 2);
-            if (MODE == MX4_GATE_UP) {
-              tma_load_2d_hint(dst, wm, x, w0, &full[s], stream);
-              tma_load_2d_hint(dst + GABYTES / 4, wm, x, w0 + it.rows, &full[s], stream);
-            } else if (MODE == MX4_DOWN) {
-              tma_load_2d_hint(dst, wm, x, w0, &full[s], stream);
+            if (!LAYER) {
+              tma_load_2d(dst, wm, x, it.wrow, &full[s]);
+            } else if (down) {
+              tma_load_2d_hint(dst, wm, x, it.wrow, &full[s], stream);
             } else {
-              tma_load_2d(dst, wm, x, w0, &full[s]);
+              tma_load_2d_hint(dst, wm, x, it.wrow, &full[s], stream);
+              tma_load_2d_hint(dst + GABYTES / 4, wm, x, it.wrow + it.rows, &full[s], stream);
             }
           } else {
+            const CUtensorMap* xm = down ? maps.h : maps.x;
             dst += GABYTES + h * T.n * 128;
             mbar_arrive_expect_tx(&full[s], (uint32_t)n16 * 2048);
             int row = 0;
 #pragma unroll
             for (int i = 3; i >= 0; --i)  // the rows in boxes of 128, 64, 32, 16
               if (n16 >> i & 1) {
-                tma_load_2d(dst + row * 128, &maps.x[i], x, it.row0 + row, &full[s]);
+                tma_load_2d(dst + row * 128, xm + i, x, it.row0 + row, &full[s]);
                 row += 16 << i;
               }
           }
         }
       }
-      // every copy issued has landed before the CTA can exit; a stage's phase
-      // also needs the other warps, so after an abort this wait is bounded
+      done_item();
+    }
+    // every copy issued has landed before the CTA can exit; a stage's phase
+    // also needs the other warps, so after an abort this wait is bounded
+    if (lane == 0)
       for (uint32_t k = gs > (uint32_t)NST ? gs - NST : 0; k < gs; ++k)
         for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full[k % NST], (k / NST) & 1u); ++i) {
         }
-    }
   } else if (warp == GW_MMA) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      uint32_t gs = 0, n = 0;
-      for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++n) {
-        const Item it = item_at(item);
+    // ------------------------------------------------------------ MMA issuer
+    uint32_t gs = 0;
+    Mx4Item it;
+    while (next_item(it)) {
+      if (lane == 0) {
         const uint32_t idesc = mx4_idesc((it.ntok + 15) & ~15);
-        const uint32_t buf = n & 1u, d = taddr + buf * acc_cols;
-        bool ok = pf_wait_poll(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, status, s_abort);
+        const uint32_t buf = n_item & 1u, d = taddr + buf * acc_cols;
+        bool ok = pf_wait_poll(&acc_empty[buf], ((n_item >> 1) & 1u) ^ 1u, status, s_abort);
         for (int st = 0; st < it.nst; ++st, ++gs) {
           const uint32_t s = gs % NST;
           ok = ok && pf_wait_poll(&full[s], (gs / NST) & 1u, status, s_abort);
@@ -419,7 +500,10 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
         }
         umma_commit(&acc_full[buf]);
       }
-      // every MMA issued has completed before the accumulators are freed
+      done_item();
+    }
+    // every MMA issued has completed before the accumulators are freed
+    if (lane == 0) {
       umma_commit(fin);
       for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(fin, 0u); ++i) {
       }
@@ -428,14 +512,13 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     // ------------------------------------------------------------------ epilogue
     const int q = warp - GW_EPI, r = q * 32 + lane;
     const uint32_t lane0 = taddr + ((uint32_t)(32 * q) << 16);
-    uint32_t n = 0;
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++n) {
-      const Item it = item_at(item);
-      const uint32_t buf = n & 1u, d = lane0 + buf * acc_cols;
-      pf_wait(&acc_full[buf], (n >> 1) & 1u, status, s_abort);
+    Mx4Item it;
+    while (named_bar_and(2, 128, next_item(it))) {
+      const uint32_t buf = n_item & 1u, d = lane0 + buf * acc_cols;
+      pf_wait(&acc_full[buf], (n_item >> 1) & 1u, status, s_abort);
       tmem_fence_after();
       __syncwarp();
-      if (MODE == MX4_GATE_UP) {
+      if (LAYER && !it.down) {
         // lanes 0-63 hold gate rows, 64-127 up rows: through shared memory, GEC
         // columns at a time; then warps 0, 1 take the first half of the columns
         // and warps 2, 3 the second, each warp one MX4 block of 32 h rows
@@ -450,25 +533,32 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
 #pragma unroll
           for (int i = 0; i < GEC; ++i) ex[r * (GEC + 1) + i] = __uint_as_float(v[i]);
           named_bar(2, 128);
+          // every value before the first store, or the columns run one after
+          // the other (byte stores may alias anything)
+          uint32_t code[GEC / 2], byte[GEC / 2];
 #pragma unroll
           for (int i = 0; i < GEC / 2; ++i) {
             const float g = ex[hr * (GEC + 1) + c0 + i], u = ex[(64 + hr) * (GEC + 1) + c0 + i];
-            const float h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
+            const float h = __fdividef(g, 1.0f + expf(-g)) * u;
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
-            const uint32_t b = mx4_scale_byte(m);
-            const float hv = b == 255u ? 0.f : h * mx4_inv(b);
-            const float up = __shfl_down_sync(0xffffffffu, hv, 1);
-            if (c + c0 + i < it.ntok) {
-              const long long at = (long long)(it.row0 + c + c0 + i) * A.L.imax + it.r0 + blk * 32;
-              if ((lane & 1) == 0) hq[at / 2 + lane / 2] = (uint8_t)mx4_pack2(hv, up);
-              if (lane == 0) {
-                hs[at / MXB] = (uint8_t)b;
-                if (b == 255u) atomicOr(status, COLI_STATUS_NONFINITE);
-              }
+            byte[i] = mx4_scale_byte(m);
+            const float hv = byte[i] == 255u ? 0.f : h * mx4_inv(byte[i]);
+            code[i] = mx4_pack2(hv, __shfl_down_sync(0xffffffffu, hv, 1));
+          }
+          const long long at = (long long)(it.row0 + c + c0) * A.L.imax + it.r0 + blk * 32;
+#pragma unroll
+          for (int i = 0; i < GEC / 2; ++i) {
+            if (c + c0 + i >= it.ntok) break;
+            if ((lane & 1) == 0) hq[(at + (long long)i * A.L.imax) / 2 + lane / 2] = (uint8_t)code[i];
+            if (lane == 0) {
+              hs[(at + (long long)i * A.L.imax) / MXB] = (uint8_t)byte[i];
+              if (byte[i] == 255u) atomicOr(status, COLI_STATUS_NONFINITE);
             }
           }
+          if (c + GEC >= it.ntok) fence_proxy_async_global();  // the down items read h through TMA
           named_bar(2, 128);
         }
+        if (q == 0 && lane == 0) red_release_add(ready + it.entry, 1u);
       } else {
         const bool live = it.r0 + r < it.rows;
         for (int c = 0; c < it.ntok; c += 16) {
@@ -477,7 +567,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
           tmem_wait_ld();
           const int nc = live ? it.ntok - c : 0;
           const long long at = (long long)(it.row0 + c) * A.ldy + it.r0 + r;
-          if (A.y_type == COLI_F32) store_cols(static_cast<float*>(A.y) + at, A.ldy, v, nc);
+          if (LAYER || A.y_type == COLI_F32) store_cols(static_cast<float*>(A.y) + at, A.ldy, v, nc);
           else if (A.y_type == COLI_BF16) store_cols(static_cast<__nv_bfloat16*>(A.y) + at, A.ldy, v, nc);
           else store_cols(static_cast<__half*>(A.y) + at, A.ldy, v, nc);
         }
@@ -485,6 +575,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      done_item();
     }
   }
   tmem_fence_before();
@@ -500,47 +591,53 @@ bool encode_bytes(CUtensorMap* m, const void* base, size_t row_bytes, size_t row
   return encode_rows_sw(m, base, row_bytes, rows, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int MODE>
-cudaError_t launch_mode(const Mx4Gemm& A, cudaStream_t st) {
-  const int sms = device_sms();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  // most rows an entry can hold
-  const int most = MODE == MX4_PRODUCT ? A.P : A.L.T;
+Mx4Tile tile_for(int most) {
   Mx4Tile T;
-  const int n_env = getenv("MXN") ? atoi(getenv("MXN")) : 0;
   T.n = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
+  const int n_env = getenv("MXN") ? atoi(getenv("MXN")) : 0;
   if (n_env && n_env < T.n) T.n = n_env;
   T.stages = T.n == 128 ? 3 : T.n == 64 ? 4 : 5;
+  return T;
+}
+
+template <bool LAYER>
+cudaError_t launch(const Mx4Maps& maps, const Mx4Gemm& A, const Mx4Tile& T, cudaStream_t st) {
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   const Mx4Smem S = g_smem(T);
   if (S.total > (uint32_t)G_MAX_SMEM) return cudaErrorInvalidConfiguration;
-  Mx4Maps maps{};
-  const coli_moe_cfg& c = A.cfg;
-  const size_t pitch = MODE == MX4_PRODUCT ? A.K : MODE == MX4_GATE_UP ? c.hidden : c.inter;
-  const size_t rows = MODE == MX4_PRODUCT ? (size_t)A.G * A.N : (size_t)ep_records(c) * 3 * (MODE == MX4_GATE_UP ? c.inter : c.hidden);
-  const uint32_t box = MODE == MX4_GATE_UP ? 64 : 128;
-  bool ok = encode_bytes(&maps.w, A.wc, pitch / 2, rows, box);
-  for (int i = 0; ok && 16 << i <= T.n; ++i) ok = encode_bytes(&maps.x[i], A.xc, A.xpitch / 2, A.P, 16u << i);
-  maps.w_sh = maps.w;
-  if (ok && MODE != MX4_PRODUCT && c.n_shared > 0)
-    ok = encode_bytes(&maps.w_sh, A.shc, (MODE == MX4_GATE_UP ? c.hidden : c.shared_inter) / 2,
-                      (size_t)c.n_shared * 3 * (MODE == MX4_GATE_UP ? c.shared_inter : c.hidden), box);
-  if (!ok) return cudaErrorInvalidValue;
   // the kernel's shared-memory limit is raised once per device, to the most any tile needs
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(raised.load(std::memory_order_acquire) >> dev & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(mx4_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, G_MAX_SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(mx4_gemm<LAYER>, cudaFuncAttributeMaxDynamicSharedMemorySize, G_MAX_SMEM);
     if (e != cudaSuccess) return e;
     raised.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_pdl(mx4_gemm<MODE>, (unsigned)sms, GTHREADS, S.total, st, maps, A, T);
+  return launch_pdl(mx4_gemm<LAYER>, (unsigned)sms, GTHREADS, S.total, st, maps, A, T);
 }
 
 }  // namespace
 
-cudaError_t launch_mx4_gemm(const Mx4Gemm& A, Mx4Mode mode, cudaStream_t st) {
-  return mode == MX4_PRODUCT ? launch_mode<MX4_PRODUCT>(A, st) : mode == MX4_GATE_UP ? launch_mode<MX4_GATE_UP>(A, st) : launch_mode<MX4_DOWN>(A, st);
+cudaError_t launch_mx4_product(const Mx4Gemm& A, cudaStream_t st) {
+  const Mx4Tile T = tile_for(A.P);
+  Mx4Maps maps{};
+  bool ok = encode_bytes(&maps.w[0], A.wc, A.K / 2, (size_t)A.G * A.N, GM);
+  for (int i = 0; ok && 16 << i <= T.n; ++i) ok = encode_bytes(&maps.x[i], A.xc, A.xpitch / 2, A.P, 16u << i);
+  return ok ? launch<false>(maps, A, T, st) : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_mx4_layer(const Mx4Gemm& A, cudaStream_t st) {
+  const Mx4Tile T = tile_for(A.L.T);  // an expert holds at most every position
+  Mx4Maps maps{};
+  const coli_moe_cfg& c = A.cfg;
+  const size_t H = c.hidden, I = c.inter, Is = c.shared_inter, n = (size_t)ep_records(c) * 3, ns = (size_t)c.n_shared * 3;
+  bool ok = encode_bytes(&maps.w[0], A.wc, H / 2, n * I, 64) && encode_bytes(&maps.wd[0], A.wc, I / 2, n * H, GM);
+  if (ok && ns > 0) ok = encode_bytes(&maps.w[1], A.shc, H / 2, ns * Is, 64) && encode_bytes(&maps.wd[1], A.shc, Is / 2, ns * H, GM);
+  for (int i = 0; ok && 16 << i <= T.n; ++i)
+    ok = encode_bytes(&maps.x[i], A.xc, H / 2, A.P, 16u << i) && encode_bytes(&maps.h[i], A.ws + A.L.hq, A.L.imax / 2, A.P, 16u << i);
+  return ok ? launch<true>(maps, A, T, st) : cudaErrorInvalidValue;
 }
 
 }  // namespace colimoe
