@@ -50,6 +50,7 @@ constexpr int GM = 128;                  // weight rows of a tile
 constexpr int GK = 512;                  // K of a stage
 constexpr uint32_t GABYTES = GM * GK / 2;  // 32 KB of weight codes per stage
 constexpr int GIR = 4;                   // ring of items
+constexpr uint32_t GAHEAD = 3;           // stages left to request when the next item is claimed
 constexpr int GTHREADS = 576;
 constexpr int GW_EPI = 4, GW_MMA = 8, GW_TMA = 9, GW_SCHED = 13, GW_COPY = 14;
 constexpr int GROLES = 17;               // warps that read an item
@@ -154,7 +155,7 @@ __device__ __forceinline__ void wait_ready(const uint32_t* ready, int target, ui
   for (uint32_t i = 0; i < SPIN_LIMIT; ++i) {
     if (ld_acquire_u32(ready) >= (uint32_t)target) return;
     if (*abort) return;
-    if (i > 64) __nanosleep(64);
+    __nanosleep(100);
   }
   *abort = 1;
   atomicOr(status, COLI_STATUS_TIMEOUT);
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
   uint64_t* fin = acc_empty + 2;
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_taddr + 1);
+  volatile uint32_t* s_issued = reinterpret_cast<volatile uint32_t*>(s_taddr + 2);  // stages whose weights are requested
   uint32_t* status = reinterpret_cast<uint32_t*>(A.ws);
   uint32_t* ready = reinterpret_cast<uint32_t*>(A.ws + A.L.ready);
   uint32_t* claim = reinterpret_cast<uint32_t*>(A.ws + A.L.claim);
@@ -219,6 +221,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     }
     mbar_init(fin, 1);
     *s_abort = 0;
+    *s_issued = 0;
     fence_barrier_init();
   }
   if (warp == GW_MMA) {
@@ -294,6 +297,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       const int n_gr = mt * routed, n_gu = n_gr + mts * (all - routed);  // gate/up items (or all items of a product)
       const int n_items = n_gu + mtd * all;
       int item = first;
+      uint32_t stages = 0;  // of the items posted
       for (uint32_t n = 0;; ++n) {
         Mx4Item it;
         it.nst = 0;
@@ -338,7 +342,16 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
         s_items[n % GIR] = it;
         mbar_arrive(&item_full[n % GIR]);  // (release)
         if (it.nst == 0) break;
-        item = LAYER ? (int)atomicAdd(claim, 1u) : item + (int)gridDim.x;
+        stages += (uint32_t)it.nst;
+        if (LAYER) {
+          // the next claim only when the weights of all but GAHEAD posted stages
+          // are requested: a CTA that claimed several items at once would hold
+          // gate/up items back that others' down items wait for
+          for (uint32_t i = 0; i < SPIN_LIMIT && stages > *s_issued + GAHEAD && !*s_abort; ++i) __nanosleep(40);
+          item = (int)atomicAdd(claim, 1u);
+        } else {
+          item += (int)gridDim.x;
+        }
       }
     }
   } else if (warp < GW_EPI) {
@@ -385,7 +398,11 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     Mx4Item it;
     while (next_item(it)) {
       const bool gate_up = LAYER && !it.down;
-      if (LAYER && it.down) wait_ready(ready + it.entry, it.ready, status, s_abort);
+      if (LAYER && it.down) {
+        // one lane looks (thousands of threads on one counter hold its additions up)
+        if (lane == 0) wait_ready(ready + it.entry, it.ready, status, s_abort);
+        __syncwarp();
+      }
       const int pitch = it.K / MXB, xpitch = (LAYER && it.down ? A.L.imax : A.xpitch) / MXB;
       // gate/up: threads 64..127 hold the up rows of threads 0..63
       const int r = gate_up ? t & 63 : t;
@@ -434,6 +451,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
           uint8_t* dst = sm + (size_t)s * STAGE;
           if (weights) {
             dst += h * (GABYTES / 2);
+            if (h == 0) *s_issued = gs + 1;
             mbar_arrive_expect_tx(&full[s], GABYTES / 2);
             if (!LAYER) {
               tma_load_2d(dst, wm, x, it.wrow, &full[s]);
