@@ -50,7 +50,6 @@ __global__ void __launch_bounds__(TT) mx4_tables(const coli_moe_cfg c, const Mx4
   const int tid = threadIdx.x, E = c.n_experts, np = T * c.top_k;
   int32_t* slot = reinterpret_cast<int32_t*>(ws + L.slot);
   int32_t* ent_expert = reinterpret_cast<int32_t*>(ws + L.ent_expert);
-  int32_t* ent_count = reinterpret_cast<int32_t*>(ws + L.ent_count);
   int32_t* ent_offset = reinterpret_cast<int32_t*>(ws + L.ent_offset);
   int32_t* hdr = reinterpret_cast<int32_t*>(ws + L.hdr);
   cnt[tid] = 0;
@@ -75,13 +74,11 @@ __global__ void __launch_bounds__(TT) mx4_tables(const coli_moe_cfg c, const Mx4
   off[tid] = o;
   if (v > 0) {
     ent_expert[ent] = tid;
-    ent_count[ent] = v;
     ent_offset[ent] = o;
   }
   const int ns = c.n_shared;
   if (tid < ns) {
     ent_expert[uniq + tid] = E + tid;
-    ent_count[uniq + tid] = T;
     ent_offset[uniq + tid] = pairs + tid * T;
   }
   if (tid == 0) {
@@ -168,7 +165,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) mx4_prep_small(const coli_moe_cfg c, const Mx4Layout L, const T* __restrict__ x,
                                                       const uint8_t* __restrict__ x_scales, int rows, const int32_t* __restrict__ idx,
                                                       uint8_t* __restrict__ ws) {
-  __shared__ int s_id[PREP_PAIRS], s_row[PREP_PAIRS];
+  __shared__ int4 s_keys[PREP_PAIRS / 4];
+  __shared__ int s_row[PREP_PAIRS], s_expert[PREP_PAIRS + 1], s_leads[8];
   const int tid = threadIdx.x, lane = tid & 31, H = c.hidden, E = c.n_experts, k = c.top_k, ns = c.n_shared, np = rows * k;
   constexpr int NONE = 0x7fffffff;
   pdl_wait();
@@ -180,55 +178,55 @@ __global__ void __launch_bounds__(256) mx4_prep_small(const coli_moe_cfg c, cons
   uint32_t w[1], b[1];
   w[0] = unit_codes(x, x_scales, (long long)t * H + k0, t < rows && k0 < H, &b[0]);
   bool bad = false;
-  int id = NONE;
+  int key = NONE;
   if (tid < np) {
     const int e = idx[tid];
     const bool in = e >= 0 && e < E;
     bad = !in && e != -1;
-    id = in && ep_owned(c, e) ? e : NONE;
+    if (in && ep_owned(c, e)) key = e * PREP_PAIRS + tid;
   }
-  s_id[tid] = id;
+  reinterpret_cast<int*>(s_keys)[tid] = key;
   if (bad && blockIdx.x == 0) atomicOr(reinterpret_cast<uint32_t*>(ws), COLI_STATUS_BADIDX);
-  __syncthreads();
-  // row = pairs of lower experts + earlier pairs of the same one
-  int row = 0, before = 0, same = 0, firsts = 0;
-  for (int q = 0; q < np; ++q) {
-    const int o = s_id[q];
-    row += o < id || (o == id && q < tid);
-    before += o == id && q < tid;
-    same += o == id;
-  }
-  const bool first = id != NONE && before == 0;
-  s_row[tid] = id == NONE ? -1 : row;
-  const int pairs = __syncthreads_count(id != NONE);
+  const int pairs = __syncthreads_count(key != NONE);
+  // a pair's row: the keys below its own
+  int row = 0;
+  if (key != NONE)
+#pragma unroll 4
+    for (int q = 0; q < (np + 3) / 4; ++q) {
+      const int4 o = s_keys[q];
+      row += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
+    }
+  s_row[tid] = key == NONE ? -1 : row;
   if (blockIdx.x == 0) {
-    for (int u = tid; u < L.n_ent_max; u += 256) reinterpret_cast<uint32_t*>(ws + L.ready)[u] = 0u;
-    if (tid == 0) *reinterpret_cast<uint32_t*>(ws + L.claim) = 0u;
-    // entry number: first pairs of lower experts
+    // entries: runs of one expert among the rows
     int32_t* ent_expert = reinterpret_cast<int32_t*>(ws + L.ent_expert);
-    int32_t* ent_count = reinterpret_cast<int32_t*>(ws + L.ent_count);
     int32_t* ent_offset = reinterpret_cast<int32_t*>(ws + L.ent_offset);
     int32_t* hdr = reinterpret_cast<int32_t*>(ws + L.hdr);
-    s_id[tid] = first ? id : NONE;
-    const int uniq = __syncthreads_count(first);
-    for (int q = 0; q < np; ++q) firsts += s_id[q] < id;
-    if (first) {
-      ent_expert[firsts] = id;
-      ent_count[firsts] = same;
-      ent_offset[firsts] = row;
+    for (int u = tid; u < L.n_ent_max; u += 256) reinterpret_cast<uint32_t*>(ws + L.ready)[u] = 0u;
+    if (tid == 0) *reinterpret_cast<uint32_t*>(ws + L.claim) = 0u;
+    if (key != NONE) s_expert[row + 1] = key / PREP_PAIRS;
+    if (tid == 0) s_expert[0] = -1;
+    __syncthreads();
+    const bool lead = tid < pairs && s_expert[tid + 1] != s_expert[tid];
+    const unsigned leads = __ballot_sync(0xffffffffu, lead);
+    if (lane == 0) s_leads[tid >> 5] = __popc(leads);
+    const int uniq = __syncthreads_count(lead);
+    if (lead) {
+      int entry = __popc(leads & ((1u << lane) - 1u));
+      for (int v = 0; v < tid >> 5; ++v) entry += s_leads[v];
+      ent_expert[entry] = s_expert[tid + 1];
+      ent_offset[entry] = tid;
     }
-    if (tid < ns) {
-      ent_expert[uniq + tid] = E + tid;
-      ent_count[uniq + tid] = rows;
-      ent_offset[uniq + tid] = pairs + tid * rows;
-    }
+    if (tid < ns) ent_expert[uniq + tid] = E + tid;
+    if (tid <= ns) ent_offset[uniq + tid] = pairs + tid * rows;
     if (tid == 0) {
-      ent_offset[uniq + ns] = pairs + ns * rows;
       hdr[MH_NENT] = uniq + ns;
       hdr[MH_NUNIQ] = uniq;
       hdr[MH_NPAIRS] = pairs + ns * rows;
     }
     if (tid < np) reinterpret_cast<int32_t*>(ws + L.slot)[tid] = s_row[tid];
+  } else {
+    __syncthreads();
   }
   if (t >= rows) return;  // (whole warps)
   for (int j0 = 0; j0 < k + ns; j0 += 32) {

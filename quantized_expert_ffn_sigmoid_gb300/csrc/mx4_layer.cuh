@@ -7,7 +7,7 @@ namespace colimoe {
 
 struct Mx4Layout {
   int T, P, n_ent_max, imax;
-  size_t hdr, claim, ready, ent_expert, ent_count, ent_offset, slot, xq, xs, hq, hs, o, total;
+  size_t hdr, claim, ready, ent_expert, ent_offset, slot, xq, xs, hq, hs, o, total;
 };
 enum Mx4Hdr { MH_NENT = 0, MH_NUNIQ, MH_NPAIRS, MH_FIELDS = 8 };
 
@@ -25,9 +25,8 @@ inline Mx4Layout make_mx4_layout(const coli_moe_cfg& c, int T) {
   auto take = [&](size_t bytes) { const size_t r = off; off = align_up(off + bytes, 256); return r; };
   L.hdr = take(4 * MH_FIELDS);
   L.claim = take(4);                           // next item of the products
-  L.ready = take(4 * (size_t)L.n_ent_max);     // gate/up items done per entry; both zeroed by the dispatch
+  L.ready = take(4 * (size_t)L.n_ent_max);  // gate/up items done per entry; both zeroed by the dispatch
   L.ent_expert = take(4 * (size_t)L.n_ent_max);
-  L.ent_count = take(4 * (size_t)L.n_ent_max);
   L.ent_offset = take(4 * ((size_t)L.n_ent_max + 1));
   L.slot = take(4 * (size_t)T * k);
   L.xq = take(P * H / 2);
