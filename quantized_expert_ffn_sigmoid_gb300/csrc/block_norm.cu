@@ -63,8 +63,8 @@ __device__ __forceinline__ void load_w(const float* p, int n, float* v) {
 
 // U units of 8 elements per thread; WARP: one row per warp, else per CTA.
 // Every load of the row (x, y and gate) is issued before the first reduction.
-template <typename T, typename TN, int U, bool VEC, bool WARP>
-__global__ void __launch_bounds__(U <= 2 ? 1024 : 512) norm_kernel(const NormParams P) {
+template <typename T, typename TN, int U, int THREADS, int CTAS, bool VEC, bool WARP>
+__global__ void __launch_bounds__(THREADS, CTAS) norm_kernel(const NormParams P) {
   __shared__ float red[2][32];
   const int H = P.H;
   const int nthr = WARP ? 32 : (int)blockDim.x, t = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
@@ -144,33 +144,32 @@ __global__ void __launch_bounds__(U <= 2 ? 1024 : 512) norm_kernel(const NormPar
   }
 }
 
-template <typename T, typename TN, int U>
+template <typename T, typename TN, int U, int THREADS, int CTAS>
 cudaError_t launch_u(const NormParams& P, bool vec, unsigned block, cudaStream_t st) {
   const unsigned grid = (unsigned)P.rows;
-  return vec ? launch_pdl(norm_kernel<T, TN, U, true, false>, grid, block, 0, st, P)
-             : launch_pdl(norm_kernel<T, TN, U, false, false>, grid, block, 0, st, P);
+  return vec ? launch_pdl(norm_kernel<T, TN, U, THREADS, CTAS, true, false>, grid, block, 0, st, P)
+             : launch_pdl(norm_kernel<T, TN, U, THREADS, CTAS, false, false>, grid, block, 0, st, P);
 }
 
-// Threads of a row: one warp up to 512 elements (no barrier); else a CTA with
-// one unit per thread, which is the shortest chain for few rows, or with more
-// rows than SMs 256 threads of up to four units (512 beyond 8192 elements),
-// so that several CTAs share an SM and cover each other's reductions.
+// Threads of a row: one warp up to 512 elements (no barrier).  Beyond, with no
+// more rows than SMs, a CTA with one unit per thread, the shortest chain.
+// With more rows two units per thread and three CTAs of up to 384 threads on
+// an SM, which cover each other's reductions: 4096 x 6144 bf16 with codes and
+// their values take 59 us, against 63 with three units and 256 threads, 66
+// with one unit and 768, 74 with 256 threads and the registers unbounded.
 template <typename T, typename TN>
 cudaError_t launch(const NormParams& P, bool vec, cudaStream_t st) {
   const int units = (P.H + 7) / 8;
-  const int sms = device_sms();
   if (units <= 64) {
     const unsigned grid = (unsigned)(((long long)P.rows + 7) / 8);
-    return vec ? launch_pdl(norm_kernel<T, TN, 2, true, true>, grid, 256, 0, st, P)
-               : launch_pdl(norm_kernel<T, TN, 2, false, true>, grid, 256, 0, st, P);
+    return vec ? launch_pdl(norm_kernel<T, TN, 2, 256, 1, true, true>, grid, 256, 0, st, P)
+               : launch_pdl(norm_kernel<T, TN, 2, 256, 1, false, true>, grid, 256, 0, st, P);
   }
-  const int most = P.rows <= sms ? 1024 : units <= 1024 ? 256 : 512;
-  const int u = (units + most - 1) / most;
-  const unsigned block = (unsigned)(((units + u - 1) / u + 31) / 32 * 32);
-  if (u == 1) return launch_u<T, TN, 1>(P, vec, block, st);
-  if (u == 2) return launch_u<T, TN, 2>(P, vec, block, st);
-  if (u == 3) return launch_u<T, TN, 3>(P, vec, block, st);
-  return launch_u<T, TN, 4>(P, vec, block, st);
+  auto threads = [&](int u) { return (unsigned)(((units + u - 1) / u + 31) / 32 * 32); };
+  if (P.rows <= device_sms())
+    return units <= 1024 ? launch_u<T, TN, 1, 1024, 1>(P, vec, threads(1), st) : launch_u<T, TN, 2, 1024, 1>(P, vec, threads(2), st);
+  if (units <= 768) return launch_u<T, TN, 2, 384, 3>(P, vec, threads(2), st);
+  return launch_u<T, TN, 4, 512, 1>(P, vec, threads(4), st);
 }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }

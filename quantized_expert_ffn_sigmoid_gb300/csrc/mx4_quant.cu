@@ -3,9 +3,12 @@
 // Both are one pass over the data and bound by HBM: 2 (bf16) or 4 (fp32)
 // bytes in and 17/32 bytes out per element, or the reverse.  A lane holds 8
 // consecutive elements (one or two 16-byte loads), so a block of 32 is four
-// neighbouring lanes and its maximum two shuffles; a warp takes 1024
-// consecutive elements of one row, four loads of every lane in flight before
-// the first use.
+// neighbouring lanes and its maximum two shuffles; a warp takes 2048
+// consecutive elements of one row, all loads of every lane in flight before
+// the first use.  8192 x 6144 bf16 there and back take 43.7 us (45.4 with
+// 1024 elements a warp, 50.3 with 512).  Calls too small to give every SM 64
+// such warps take 512 a warp: the shorter chain (one row of 6144 there and
+// back: 2.8 us against 3.7).
 #include "mx4_common.cuh"
 
 namespace {
@@ -13,12 +16,12 @@ namespace {
 using namespace colimoe;
 
 constexpr int QT = 256;      // threads per CTA
-constexpr int QU = 4;        // 8-element units per lane and step
-constexpr int QW = 256 * QU; // elements per warp and step
 
-template <typename T, bool VEC>
+// QU: 8-element units per lane
+template <typename T, bool VEC, int QU>
 __global__ void __launch_bounds__(QT) quantize_kernel(const T* __restrict__ x, long long ldx, int rows, int K,
                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr int QW = 256 * QU;  // elements per warp and step
   const int lane = threadIdx.x & 31;
   const int per_row = (K + QW - 1) / QW;
   const long long tasks = (long long)rows * per_row, step = (long long)gridDim.x * (QT / 32);
@@ -46,9 +49,10 @@ __global__ void __launch_bounds__(QT) quantize_kernel(const T* __restrict__ x, l
   }
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int QU>
 __global__ void __launch_bounds__(QT) dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                         int rows, int K, T* __restrict__ out, long long ldo) {
+  constexpr int QW = 256 * QU;  // elements per warp and step
   const int lane = threadIdx.x & 31;
   const int per_row = (K + QW - 1) / QW;
   const long long tasks = (long long)rows * per_row, step = (long long)gridDim.x * (QT / 32);
@@ -81,30 +85,39 @@ __global__ void __launch_bounds__(QT) dequantize_kernel(const uint8_t* __restric
 }
 
 // A CTA per 8 warp tasks: the hardware deals them out as CTAs end (a grid of
-// resident CTAs that stride over the tasks left a sixth of the last round
-// idle: 27.7 instead of XX us for 8192 x 6144 bf16).
-unsigned grid_for(long long rows, int K) {
-  const long long tasks = rows * ((K + QW - 1) / QW);
+// resident CTAs that stride over the tasks left a sixth of the last round idle)
+unsigned grid_for(long long rows, int K, int units) {
+  const long long tasks = rows * ((K + 256 * units - 1) / (256 * units));
   const long long blocks = (tasks + QT / 32 - 1) / (QT / 32);
   return (unsigned)(blocks < 0x7fffffffLL ? blocks : 0x7fffffffLL);
 }
+constexpr int FEW = 2, MANY = 8;  // units per lane
+bool many(long long rows, int K) { return rows * ((K + 256 * MANY - 1) / (256 * MANY)) >= 64LL * device_sms(); }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+template <typename T, int QU>
+cudaError_t quantize_u(const T* x, long long ldx, int rows, int K, uint8_t* codes, uint8_t* scales, bool vec, cudaStream_t st) {
+  const unsigned grid = grid_for(rows, K, QU);
+  return vec ? launch_pdl(quantize_kernel<T, true, QU>, grid, QT, 0, st, x, ldx, rows, K, codes, scales)
+             : launch_pdl(quantize_kernel<T, false, QU>, grid, QT, 0, st, x, ldx, rows, K, codes, scales);
+}
+template <typename T, int QU>
+cudaError_t dequantize_u(const uint8_t* codes, const uint8_t* scales, int rows, int K, T* out, long long ldo, bool vec, cudaStream_t st) {
+  const unsigned grid = grid_for(rows, K, QU);
+  return vec ? launch_pdl(dequantize_kernel<T, true, QU>, grid, QT, 0, st, codes, scales, rows, K, out, ldo)
+             : launch_pdl(dequantize_kernel<T, false, QU>, grid, QT, 0, st, codes, scales, rows, K, out, ldo);
+}
 template <typename T>
 cudaError_t quantize(const void* x, long long ldx, int rows, int K, uint8_t* codes, uint8_t* scales, bool vec, cudaStream_t st) {
-  const unsigned grid = grid_for(rows, K);
   const T* xt = static_cast<const T*>(x);
-  return vec ? launch_pdl(quantize_kernel<T, true>, grid, QT, 0, st, xt, ldx, rows, K, codes, scales)
-             : launch_pdl(quantize_kernel<T, false>, grid, QT, 0, st, xt, ldx, rows, K, codes, scales);
+  return many(rows, K) ? quantize_u<T, MANY>(xt, ldx, rows, K, codes, scales, vec, st) : quantize_u<T, FEW>(xt, ldx, rows, K, codes, scales, vec, st);
 }
 template <typename T>
 cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int K, void* out, long long ldo, bool vec, cudaStream_t st) {
-  const unsigned grid = grid_for(rows, K);
   T* ot = static_cast<T*>(out);
-  return vec ? launch_pdl(dequantize_kernel<T, true>, grid, QT, 0, st, codes, scales, rows, K, ot, ldo)
-             : launch_pdl(dequantize_kernel<T, false>, grid, QT, 0, st, codes, scales, rows, K, ot, ldo);
+  return many(rows, K) ? dequantize_u<T, MANY>(codes, scales, rows, K, ot, ldo, vec, st) : dequantize_u<T, FEW>(codes, scales, rows, K, ot, ldo, vec, st);
 }
 
 int check(const void* x, int32_t type, int64_t ld, int32_t T, int32_t K, const void* codes, const void* scales) {
