@@ -108,12 +108,31 @@ __host__ __device__ inline Mx4Smem g_smem(const Mx4Tile& t) {
 __device__ __forceinline__ uint32_t mx4_idesc(int n) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(GM >> 7) << 27);
 }
-__device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
+// Issued by the lane whose `leader` is set; executed by a whole converged
+// warp, so that the operands stay in uniform registers.
+__device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc,
+                                         uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\t"
+      "setp.ne.u32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(leader) : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(leader) : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc) : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -485,46 +504,48 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
         }
   } else if (warp == GW_MMA) {
     // ------------------------------------------------------------ MMA issuer
-    uint32_t gs = 0;
+    // The whole warp runs the loop and one elected lane issues: with the loop
+    // in one lane every operand of every instruction went through a register
+    // copy of its own, 95 cycles an instruction.
+    const uint32_t leader = elect_one();
+    const uint32_t bh = (uint32_t)T.n * 8;  // second box of B, in descriptor units of 16 bytes
+    uint32_t s = 0, phase = 0;
     Mx4Item it;
     while (next_item(it)) {
-      if (lane == 0) {
-        const uint32_t idesc = mx4_idesc((it.ntok + 15) & ~15);
-        const uint32_t buf = n_item & 1u, d = taddr + buf * acc_cols;
-        bool ok = pf_wait_poll(&acc_empty[buf], ((n_item >> 1) & 1u) ^ 1u, status, s_abort);
-        for (int st = 0; st < it.nst; ++st, ++gs) {
-          const uint32_t s = gs % NST;
-          ok = ok && pf_wait_poll(&full[s], (gs / NST) & 1u, status, s_abort);
-          if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
-            tmem_fence_after();
-            const uint32_t a0 = smem_u32(sm + (size_t)s * STAGE), b0 = a0 + GABYTES;
-            const uint32_t sa = taddr + sc_col0 + s * GSCOLS, sb = sa + 16;
-            // kept short: this thread's instructions are on the pipeline's critical path
-            const uint64_t da = umma_desc_sw128(a0), db = umma_desc_sw128(b0);
-            const uint32_t bh = (uint32_t)T.n * 8;  // second box of B, in descriptor units of 16 bytes
-            const int steps = min(GK / 64, (it.K - st * GK + 63) / 64);
-            if (steps == GK / 64) {
+      const uint32_t idesc = mx4_idesc((it.ntok + 15) & ~15);
+      const uint32_t buf = n_item & 1u, d = taddr + buf * acc_cols;
+      bool ok = pf_wait_poll(&acc_empty[buf], ((n_item >> 1) & 1u) ^ 1u, status, s_abort);
+      for (int st = 0; st < it.nst; ++st) {
+        ok = ok && pf_wait_poll(&full[s], phase, status, s_abort);
+        if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
+          tmem_fence_after();
+          const uint32_t a0 = smem_u32(sm) + s * STAGE, b0 = a0 + GABYTES;
+          const uint32_t sa = taddr + sc_col0 + s * GSCOLS, sb = sa + 16;
+          const uint64_t da = umma_desc_sw128(a0), db = umma_desc_sw128(b0);
+          const int steps = min(GK / 64, (it.K - st * GK + 63) / 64);
+          if (steps == GK / 64) {
 #pragma unroll
-              for (int k = 0; k < GK / 64; ++k)
-                umma_mx4(d, da + (k >> 2) * (GABYTES / 32) + (k & 3) * 2, db + (k >> 2) * bh + (k & 3) * 2,
-                         idesc | ((k & 1) * ((2u << 4) | (2u << 29))), sa + 4 * (k >> 1), sb + 4 * (k >> 1), k ? 1u : (uint32_t)(st != 0));
-            } else {
-              for (int k = 0; k < steps; ++k)
-                umma_mx4(d, da + (k >> 2) * (GABYTES / 32) + (k & 3) * 2, db + (k >> 2) * bh + (k & 3) * 2,
-                         idesc | ((k & 1) * ((2u << 4) | (2u << 29))), sa + 4 * (k >> 1), sb + 4 * (k >> 1), (st | k) != 0);
-            }
+            for (int k = 0; k < GK / 64; ++k)
+              umma_mx4(d, da + (k >> 2) * (GABYTES / 32) + (k & 3) * 2, db + (k >> 2) * bh + (k & 3) * 2,
+                       idesc | ((k & 1) * ((2u << 4) | (2u << 29))), sa + 4 * (k >> 1), sb + 4 * (k >> 1), k ? 1u : (uint32_t)(st != 0), leader);
+          } else {
+            for (int k = 0; k < steps; ++k)
+              umma_mx4(d, da + (k >> 2) * (GABYTES / 32) + (k & 3) * 2, db + (k >> 2) * bh + (k & 3) * 2,
+                       idesc | ((k & 1) * ((2u << 4) | (2u << 29))), sa + 4 * (k >> 1), sb + 4 * (k >> 1), (st | k) != 0, leader);
           }
-          umma_commit(&empty[s]);
         }
-        umma_commit(&acc_full[buf]);
+        umma_commit_if(&empty[s], leader);
+        if (++s == (uint32_t)NST) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
+      umma_commit_if(&acc_full[buf], leader);
       done_item();
     }
     // every MMA issued has completed before the accumulators are freed
-    if (lane == 0) {
-      umma_commit(fin);
-      for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(fin, 0u); ++i) {
-      }
+    umma_commit_if(fin, leader);
+    for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(fin, 0u); ++i) {
     }
   } else {
     // ------------------------------------------------------------------ epilogue
