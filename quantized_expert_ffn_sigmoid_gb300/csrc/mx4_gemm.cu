@@ -54,7 +54,9 @@ constexpr uint32_t GAHEAD = 3;           // stages left to request when the next
 constexpr int GTHREADS = 576;
 constexpr int GW_EPI = 4, GW_MMA = 8, GW_TMA = 9, GW_SCHED = 13, GW_COPY = 14;
 constexpr int GROLES = 17;               // warps that read an item
-constexpr int GEC = 8;                   // columns exchanged at a time between gate and up lanes
+// columns exchanged at a time between gate and up lanes (small tiles leave
+// less shared memory, and have few columns)
+__host__ __device__ constexpr int g_ex_cols(int n) { return n <= 32 ? 8 : 16; }
 constexpr int GMAXENT = MAX_E + MAX_SHARED;
 constexpr uint32_t GSCOLS = 32;          // TMEM columns of one stage's scales: 4 x K / 128 x 4 for each operand
 constexpr uint32_t GTMEM = 512;
@@ -94,7 +96,7 @@ __host__ __device__ inline Mx4Smem g_smem(const Mx4Tile& t) {
   Mx4Smem s;
   uint32_t at = g_stage(t.n) * (uint32_t)t.stages;
   s.scales = at;  at += g_scale_slot(t.n) * (uint32_t)t.stages;
-  s.ex = at;      at += GM * (GEC + 1) * 4;
+  s.ex = at;      at += GM * (uint32_t)(g_ex_cols(t.n) + 1) * 4;
   s.bars = at;    at += 320;
   s.items = at;   at += GIR * sizeof(Mx4Item);
   s.tiles = at;   at += (GMAXENT + 1) * 4;
@@ -167,6 +169,60 @@ __device__ __forceinline__ void store_cols(T* y, long long ldy, const uint32_t* 
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     if (i < n) y[i * ldy] = from_f32<T>(__uint_as_float(v[i]));
+}
+
+// EC columns of a gate/up tile: lanes 0-63 hold gate rows, 64-127 up rows.
+// Through shared memory warps 0 and 1 take the first half of the columns and
+// warps 2 and 3 the second, each warp 32 h rows: one MX4 block a column.
+// r: lane of the tile; n: columns from here on that exist; codes, scales: of
+// the block in the first column's h row, rows `pitch` values apart.
+template <int EC>
+__device__ __forceinline__ void swiglu_cols(float* ex, uint32_t tmem, int r, int n, uint8_t* codes, uint8_t* scales, int pitch, uint32_t* status) {
+  const int lane = r & 31, c0 = (r >> 6) * (EC / 2), hr = r & 63;
+  uint32_t v[EC];
+  if constexpr (EC == 16) tmem_ld16_nowait(tmem, v);
+  else tmem_ld8_nowait(tmem, v);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < EC; ++i) ex[r * (EC + 1) + i] = __uint_as_float(v[i]);
+  named_bar(2, 128);
+  // every value before the first store, or the columns run one after the
+  // other (byte stores may alias anything)
+  uint32_t code[EC / 2], byte[EC / 2];
+#pragma unroll
+  for (int i = 0; i < EC / 2; ++i) {
+    const float g = ex[hr * (EC + 1) + c0 + i], u = ex[(64 + hr) * (EC + 1) + c0 + i];
+    const float h = __fdividef(g, 1.0f + expf(-g)) * u;
+    byte[i] = mx4_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu));
+    const float hv = byte[i] == 255u ? 0.f : h * mx4_inv(byte[i]);
+    code[i] = mx4_pack2(hv, __shfl_down_sync(0xffffffffu, hv, 1));
+  }
+  named_bar(2, 128);  // the exchange space is free
+  codes += (long long)c0 * (pitch / 2) + lane / 2;
+  scales += (long long)c0 * (pitch / MXB);
+#pragma unroll
+  for (int i = 0; i < EC / 2; ++i) {
+    if (c0 + i < n) {
+      if ((lane & 1) == 0) codes[(long long)i * (pitch / 2)] = (uint8_t)code[i];
+      if (lane == 0) {
+        scales[(long long)i * (pitch / MXB)] = (uint8_t)byte[i];
+        if (byte[i] == 255u) atomicOr(status, COLI_STATUS_NONFINITE);
+      }
+    }
+  }
+}
+
+// A bounded wait (as pf_wait) without a suspend-time hint, for the two roles
+// on the pipeline's critical path: it wakes sooner than a hinted one and takes
+// fewer issue slots from the epilogue than polling.
+__device__ __forceinline__ bool pf_wait_try(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+  for (uint32_t i = 0; i < SPIN_LIMIT; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  atomicOr(status, COLI_STATUS_TIMEOUT);
+  return false;
 }
 
 // Waits until the entry's gate/up items are complete (bounded, as pf_wait).
@@ -383,7 +439,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     while (next_item(it)) {
       for (int st = 0; st < it.nst; ++st, ++gs) {
         const uint32_t s = gs % NST;
-        pf_wait_poll(&sc_full[s], (gs / NST) & 1u, status, s_abort);
+        pf_wait_try(&sc_full[s], (gs / NST) & 1u, status, s_abort);
         const uint4* src = reinterpret_cast<const uint4*>(sm + S.scales + s * slot);
         uint32_t a[16], b[16];
 #pragma unroll
@@ -514,9 +570,9 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     while (next_item(it)) {
       const uint32_t idesc = mx4_idesc((it.ntok + 15) & ~15);
       const uint32_t buf = n_item & 1u, d = taddr + buf * acc_cols;
-      bool ok = pf_wait_poll(&acc_empty[buf], ((n_item >> 1) & 1u) ^ 1u, status, s_abort);
+      bool ok = pf_wait_try(&acc_empty[buf], ((n_item >> 1) & 1u) ^ 1u, status, s_abort);
       for (int st = 0; st < it.nst; ++st) {
-        ok = ok && pf_wait_poll(&full[s], phase, status, s_abort);
+        ok = ok && pf_wait_try(&full[s], phase, status, s_abort);
         if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
           tmem_fence_after();
           const uint32_t a0 = smem_u32(sm) + s * STAGE, b0 = a0 + GABYTES;
@@ -558,45 +614,19 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       tmem_fence_after();
       __syncwarp();
       if (LAYER && !it.down) {
-        // lanes 0-63 hold gate rows, 64-127 up rows: through shared memory, GEC
-        // columns at a time; then warps 0, 1 take the first half of the columns
-        // and warps 2, 3 the second, each warp one MX4 block of 32 h rows
         float* ex = reinterpret_cast<float*>(sm + S.ex);
-        const int blk = q & 1, c0 = (q >> 1) * (GEC / 2), hr = blk * 32 + lane;
-        uint8_t* hq = A.ws + A.L.hq;
-        uint8_t* hs = A.ws + A.L.hs;
-        for (int c = 0; c < it.ntok; c += GEC) {
-          uint32_t v[GEC];
-          tmem_ld8_nowait(d + c, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < GEC; ++i) ex[r * (GEC + 1) + i] = __uint_as_float(v[i]);
-          named_bar(2, 128);
-          // every value before the first store, or the columns run one after
-          // the other (byte stores may alias anything)
-          uint32_t code[GEC / 2], byte[GEC / 2];
-#pragma unroll
-          for (int i = 0; i < GEC / 2; ++i) {
-            const float g = ex[hr * (GEC + 1) + c0 + i], u = ex[(64 + hr) * (GEC + 1) + c0 + i];
-            const float h = __fdividef(g, 1.0f + expf(-g)) * u;
-            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
-            byte[i] = mx4_scale_byte(m);
-            const float hv = byte[i] == 255u ? 0.f : h * mx4_inv(byte[i]);
-            code[i] = mx4_pack2(hv, __shfl_down_sync(0xffffffffu, hv, 1));
-          }
-          const long long at = (long long)(it.row0 + c + c0) * A.L.imax + it.r0 + blk * 32;
-#pragma unroll
-          for (int i = 0; i < GEC / 2; ++i) {
-            if (c + c0 + i >= it.ntok) break;
-            if ((lane & 1) == 0) hq[(at + (long long)i * A.L.imax) / 2 + lane / 2] = (uint8_t)code[i];
-            if (lane == 0) {
-              hs[(at + (long long)i * A.L.imax) / MXB] = (uint8_t)byte[i];
-              if (byte[i] == 255u) atomicOr(status, COLI_STATUS_NONFINITE);
-            }
-          }
-          if (c + GEC >= it.ntok) fence_proxy_async_global();  // the down items read h through TMA
-          named_bar(2, 128);
+        const int pitch = A.L.imax;
+        const long long at = (long long)it.row0 * pitch + it.r0 + (q & 1) * 32;
+        uint8_t* hq = A.ws + A.L.hq + at / 2;
+        uint8_t* hs = A.ws + A.L.hs + at / MXB;
+        if (T.n > 32) {
+          for (int c = 0; c < it.ntok; c += 16)
+            swiglu_cols<16>(ex, d + c, r, it.ntok - c, hq + (long long)c * (pitch / 2), hs + (long long)c * (pitch / MXB), pitch, status);
+        } else {
+          for (int c = 0; c < it.ntok; c += 8)
+            swiglu_cols<8>(ex, d + c, r, it.ntok - c, hq + (long long)c * (pitch / 2), hs + (long long)c * (pitch / MXB), pitch, status);
         }
+        named_bar(2, 128);  // (the down items' producers order h before their TMA reads)
         if (q == 0 && lane == 0) red_release_add(ready + it.entry, 1u);
       } else {
         const bool live = it.r0 + r < it.rows;
