@@ -22,11 +22,14 @@
 // entry) ends however many CTAs are resident; meanwhile the down weights
 // already stream into the ring.
 //
-// One persistent CTA per SM, eighteen warps meeting at mbarriers:
+// One persistent CTA per SM, 22 warps meeting at mbarriers:
 //   warps 0-3   scales into tensor memory.  Row r of a 128-row tile is lane
 //               r % 32, column r / 32 (the four bytes of K / 128 in one 32-bit
 //               column), repeated in all four lane quarters, one per warp;
-//   warps 4-7   epilogue: accumulators to y, or SwiGLU and MX4 of h;
+//   warps 4-7 and 18-21  epilogue: accumulators to y, or SwiGLU and MX4 of h.
+//               Two sets of four, taking the columns of a tile in turn: with
+//               one set a gate/up tile of 64 columns took 18,000 cycles,
+//               longer than its products;
 //   warp 8      MMA issuer;
 //   warps 9-12  TMA producers of the codes, one for each 128-byte half of a
 //               stage of each operand (one thread issues a box of 8 KB every
@@ -51,13 +54,10 @@ constexpr int GK = 512;                  // K of a stage
 constexpr uint32_t GABYTES = GM * GK / 2;  // 32 KB of weight codes per stage
 constexpr int GIR = 4;                   // ring of items
 constexpr uint32_t GAHEAD = 3;           // stages left to request when the next item is claimed
-constexpr int GTHREADS = 576;
-constexpr int GW_EPI = 4, GW_MMA = 8, GW_TMA = 9, GW_SCHED = 13, GW_COPY = 14;
-constexpr int GROLES = 17;               // warps that read an item
-// columns exchanged at a time between gate and up lanes (small tiles leave
-// less shared memory, and have few columns)
-__host__ __device__ constexpr int g_ex_cols(int n) { return n <= 32 ? 8 : 16; }
-constexpr int GMAXENT = MAX_E + MAX_SHARED;
+constexpr int GTHREADS = 704;
+constexpr int GW_EPI = 4, GW_MMA = 8, GW_TMA = 9, GW_SCHED = 13, GW_COPY = 14, GW_EPI2 = 18;
+constexpr int GROLES = 21;               // warps that read an item
+constexpr int GEC = 8;                   // columns exchanged at a time between gate and up lanes
 constexpr uint32_t GSCOLS = 32;          // TMEM columns of one stage's scales: 4 x K / 128 x 4 for each operand
 constexpr uint32_t GTMEM = 512;
 constexpr int G_MAX_SMEM = 227 * 1024;   // dynamic shared memory of a CTA
@@ -72,7 +72,8 @@ struct Mx4Maps {
 // tile capacity on the N side and what follows from it
 struct Mx4Tile {
   int n;          // activation rows per tile: 16, 32, 64 or 128
-  int stages;
+  int entries;    // most entries of the launch
+  int stages;     // as many as fit
 };
 
 // one item, as the schedule warp leaves it for the others
@@ -96,11 +97,11 @@ __host__ __device__ inline Mx4Smem g_smem(const Mx4Tile& t) {
   Mx4Smem s;
   uint32_t at = g_stage(t.n) * (uint32_t)t.stages;
   s.scales = at;  at += g_scale_slot(t.n) * (uint32_t)t.stages;
-  s.ex = at;      at += GM * (uint32_t)(g_ex_cols(t.n) + 1) * 4;
+  s.ex = at;      at += 2 * GM * (GEC + 1) * 4;
   s.bars = at;    at += 320;
   s.items = at;   at += GIR * sizeof(Mx4Item);
-  s.tiles = at;   at += (GMAXENT + 1) * 4;
-  s.row0 = at;    at += (GMAXENT + 1) * 4;
+  s.tiles = at;   at += (uint32_t)(t.entries + 1) * 4;
+  s.row0 = at;    at += (uint32_t)(t.entries + 1) * 4;
   s.total = at + 1024;  // alignment slack
   return s;
 }
@@ -171,41 +172,41 @@ __device__ __forceinline__ void store_cols(T* y, long long ldy, const uint32_t* 
     if (i < n) y[i * ldy] = from_f32<T>(__uint_as_float(v[i]));
 }
 
-// EC columns of a gate/up tile: lanes 0-63 hold gate rows, 64-127 up rows.
-// Through shared memory warps 0 and 1 take the first half of the columns and
-// warps 2 and 3 the second, each warp 32 h rows: one MX4 block a column.
-// r: lane of the tile; n: columns from here on that exist; codes, scales: of
-// the block in the first column's h row, rows `pitch` values apart.
-template <int EC>
-__device__ __forceinline__ void swiglu_cols(float* ex, uint32_t tmem, int r, int n, uint8_t* codes, uint8_t* scales, int pitch, uint32_t* status) {
-  const int lane = r & 31, c0 = (r >> 6) * (EC / 2), hr = r & 63;
-  uint32_t v[EC];
-  if constexpr (EC == 16) tmem_ld16_nowait(tmem, v);
-  else tmem_ld8_nowait(tmem, v);
+// GEC columns of a gate/up tile by one set of epilogue warps: lanes 0-63 hold
+// gate rows, 64-127 up rows.  Through shared memory warps 0 and 1 take the
+// first half of the columns and warps 2 and 3 the second, each warp 32 h rows:
+// one MX4 block a column.  r: lane of the tile; n: columns from here on that
+// exist; codes, scales: of the block in the first column's h row, the next
+// column's `pitch` values further.
+__device__ __forceinline__ void swiglu_cols(float* ex, int bar, uint32_t tmem, int r, int n, uint8_t* codes, uint8_t* scales, int pitch,
+                                            uint32_t* status) {
+  const int lane = r & 31, c0 = (r >> 6) * (GEC / 2), hr = r & 63;
+  uint32_t v[GEC];
+  tmem_ld8_nowait(tmem, v);
   tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < EC; ++i) ex[r * (EC + 1) + i] = __uint_as_float(v[i]);
-  named_bar(2, 128);
+  for (int i = 0; i < GEC; ++i) ex[r * (GEC + 1) + i] = __uint_as_float(v[i]);
+  named_bar(bar, 128);
   // every value before the first store, or the columns run one after the
   // other (byte stores may alias anything)
-  uint32_t code[EC / 2], byte[EC / 2];
+  uint32_t code[GEC / 2], byte[GEC / 2];
 #pragma unroll
-  for (int i = 0; i < EC / 2; ++i) {
-    const float g = ex[hr * (EC + 1) + c0 + i], u = ex[(64 + hr) * (EC + 1) + c0 + i];
-    const float h = __fdividef(g, 1.0f + expf(-g)) * u;
+  for (int i = 0; i < GEC / 2; ++i) {
+    const float g = ex[hr * (GEC + 1) + c0 + i], u = ex[(64 + hr) * (GEC + 1) + c0 + i];
+    const float h = __fdividef(g, 1.0f + __expf(-g)) * u;
     byte[i] = mx4_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu));
     const float hv = byte[i] == 255u ? 0.f : h * mx4_inv(byte[i]);
     code[i] = mx4_pack2(hv, __shfl_down_sync(0xffffffffu, hv, 1));
   }
-  named_bar(2, 128);  // the exchange space is free
-  codes += (long long)c0 * (pitch / 2) + lane / 2;
-  scales += (long long)c0 * (pitch / MXB);
+  named_bar(bar, 128);  // the exchange space is free
+  codes += c0 * (pitch / 2) + lane / 2;
+  scales += c0 * (pitch / MXB);
 #pragma unroll
-  for (int i = 0; i < EC / 2; ++i) {
+  for (int i = 0; i < GEC / 2; ++i) {
     if (c0 + i < n) {
-      if ((lane & 1) == 0) codes[(long long)i * (pitch / 2)] = (uint8_t)code[i];
+      if ((lane & 1) == 0) codes[i * (pitch / 2)] = (uint8_t)code[i];
       if (lane == 0) {
-        scales[(long long)i * (pitch / MXB)] = (uint8_t)byte[i];
+        scales[i * (pitch / MXB)] = (uint8_t)byte[i];
         if (byte[i] == 255u) atomicOr(status, COLI_STATUS_NONFINITE);
       }
     }
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 8);
     }
     mbar_init(fin, 1);
     *s_abort = 0;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
             // a record is gate, up, down: 3 * inter rows of pitch hidden, or 3 * hidden
             // rows of pitch inter of which the last third are the down rows
             it.wrow = rec * 3 * it.rows + (it.down ? 2 * it.rows : 0) + it.r0;
-            it.ready = inter / 64 * ntn;
+            it.ready = 2 * (inter / 64) * ntn;  // both epilogue sets of every item
           } else {
             it.r0 = m * GM;
             it.rows = A.N;
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       }
       done_item();
     }
-  } else if (warp >= GW_COPY) {
+  } else if (warp >= GW_COPY && warp < GW_EPI2) {
     // ------------------------------------------------------- copies of scale bytes
     const int t = tid - 32 * GW_COPY;
     const uint32_t slot = g_scale_slot(T.n);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       done_item();
     }
     cp_async_wait<0>();
-  } else if (warp >= GW_TMA) {
+  } else if (warp >= GW_TMA && warp < GW_SCHED) {
     // ------------------------------------------------------------ TMA producers
     const int h = (warp - GW_TMA) & 1;         // 128-byte half of the stage
     const bool weights = warp - GW_TMA < 2;
@@ -605,32 +606,28 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    const int q = warp - GW_EPI, r = q * 32 + lane;
+    const int set = warp >= GW_EPI2, bar = 2 + set;
+    const int q = warp & 3, r = q * 32 + lane;  // lane quarter, lane of the tile
     const uint32_t lane0 = taddr + ((uint32_t)(32 * q) << 16);
     Mx4Item it;
-    while (named_bar_and(2, 128, next_item(it))) {
+    while (named_bar_and(bar, 128, next_item(it))) {
       const uint32_t buf = n_item & 1u, d = lane0 + buf * acc_cols;
       pf_wait(&acc_full[buf], (n_item >> 1) & 1u, status, s_abort);
       tmem_fence_after();
       __syncwarp();
       if (LAYER && !it.down) {
-        float* ex = reinterpret_cast<float*>(sm + S.ex);
+        float* ex = reinterpret_cast<float*>(sm + S.ex) + set * GM * (GEC + 1);
         const int pitch = A.L.imax;
         const long long at = (long long)it.row0 * pitch + it.r0 + (q & 1) * 32;
         uint8_t* hq = A.ws + A.L.hq + at / 2;
         uint8_t* hs = A.ws + A.L.hs + at / MXB;
-        if (T.n > 32) {
-          for (int c = 0; c < it.ntok; c += 16)
-            swiglu_cols<16>(ex, d + c, r, it.ntok - c, hq + (long long)c * (pitch / 2), hs + (long long)c * (pitch / MXB), pitch, status);
-        } else {
-          for (int c = 0; c < it.ntok; c += 8)
-            swiglu_cols<8>(ex, d + c, r, it.ntok - c, hq + (long long)c * (pitch / 2), hs + (long long)c * (pitch / MXB), pitch, status);
-        }
-        named_bar(2, 128);  // (the down items' producers order h before their TMA reads)
-        if (q == 0 && lane == 0) red_release_add(ready + it.entry, 1u);
+        for (int c = set * GEC; c < it.ntok; c += 2 * GEC)
+          swiglu_cols(ex, bar, d + c, r, it.ntok - c, hq + c * (pitch / 2), hs + c * (pitch / MXB), pitch, status);
+        named_bar(bar, 128);  // (the down items' producers order h before their TMA reads)
+        if (r == 0) red_release_add(ready + it.entry, 1u);
       } else {
         const bool live = it.r0 + r < it.rows;
-        for (int c = 0; c < it.ntok; c += 16) {
+        for (int c = set * 16; c < it.ntok; c += 32) {
           uint32_t v[16];
           tmem_ld16_nowait(d + c, v);
           tmem_wait_ld();
@@ -660,12 +657,16 @@ bool encode_bytes(CUtensorMap* m, const void* base, size_t row_bytes, size_t row
   return encode_rows_sw(m, base, row_bytes, rows, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-Mx4Tile tile_for(int most) {
+// The tile for at most `most` activation rows per entry: the smallest that
+// holds them, up to 128.
+Mx4Tile tile_for(int most, int entries) {
   Mx4Tile T;
   T.n = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
-  const int n_env = getenv("MXN") ? atoi(getenv("MXN")) : 0;
-  if (n_env && n_env < T.n) T.n = n_env;
-  T.stages = T.n == 128 ? 3 : T.n == 64 ? 4 : 5;
+  const char* ev = getenv("MXN");
+  if (ev && atoi(ev) < T.n) T.n = atoi(ev);
+  T.entries = entries;
+  T.stages = 6;
+  while (T.stages > 1 && g_smem(T).total > (uint32_t)G_MAX_SMEM) --T.stages;
   return T;
 }
 
@@ -690,7 +691,7 @@ cudaError_t launch(const Mx4Maps& maps, const Mx4Gemm& A, const Mx4Tile& T, cuda
 }  // namespace
 
 cudaError_t launch_mx4_product(const Mx4Gemm& A, cudaStream_t st) {
-  const Mx4Tile T = tile_for(A.P);
+  const Mx4Tile T = tile_for(A.P, A.G);
   Mx4Maps maps{};
   bool ok = encode_bytes(&maps.w[0], A.wc, A.K / 2, (size_t)A.G * A.N, GM);
   for (int i = 0; ok && 16 << i <= T.n; ++i) ok = encode_bytes(&maps.x[i], A.xc, A.xpitch / 2, A.P, 16u << i);
@@ -698,7 +699,7 @@ cudaError_t launch_mx4_product(const Mx4Gemm& A, cudaStream_t st) {
 }
 
 cudaError_t launch_mx4_layer(const Mx4Gemm& A, cudaStream_t st) {
-  const Mx4Tile T = tile_for(A.L.T);  // an expert holds at most every position
+  const Mx4Tile T = tile_for(A.L.T, A.L.n_ent_max);  // an expert holds at most every position
   Mx4Maps maps{};
   const coli_moe_cfg& c = A.cfg;
   const size_t H = c.hidden, I = c.inter, Is = c.shared_inter, n = (size_t)ep_records(c) * 3, ns = (size_t)c.n_shared * 3;
