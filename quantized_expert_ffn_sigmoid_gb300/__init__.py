@@ -372,13 +372,17 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
     """y[p] = w[group of p] x[p] for x_codes [P, K/2], w_codes [G, N, K/2] (or [N, K/2]) with their
     scales; ``offsets`` [G + 1] int32 on the device gives each group's first row (None: one group)."""
     P, k2 = shape = x_codes.shape
-    K = 2 * k2
-    ws_shape = w_codes.shape
-    G, N = (ws_shape[0], ws_shape[1]) if len(ws_shape) == 3 else (1, ws_shape[0])
-    off = None if offsets is None else _flat(offsets, (G + 1,), 4, "offsets")
-    rc = lib.coli_mx4_product(_bytes(x_codes, shape, "x_codes"), _bytes(x_scales, (P, K // 32), "x_scales"), P,
-                              _bytes(w_codes, (*ws_shape[:-1], k2), "w_codes"), _bytes(w_scales, (*ws_shape[:-1], K // 32), "w_scales"),
-                              G, N, K, off, y.data_ptr(), _type(y), _rows(y, (P, N), "y"), ws.data_ptr(), ws.numel(), _on(y, stream))
+    w_shape = w_codes.shape
+    if len(w_shape) == 3:
+        G, N, _ = w_shape
+        codes, scales = (G, N, k2), (G, N, k2 // 16)
+    else:
+        G, (N, _) = 1, w_shape
+        codes, scales = (N, k2), (N, k2 // 16)
+    rc = lib.coli_mx4_product(_bytes(x_codes, shape, "x_codes"), _bytes(x_scales, (P, k2 // 16), "x_scales"), P,
+                              _bytes(w_codes, codes, "w_codes"), _bytes(w_scales, scales, "w_scales"), G, N, 2 * k2,
+                              None if offsets is None else _flat(offsets, (G + 1,), 4, "offsets"),
+                              y.data_ptr(), _type(y), _rows(y, (P, N), "y"), ws.data_ptr(), ws.numel(), _on(y, stream))
     if rc:
         _check(rc, "coli_mx4_product")
 
@@ -430,30 +434,33 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
     x [T, H]: writes whichever of x_out (may be x), n_out, codes + scales (MX4 of n) are given.
     ``gate`` is [H] or [T, H]."""
     T, H = shape = x.shape
-    ty = _type(x)
-    a = NormArgs(x.data_ptr(), _rows(x, shape, "x"), res_scale=res_scale, eps=eps, type=ty, n_type=ty)
+    dtype, ty = x.dtype, _type(x)
+    yp = gp = xp = np = None
+    ldy = ldg = ldx = ldn = 0
+    nt = ty
     if y is not None:
-        a.y, a.ldy = y.data_ptr(), _rows(y, shape, "y")
+        if y.dtype is not dtype:
+            raise TypeError(f"y must have x's type {dtype}, not {y.dtype}")
+        yp, ldy = y.data_ptr(), _rows(y, shape, "y")
     if gate is not None:
+        if gate.dtype is not dtype:
+            raise TypeError(f"gate must have x's type {dtype}, not {gate.dtype}")
         if gate.dim() == 1:
-            a.gate = _flat(gate, (H,), gate.element_size(), "gate")
+            gp = _flat(gate, (H,), gate.element_size(), "gate")
         else:
-            a.gate, a.ld_gate = gate.data_ptr(), _rows(gate, shape, "gate")
+            gp, ldg = gate.data_ptr(), _rows(gate, shape, "gate")
     if x_out is not None:
-        a.x_out, a.ld_x_out = x_out.data_ptr(), _rows(x_out, shape, "x_out")
+        if x_out.dtype is not dtype:
+            raise TypeError(f"x_out must have x's type {dtype}, not {x_out.dtype}")
+        xp, ldx = x_out.data_ptr(), _rows(x_out, shape, "x_out")
     if n_out is not None:
-        a.n_out, a.ld_n_out, a.n_type = n_out.data_ptr(), _rows(n_out, shape, "n_out"), _type(n_out)
-    for t in (y, gate, x_out):
-        if t is not None and t.dtype is not x.dtype:
-            raise TypeError(f"y, gate and x_out must have x's type {x.dtype}, not {t.dtype}")
-    if post_w is not None:
-        a.post_w = _flat(post_w, (H,), 4, "post_w")
-    if pre_w is not None:
-        a.pre_w = _flat(pre_w, (H,), 4, "pre_w")
-    if codes is not None:
-        a.codes = _bytes(codes, (T, H // 2), "codes")
-    if scales is not None:
-        a.scales = _bytes(scales, (T, H // 32), "scales")
-    rc = lib.coli_moe_block_norm(ctypes.byref(a), T, H, _on(x, stream))
+        np, ldn = n_out.data_ptr(), _rows(n_out, shape, "n_out")
+        if n_out.dtype is not dtype:
+            nt = _type(n_out)
+    args = NormArgs(x.data_ptr(), _rows(x, shape, "x"), yp, ldy, gp, ldg, xp, ldx, np, ldn,
+                    None if post_w is None else _flat(post_w, (H,), 4, "post_w"), None if pre_w is None else _flat(pre_w, (H,), 4, "pre_w"),
+                    None if codes is None else _bytes(codes, (T, H // 2), "codes"),
+                    None if scales is None else _bytes(scales, (T, H // 32), "scales"), res_scale, eps, ty, nt)
+    rc = lib.coli_moe_block_norm(args, T, H, _on(x, stream))
     if rc:
         _check(rc, "coli_moe_block_norm")

@@ -62,11 +62,17 @@ constexpr uint32_t GSCOLS = 32;          // TMEM columns of one stage's scales: 
 constexpr uint32_t GTMEM = 512;
 constexpr int G_MAX_SMEM = 227 * 1024;   // dynamic shared memory of a CTA
 
+template <bool LAYER>
 struct Mx4Maps {
-  // 128 bytes x 128 rows (gate/up: 64) of weight codes; [1]: of the shared experts
-  CUtensorMap w[2], wd[2];
-  // 128 bytes x 16, 32, 64, 128 rows of activation codes, up to the tile's: x, and h for the down items
-  CUtensorMap x[4], h[4];
+  // 128 bytes x 16, 32, 64, 128 rows of activation codes, up to the tile's
+  CUtensorMap x[4];
+  // 128 bytes x 128 rows of weight codes
+  CUtensorMap w[1];
+};
+template <>
+struct Mx4Maps<true> {
+  CUtensorMap x[4], h[4];    // h: of the down items
+  CUtensorMap w[2], wd[2];   // gate/up (64 rows) and down; [1]: of the shared experts
 };
 
 // tile capacity on the N side and what follows from it
@@ -256,7 +262,7 @@ __device__ __forceinline__ bool named_bar_and(int id, int threads, bool v) {
 
 // LAYER: both passes of the expert layer; otherwise a grouped product
 template <bool LAYER>
-__global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ Mx4Maps maps, const Mx4Gemm A, const Mx4Tile T) {
+__global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ Mx4Maps<LAYER> maps, const Mx4Gemm A, const Mx4Tile T) {
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<size_t>(sm_raw), 1024));
   const Mx4Smem S = g_smem(T);
@@ -510,7 +516,9 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     while (next_item(it)) {
       if (lane == 0 && go) {
         const bool down = LAYER && it.down;
-        const CUtensorMap* wm = down ? &maps.wd[it.shared] : &maps.w[it.shared];
+        const CUtensorMap* wm = &maps.w[LAYER ? it.shared : 0];
+        if constexpr (LAYER)
+          if (down) wm = &maps.wd[it.shared];
         const int n16 = (it.ntok + 15) / 16;
         if (down && !weights) {  // h was written by ordinary stores
           wait_ready(ready + it.entry, it.ready, status, s_abort);
@@ -538,7 +546,9 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
               tma_load_2d_hint(dst + GABYTES / 4, wm, x, it.wrow + it.rows, &full[s], stream);
             }
           } else {
-            const CUtensorMap* xm = down ? maps.h : maps.x;
+            const CUtensorMap* xm = maps.x;
+            if constexpr (LAYER)
+              if (down) xm = maps.h;
             dst += GABYTES + h * T.n * 128;
             mbar_arrive_expect_tx(&full[s], (uint32_t)n16 * 2048);
             int row = 0;
@@ -671,7 +681,7 @@ Mx4Tile tile_for(int most, int entries) {
 }
 
 template <bool LAYER>
-cudaError_t launch(const Mx4Maps& maps, const Mx4Gemm& A, const Mx4Tile& T, cudaStream_t st) {
+cudaError_t launch(const Mx4Maps<LAYER>& maps, const Mx4Gemm& A, const Mx4Tile& T, long long items, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const Mx4Smem S = g_smem(T);
@@ -685,29 +695,33 @@ cudaError_t launch(const Mx4Maps& maps, const Mx4Gemm& A, const Mx4Tile& T, cuda
     if (e != cudaSuccess) return e;
     raised.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch_pdl(mx4_gemm<LAYER>, (unsigned)sms, GTHREADS, S.total, st, maps, A, T);
+  return launch_pdl(mx4_gemm<LAYER>, (unsigned)(items < sms ? items : sms), GTHREADS, S.total, st, maps, A, T);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_product(const Mx4Gemm& A, cudaStream_t st) {
   const Mx4Tile T = tile_for(A.P, A.G);
-  Mx4Maps maps{};
+  Mx4Maps<false> maps;
   bool ok = encode_bytes(&maps.w[0], A.wc, A.K / 2, (size_t)A.G * A.N, GM);
   for (int i = 0; ok && 16 << i <= T.n; ++i) ok = encode_bytes(&maps.x[i], A.xc, A.xpitch / 2, A.P, 16u << i);
-  return ok ? launch<false>(maps, A, T, st) : cudaErrorInvalidValue;
+  // (at most: a partial tile per group that can have rows)
+  const long long tiles = A.P / T.n + (A.G < A.P ? A.G : A.P);
+  return ok ? launch<false>(maps, A, T, tiles * ((A.N + GM - 1) / GM), st) : cudaErrorInvalidValue;
 }
 
 cudaError_t launch_mx4_layer(const Mx4Gemm& A, cudaStream_t st) {
   const Mx4Tile T = tile_for(A.L.T, A.L.n_ent_max);  // an expert holds at most every position
-  Mx4Maps maps{};
+  Mx4Maps<true> maps;
   const coli_moe_cfg& c = A.cfg;
   const size_t H = c.hidden, I = c.inter, Is = c.shared_inter, n = (size_t)ep_records(c) * 3, ns = (size_t)c.n_shared * 3;
   bool ok = encode_bytes(&maps.w[0], A.wc, H / 2, n * I, 64) && encode_bytes(&maps.wd[0], A.wc, I / 2, n * H, GM);
+  maps.w[1] = maps.w[0];
+  maps.wd[1] = maps.wd[0];
   if (ok && ns > 0) ok = encode_bytes(&maps.w[1], A.shc, H / 2, ns * Is, 64) && encode_bytes(&maps.wd[1], A.shc, Is / 2, ns * H, GM);
   for (int i = 0; ok && 16 << i <= T.n; ++i)
     ok = encode_bytes(&maps.x[i], A.xc, H / 2, A.P, 16u << i) && encode_bytes(&maps.h[i], A.ws + A.L.hq, A.L.imax / 2, A.P, 16u << i);
-  return ok ? launch<true>(maps, A, T, st) : cudaErrorInvalidValue;
+  return ok ? launch<true>(maps, A, T, (long long)A.L.n_ent_max * (H / GM), st) : cudaErrorInvalidValue;
 }
 
 }  // namespace colimoe
