@@ -97,7 +97,7 @@ __host__ __device__ inline uint32_t g_stage(int n) { return GABYTES + (uint32_t)
 // scale bytes of a stage: 16 per row, the activation rows up to a multiple of 32
 __host__ __device__ inline uint32_t g_scale_slot(int n) { return (uint32_t)(GM + (n <= 32 ? 32 : n)) * (GK / MXB); }
 struct Mx4Smem {
-  uint32_t scales, ex, bars, items, tiles, row0, total;
+  uint32_t scales, ex, bars, items, tiles, row0, ent, total;
 };
 __host__ __device__ inline Mx4Smem g_smem(const Mx4Tile& t) {
   Mx4Smem s;
@@ -108,6 +108,7 @@ __host__ __device__ inline Mx4Smem g_smem(const Mx4Tile& t) {
   s.items = at;   at += GIR * sizeof(Mx4Item);
   s.tiles = at;   at += (uint32_t)(t.entries + 1) * 4;
   s.row0 = at;    at += (uint32_t)(t.entries + 1) * 4;
+  s.ent = at;     at += (uint32_t)t.entries * 2;
   s.total = at + 1024;  // alignment slack
   return s;
 }
@@ -219,10 +220,12 @@ __device__ __forceinline__ void swiglu_cols(float* ex, int bar, uint32_t tmem, i
   }
 }
 
-// A bounded wait (as pf_wait) without a suspend-time hint, for the two roles
-// on the pipeline's critical path: it wakes sooner than a hinted one and takes
-// fewer issue slots from the epilogue than polling.
-__device__ __forceinline__ bool pf_wait_try(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+// A bounded wait that gives up at once after any wait of the CTA has expired
+// (the abort flag), so that a broken pipeline drains.  Without a suspend-time
+// hint, with which a thread wakes late, and not polling, which takes issue
+// slots from the epilogue: one position took 45.3 us against 47.2 with the
+// scale writers and the MMA warp polling.
+__device__ __forceinline__ bool gwait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
   for (uint32_t i = 0; i < SPIN_LIMIT; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
@@ -270,6 +273,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
   const int NST = T.stages;
   int* s_tiles = reinterpret_cast<int*>(sm + S.tiles);    // [entries + 1] tiles of activation rows before an entry
   int* s_row0 = reinterpret_cast<int*>(sm + S.row0);      // [entries + 1] first activation row
+  uint16_t* s_ent = reinterpret_cast<uint16_t*>(sm + S.ent);  // [entries] expert
   Mx4Item* s_items = reinterpret_cast<Mx4Item*>(sm + S.items);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + S.bars);  // [NST] codes landed, scales in TMEM
   uint64_t* empty = full + 8;                                 // [NST] the stage's products are done
@@ -316,9 +320,13 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
   if (LAYER && warp == GW_SCHED && lane == 0) first = (int)atomicAdd(claim, 1u);  // under way while the tables load
   const int n_ent = LAYER ? __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.hdr) + MH_NENT) : A.G;
   const int n_uniq = LAYER ? __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.hdr) + MH_NUNIQ) : n_ent;
-  for (int u = tid; u <= n_ent; u += GTHREADS) {
-    if (LAYER) s_row0[u] = __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_offset) + u);
-    else s_row0[u] = A.offsets ? min(max(__ldcg(A.offsets + u), 0), A.P) : u * A.P;
+  for (int u = tid; u <= T.entries; u += GTHREADS) {  // (beyond n_ent: not looked at)
+    if (LAYER) {
+      s_row0[u] = __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_offset) + u);
+      if (u < T.entries) s_ent[u] = (uint16_t)__ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_expert) + u);
+    } else {
+      s_row0[u] = A.offsets ? min(max(__ldcg(A.offsets + u), 0), A.P) : u * A.P;
+    }
   }
   tmem_fence_before();
   __syncthreads();
@@ -332,7 +340,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
   // waits at a barrier for one that has given up.
   uint32_t n_item = 0;
   auto next_item = [&](Mx4Item& it) {  // waits for item n_item and reads it; false: no more
-    if (!pf_wait(&item_full[n_item % GIR], (n_item / GIR) & 1u, status, s_abort)) return false;
+    if (!gwait(&item_full[n_item % GIR], (n_item / GIR) & 1u, status, s_abort)) return false;
     it = s_items[n_item % GIR];
     return it.nst > 0;
   };
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
           it.shared = LAYER && lo >= n_uniq;
           if (LAYER) {
             const int inter = it.shared ? c.shared_inter : c.inter;
-            const int rec = it.shared ? lo - n_uniq : ep_local(c, __ldcg(reinterpret_cast<const int32_t*>(A.ws + A.L.ent_expert) + lo));
+            const int rec = it.shared ? lo - n_uniq : ep_local(c, s_ent[lo]);
             it.r0 = m * (it.down ? GM : 64);
             it.rows = it.down ? c.hidden : inter;
             it.K = it.down ? inter : c.hidden;
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
           it.entry = lo;
           it.nst = (it.K + GK - 1) / GK;
         }
-        if (!pf_wait(&item_empty[n % GIR], ((n / GIR) & 1u) ^ 1u, status, s_abort)) break;
+        if (!gwait(&item_empty[n % GIR], ((n / GIR) & 1u) ^ 1u, status, s_abort)) break;
         s_items[n % GIR] = it;
         mbar_arrive(&item_full[n % GIR]);  // (release)
         if (it.nst == 0) break;
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     while (next_item(it)) {
       for (int st = 0; st < it.nst; ++st, ++gs) {
         const uint32_t s = gs % NST;
-        pf_wait_try(&sc_full[s], (gs / NST) & 1u, status, s_abort);
+        gwait(&sc_full[s], (gs / NST) & 1u, status, s_abort);
         const uint4* src = reinterpret_cast<const uint4*>(sm + S.scales + s * slot);
         uint32_t a[16], b[16];
 #pragma unroll
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       if (xlive) xp += (long long)(it.row0 + t) * xpitch;
       for (int st = 0; st < it.nst; ++st, ++gs) {
         const uint32_t s = gs % NST;
-        pf_wait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort);
+        gwait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort);
         uint8_t* dst = sm + S.scales + s * slot;
         const int at = st * (GK / MXB);
         copy_scales(dst + t * 16, wp, at, wlive ? pitch - at : 0);
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
         }
         for (int st = 0; st < it.nst; ++st, ++gs) {
           const uint32_t s = gs % NST;
-          if (!pf_wait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
+          if (!gwait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
           const int x = st * (GK / 2) + h * 128;
           if (x >= it.K / 2) {  // nothing of the row in this half: no products either
             mbar_arrive(&full[s]);
@@ -581,9 +589,9 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     while (next_item(it)) {
       const uint32_t idesc = mx4_idesc((it.ntok + 15) & ~15);
       const uint32_t buf = n_item & 1u, d = taddr + buf * acc_cols;
-      bool ok = pf_wait_try(&acc_empty[buf], ((n_item >> 1) & 1u) ^ 1u, status, s_abort);
+      bool ok = gwait(&acc_empty[buf], ((n_item >> 1) & 1u) ^ 1u, status, s_abort);
       for (int st = 0; st < it.nst; ++st) {
-        ok = ok && pf_wait_try(&full[s], phase, status, s_abort);
+        ok = ok && gwait(&full[s], phase, status, s_abort);
         if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
           tmem_fence_after();
           const uint32_t a0 = smem_u32(sm) + s * STAGE, b0 = a0 + GABYTES;
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
     Mx4Item it;
     while (named_bar_and(bar, 128, next_item(it))) {
       const uint32_t buf = n_item & 1u, d = lane0 + buf * acc_cols;
-      pf_wait(&acc_full[buf], (n_item >> 1) & 1u, status, s_abort);
+      gwait(&acc_full[buf], (n_item >> 1) & 1u, status, s_abort);
       tmem_fence_after();
       __syncwarp();
       if (LAYER && !it.down) {
