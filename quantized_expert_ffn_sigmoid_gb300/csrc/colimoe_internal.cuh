@@ -62,6 +62,7 @@ __host__ __device__ inline int ep_records(const coli_moe_cfg& c) {
 // each; the partial logits of every range are summed in range order.
 __host__ __device__ inline int route_ksplits(int T, int H, int E) {
   const int tiles = ((E + 63) / 64) * ((T + 63) / 64);
+  if (tiles == 0) return 1;  // no positions
   const int kmax = H / 192 > 0 ? H / 192 : 1;
   int ks = 1024 / tiles;
   ks = ks < 1 ? 1 : (ks > kmax ? kmax : ks);
