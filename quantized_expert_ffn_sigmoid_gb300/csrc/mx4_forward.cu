@@ -236,8 +236,12 @@ __global__ void __launch_bounds__(256) mx4_prep_small(const coli_moe_cfg c, cons
   }
 }
 
-// y[t] = sum_j w[t][j] o[row(t, j)] + sum_s o[shared row of t], in this order;
-// eight rows' loads in flight at a time
+// y[t] = sum_j w[t][j] o[row(t, j)] + sum_s o[shared row of t], in this order.
+// B rows' loads in flight per thread: 12 where there are few threads and one
+// round trip to L2 is what counts (one position: 39.8 us a layer call, 40.6
+// with 8), 3 where HBM is, so that the registers leave room for threads (2048
+// positions: 983 us, 1008 with 8, 1065 with 12).
+template <int B>
 __global__ void __launch_bounds__(256) mx4_combine(const coli_moe_cfg c, const Mx4Layout L, const uint8_t* __restrict__ ws, int T,
                                                    const float* __restrict__ topk_w, void* __restrict__ y, int32_t y_type) {
   const int H = c.hidden, k = c.top_k, ns = c.n_shared, h4 = H / 4;
@@ -250,7 +254,6 @@ __global__ void __launch_bounds__(256) mx4_combine(const coli_moe_cfg c, const M
   const int shared0 = __ldcg(reinterpret_cast<const int32_t*>(ws + L.hdr) + MH_NPAIRS) - ns * T;
   const float* o = reinterpret_cast<const float*>(ws + L.o);
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int B = 8;
   for (int j0 = 0; j0 < k + ns; j0 += B) {
     int r[B];
     float w[B];
@@ -306,7 +309,8 @@ cudaError_t launch_mx4_combine(const coli_moe_cfg& c, const Mx4Layout& L, const 
                                int32_t y_type, cudaStream_t st) {
   const long long blocks = ((long long)T * (c.hidden / 4) + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(mx4_combine, (unsigned)blocks, 256, 0, st, c, L, ws, T, topk_w, y, y_type);
+  return blocks <= 4LL * device_sms() ? launch_pdl(mx4_combine<12>, (unsigned)blocks, 256, 0, st, c, L, ws, T, topk_w, y, y_type)
+                                      : launch_pdl(mx4_combine<3>, (unsigned)blocks, 256, 0, st, c, L, ws, T, topk_w, y, y_type);
 }
 
 }  // namespace colimoe
