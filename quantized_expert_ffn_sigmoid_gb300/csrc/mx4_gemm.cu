@@ -36,7 +36,8 @@
 //               190 cycles, which alone held a stage back to 1150 cycles);
 //   warp 13     schedule: claims and decodes items ahead of their use;
 //   warps 14-17 copy the stage's scale bytes, one row of each operand per
-//               thread, with cp.async (16 bytes where the rows allow it).
+//               thread, with cp.async (16 bytes where the rows allow it) or,
+//               for rows that begin anywhere, through registers.
 //               Apart from the warps that use them, or a stage takes the sum
 //               of both latencies (1650 cycles).
 // Two accumulators, so a tile's epilogue overlaps the next tile's products.
@@ -162,23 +163,56 @@ __device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t* r) {
 }
 
 // 16 scale bytes of a row from byte `at` on, of which the first `valid` exist
-// (the rest become 0, the scale of codes that are 0), to shared memory.
-// The copies are as wide as the row's address allows.
+// (the rest become 0, the scale of codes that are 0), to shared memory; rows
+// of whole 32-bit words, copied as wide as their address allows.
 __device__ __forceinline__ void copy_scales(uint8_t* dst, const uint8_t* row, int at, int valid) {
-  const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(row + at) & 15u;
-  if (low == 0 && (valid >= 16 || valid <= 0)) {
+  if (((reinterpret_cast<uintptr_t>(row + at) & 15u) == 0) && (valid >= 16 || valid <= 0)) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(valid > 0 ? row + at : row), "r"(valid > 0 ? 16 : 0) : "memory");
-  } else if ((low & 3u) == 0 && (valid & 3) == 0) {
+  } else {
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst + i)), "l"(valid > i ? row + at + i : row), "r"(valid > i ? 4 : 0) : "memory");
-  } else {
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < valid) w[i / 4] |= (uint32_t)row[at + i] << (8 * (i % 4));
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// The same for rows that begin anywhere (K not a multiple of 128), through
+// registers: the aligned words that hold the bytes, put in place by shifts.
+// end: of the array, past which no word reaches.
+struct ScaleWords {
+  uint32_t w[5];
+};
+__device__ __forceinline__ ScaleWords load_scales(const uint8_t* row, int at, int valid, const uint8_t* end) {
+  ScaleWords s;
+  const uint8_t* p = row + at;
+  const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(p) & 3u;
+  const uint8_t* q = p - a;  // (not before the array, whose base is aligned)
+  if (q + 20 <= end) {  // all but the last bytes of the array (what is beyond `valid` is masked later)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) s.w[i] = valid > 0 ? __ldg(reinterpret_cast<const uint32_t*>(q) + i) : 0u;
+    return s;
+  }
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    uint32_t v = 0;
+    if (valid > 0 && q + 4 * i < end) {
+      v = q[4 * i];
+      if (q + 4 * i + 1 < end) v |= (uint32_t)q[4 * i + 1] << 8;
+      if (q + 4 * i + 2 < end) v |= (uint32_t)q[4 * i + 2] << 16;
+      if (q + 4 * i + 3 < end) v |= (uint32_t)q[4 * i + 3] << 24;
+    }
+    s.w[i] = v;
+  }
+  return s;
+}
+__device__ __forceinline__ void put_scales(uint8_t* dst, const ScaleWords& s, const uint8_t* row, int at, int valid) {
+  const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(row + at) & 3u;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = valid - 4 * i;  // bytes of this word that exist
+    o[i] = __funnelshift_r(s.w[i], s.w[i + 1], 8 * a) & (n >= 4 ? 0xffffffffu : n > 0 ? (1u << (8 * n)) - 1u : 0u);
+  }
+  *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // One element of y per lane and column: 16 columns (activation rows) of the
@@ -512,6 +546,30 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
       if (wlive) wp += ((long long)it.wrow + r + (gate_up && t >= 64 ? it.rows : 0)) * pitch;
       const uint8_t* xp = LAYER && it.down ? A.ws + A.L.hs : A.xs;
       if (xlive) xp += (long long)(it.row0 + t) * xpitch;
+      if (!LAYER && (pitch & 3)) {
+        // two stages ahead in registers: 2048 x 4096 x 6080 took 81 us with
+        // byte loads at their use, 44 this way (K = 6016, whose scale rows
+        // are whole words: 37)
+        const uint8_t* wend = A.wsc + (long long)A.G * A.N * pitch;
+        const uint8_t* xend = A.xs + (long long)A.P * pitch;
+        auto wload = [&](int st) { const int at = st * (GK / MXB); return load_scales(wp, at, wlive ? pitch - at : 0, wend); };
+        auto xload = [&](int st) { const int at = st * (GK / MXB); return load_scales(xp, at, xlive && has_row ? pitch - at : 0, xend); };
+        ScaleWords w0 = wload(0), x0 = xload(0), w1 = wload(1), x1 = xload(1);
+        for (int st = 0; st < it.nst; ++st, ++gs) {
+          const uint32_t s = gs % NST;
+          const ScaleWords w2 = wload(st + 2), x2 = xload(st + 2);
+          gwait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort);
+          uint8_t* dst = sm + S.scales + s * slot;
+          const int at = st * (GK / MXB);
+          put_scales(dst + t * 16, w0, wp, at, wlive ? pitch - at : 0);
+          if (has_row) put_scales(dst + (GM + t) * 16, x0, xp, at, xlive ? pitch - at : 0);
+          mbar_arrive(&sc_full[s]);
+          w0 = w1; w1 = w2;
+          x0 = x1; x1 = x2;
+        }
+        done_item();
+        continue;
+      }
       for (int st = 0; st < it.nst; ++st, ++gs) {
         const uint32_t s = gs % NST;
         gwait(&empty[s], ((gs / NST) & 1u) ^ 1u, status, s_abort);
