@@ -415,6 +415,33 @@ def test_layer_workspace_reuse_streams_and_graph(tiny):
         assert torch.equal(a, y)
 
 
+def test_layer_and_products_on_several_streams_at_once(tiny):
+    # calls on different streams share the SMs: each claims its work as it gets them
+    rng = np.random.default_rng(33)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    jobs = []
+    for i, T in enumerate((70, 1, 33, 130)):
+        x = dev(rng.standard_normal((T, 256)).astype(np.float32))
+        idx, w = tiny.routing(rng, T)
+        want = tiny.run(x, idx, w)
+        jobs.append((x, dev(idx), dev(w), torch.empty_like(want), cm.new_mx4_workspace(tiny.cfg, T), want, T))
+    xc, xb = random_mx4(rng, 500, K=512)
+    wc, wb = random_mx4(rng, 6, 700, K=512)
+    p = [dev(v) for v in (xc, xb, wc, wb)]
+    off = dev(np.array([0, 50, 50, 200, 210, 499, 500], np.int32))
+    pw = [cm.new_mx4_product_workspace() for _ in streams]
+    py = [torch.empty(500, 700, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (x, idx, w, y, ws, _, _), pws, y2 in zip(streams, jobs, pw, py):
+            cm.coli_mx4_forward(tiny.cfg, tiny.weights, x, idx, w, y, ws, stream=s)
+            cm.coli_mx4_product(*p, y2, pws, offsets=off, stream=s)
+    torch.cuda.synchronize()
+    for (_, _, _, y, ws, want, _), pws, y2 in zip(jobs, pw, py):
+        assert torch.equal(y, want) and torch.equal(y2, py[0])
+        assert cm.coli_moe_status(ws) == 0 and cm.coli_moe_status(pws) == 0
+
+
 @pytest.mark.parametrize("T", [1, 40])
 def test_layer_shards_sum_to_the_layer(T):
     rng = np.random.default_rng(40)
