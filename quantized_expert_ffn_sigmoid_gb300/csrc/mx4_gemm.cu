@@ -672,14 +672,14 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm(const __grid_constant__ 
             for (int k = 0; k < GK / 64; ++k)
               umma_mx4(d, da + (k >> 2) * (GABYTES / 32) + (k & 3) * 2, db + (k >> 2) * bh + (k & 3) * 2,
                        idesc | ((k & 1) * ((2u << 4) | (2u << 29))), sa + 4 * (k >> 1), sb + 4 * (k >> 1), k ? 1u : (uint32_t)(st != 0), leader);
-          } else if (steps == GK / 128) {
-            // half a stage unrolled too, as with K = 256, or the end of K = 768:
-            // this warp's way from one item to the next is what short items
-            // take.  256 groups of two rows, N = 4096, K = 256: 53.4 us looping,
-            // 44.9 this way; a layer of 256 experts of 2048 x 256 at 64
-            // positions 76.7 and 69.6.  The dense products of 4096 x 6144 pay
-            // about 1% for the longer code (101.8 and 103.0 at 8192 rows), a
-            // layer of 128 experts of 4096 x 512 at 64 positions 3%
+          } else if (LAYER && steps == GK / 128) {
+            // half a stage unrolled too, as in the down items of inter = 256 or
+            // the end of 768: this warp's way from one item to the next is what
+            // short items take.  256 experts of 2048 x 256 at 64 positions:
+            // 76.7 us looping, 69.6 this way; 4096 x 512 (128 experts) 99.7 and
+            // 102.9 for the longer code.  Not in the grouped product, whose long
+            // reductions would pay for the short: 8192 x 4096 x 6144 101.8 us
+            // without and 103.0 with it, 256 groups of 4096 x 256 53.4 and 44.9
 #pragma unroll
             for (int k = 0; k < GK / 128; ++k)
               umma_mx4(d, da + (k & 3) * 2, db + (k & 3) * 2,
