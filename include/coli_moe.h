@@ -316,13 +316,17 @@ int coli_moe_forward_dump(const coli_moe_cfg* cfg, const coli_moe_weights* weigh
  *     scales [K/32] bytes: b stands for 2^(b - 127); 255: the block has no
  *                   value (NaN)
  * and rows of a matrix are consecutive.  Products multiply the values that
- * codes and scales stand for and accumulate in fp32.
+ * codes and scales stand for and accumulate in fp32.  Rows have up to
+ * COLI_MX4_MAX_K values (COLI_EUNSUPPORTED beyond: the kernels index inside a
+ * row, rounded up to their steps, in 32 bits).
  *
  * Value types of the arguments named *_type: */
 #define COLI_F32  0
 #define COLI_BF16 1
 #define COLI_F16  2
 #define COLI_MX4  3   /* codes, with their scales in a second argument */
+
+#define COLI_MX4_MAX_K (1 << 30)
 
 /* Quantise rows to MX4: per block of 32 with largest magnitude A,
  * b = max(0, floor(log2 A) + 125) (0 for a block of zeros), every element

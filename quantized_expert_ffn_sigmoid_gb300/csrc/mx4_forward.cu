@@ -342,7 +342,7 @@ extern "C" int coli_mx4_product(const uint8_t* x_codes, const uint8_t* x_scales,
                                 const uint8_t* w_scales, int32_t G, int32_t N, int32_t K, const int32_t* offsets, void* y,
                                 int32_t y_type, int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t stream) {
   if (P < 0 || G < 1 || N < 1 || K < 1 || K % MXB || !float_type(y_type) || ldy < N) return COLI_EINVAL;
-  if (G > COLI_MX4_MAX_GROUPS || (long long)G * N > 0x7fffffffLL || P > 0x7fffffff / 64) return COLI_EUNSUPPORTED;
+  if (K > COLI_MX4_MAX_K || G > COLI_MX4_MAX_GROUPS || (long long)G * N > 0x7fffffffLL || P > 0x7fffffff / 64) return COLI_EUNSUPPORTED;
   if (!offsets && G != 1) return COLI_EINVAL;
   if (P == 0) return COLI_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !y || !ws) return COLI_EINVAL;

@@ -122,6 +122,7 @@ cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, int rows, in
 
 int check(const void* x, int32_t type, int64_t ld, int32_t T, int32_t K, const void* codes, const void* scales) {
   if (!float_type(type) || T < 0 || K <= 0 || K % MXB || ld < K) return COLI_EINVAL;
+  if (K > COLI_MX4_MAX_K) return COLI_EUNSUPPORTED;
   if (T == 0) return COLI_OK;
   if (!x || !codes || !scales) return COLI_EINVAL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return COLI_EALIGN;
