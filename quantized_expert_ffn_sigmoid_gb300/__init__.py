@@ -68,8 +68,11 @@ class StackLayer(ctypes.Structure):
 
 
 class Mx4Weights(ctypes.Structure):
+    """Four addresses, as in C.  ``make_mx4_weights`` also leaves the bytes behind each of them in
+    ``sizes``, which ``coli_mx4_forward`` compares with the configuration; a struct filled by hand has none."""
     _fields_ = [("experts", ctypes.c_void_p), ("expert_scales", ctypes.c_void_p),
                 ("shared", ctypes.c_void_p), ("shared_scales", ctypes.c_void_p)]
+    sizes = None
 
 
 class NormArgs(ctypes.Structure):
@@ -388,10 +391,32 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
 
 
 def make_mx4_weights(experts, expert_scales, shared=None, shared_scales=None) -> Mx4Weights:
-    """An MX4 weights struct from uint8 torch tensors (keep the tensors alive)."""
-    return Mx4Weights(experts.data_ptr(), expert_scales.data_ptr(),
-                      shared.data_ptr() if shared is not None and shared.numel() else None,
-                      shared_scales.data_ptr() if shared_scales is not None and shared_scales.numel() else None)
+    """An MX4 weights struct from contiguous uint8 GPU tensors (keep the tensors alive) that hold exactly
+    the records of the configuration they are used with: all experts, or those of its shard."""
+    at, sizes = [], []
+    for name, t in (("experts", experts), ("expert_scales", expert_scales), ("shared", shared), ("shared_scales", shared_scales)):
+        n = 0 if t is None else t.numel()
+        at.append(_bytes(t, t.shape, name) if n else None)
+        sizes.append(n)
+    w = Mx4Weights(*at)
+    w.sizes = tuple(sizes)
+    return w
+
+
+def _check_records(c, sizes):
+    """Whether weights of these sizes are the records of configuration c (its shard's experts; the shared
+    ones where they are used): the library sees addresses only."""
+    def record(n, inter):
+        return n * 3 * inter * c.hidden // 2, n * 3 * inter * c.hidden // 32
+
+    n = c.n_experts if c.ep_size <= 1 else (c.n_experts - c.ep_rank + c.ep_size - 1) // c.ep_size
+    want = record(n, c.inter)
+    if sizes[:2] != want:
+        raise ValueError(f"experts and expert_scales must be the records of {n} experts, {want} bytes, not {sizes[:2]}")
+    if c.n_shared > 0 and c.ep_rank == 0 and any(sizes[2:]):
+        want = record(c.n_shared, c.shared_inter)
+        if sizes[2:] != want:
+            raise ValueError(f"shared and shared_scales must be the records of {c.n_shared} shared experts, {want} bytes, not {sizes[2:]}")
 
 
 def coli_mx4_workspace_size(cfg, max_T: int) -> int:
@@ -420,6 +445,8 @@ def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_sca
         xp = _flat(x, (T, H), x.element_size(), "x")
     else:
         xp, xt, sp = _bytes(x, (T, H // 2), "x"), COLI_MX4, _bytes(x_scales, (T, H // 32), "x_scales")
+    if weights.sizes is not None:
+        _check_records(c, weights.sizes)
     k = c.top_k
     rc = lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, _flat(topk_idx, (T, k), 4, "topk_idx"),
                               _flat(topk_w, (T, k), 4, "topk_w"), _flat(y, (T, H), y.element_size(), "y"), _type(y),

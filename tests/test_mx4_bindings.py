@@ -1,0 +1,142 @@
+"""The MX4 bindings look at every tensor before the library is called.  No GPU:
+stand-ins answer what the bindings ask of a tensor, and a recorder takes the
+library's place, so nothing is launched whatever passes."""
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_expert_ffn_sigmoid_gb300 as cm  # noqa: E402
+
+
+class Stand:
+    """What a GPU tensor of this shape and type would answer."""
+
+    def __init__(self, *shape, dtype=torch.uint8, index=0, strides=None):
+        self.shape, self.dtype, self.index = torch.Size(shape), dtype, index
+        dense, n = [], 1
+        for s in reversed(shape):
+            dense.insert(0, n)
+            n *= s
+        self.strides = tuple(dense) if strides is None else strides
+        self.dense = self.strides == tuple(dense)
+        self.count = n
+
+    @property
+    def device(self):
+        return f"cuda:{self.index}" if self.index >= 0 else "cpu"
+
+    @property
+    def is_cuda(self):
+        return self.index >= 0
+
+    @property
+    def nbytes(self):
+        return self.count * self.element_size()
+
+    def get_device(self):
+        return self.index
+
+    def stride(self):
+        return self.strides
+
+    def is_contiguous(self):
+        return self.dense
+
+    def numel(self):
+        return self.count
+
+    def dim(self):
+        return len(self.shape)
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def data_ptr(self):
+        return 256 if self.count else 0
+
+
+class Recorder:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    rec = Recorder()
+    monkeypatch.setattr(cm, "lib", rec)
+    cm._torch_names()
+    monkeypatch.setattr(cm, "_raw_stream", lambda index: 0)
+    return rec.calls
+
+
+def cfg(ep_rank=0, ep_size=0, **kw):
+    d = dict(hidden=256, n_experts=16, n_groups=1, topk_group=1, top_k=4, inter=128, n_shared=1, shared_inter=384,
+             weight_bits=4, routed_scaling_factor=2.5)
+    d.update(kw)
+    return cm.Cfg.of(types.SimpleNamespace(**d), ep_rank, ep_size)
+
+
+def records(n, hidden=256, inter=128):
+    return Stand(n, 3 * inter * hidden // 2), Stand(n, 3 * inter * hidden // 32)
+
+
+def layer_args(T=3, hidden=256, k=4):
+    f = torch.float32
+    return [Stand(T, hidden, dtype=torch.bfloat16), Stand(T, k, dtype=torch.int32), Stand(T, k, dtype=f), Stand(T, hidden, dtype=f),
+            Stand(1 << 20)]
+
+
+# ------------------------------------------------------------------- the records
+@pytest.mark.parametrize("c,n", [(cfg(), 16), (cfg(n_shared=0), 16), (cfg(0, 3), 6), (cfg(1, 3), 5), (cfg(2, 3), 5), (cfg(0, 16), 1)])
+def test_records_of_the_configuration_are_taken(calls, c, n):
+    w = cm.make_mx4_weights(*records(n), *records(c.n_shared, inter=384))
+    cm.coli_mx4_forward(c, w, *layer_args())
+    assert calls == ["coli_mx4_forward"]
+
+
+def test_shared_records_are_looked_at_where_they_are_used(calls):
+    w = cm.make_mx4_weights(*records(16))                      # no shared experts at all: the library's own answer
+    cm.coli_mx4_forward(cfg(n_shared=0), w, *layer_args())
+    w = cm.make_mx4_weights(*records(5), *records(7))          # a shard that owns no shared experts ignores them
+    cm.coli_mx4_forward(cfg(1, 3), w, *layer_args())
+    assert len(calls) == 2
+
+
+@pytest.mark.parametrize("c,routed,shared", [
+    (cfg(), records(15), records(1, inter=384)),                                       # an expert short
+    (cfg(), records(6), records(1, inter=384)),                                        # a shard's records, the whole layer's configuration
+    (cfg(1, 3), records(16), ()),                                                      # the whole layer's, a shard's configuration
+    (cfg(), records(16, inter=64), records(1, inter=384)),                             # another layer's inter
+    (cfg(), records(16, hidden=128), records(1, inter=384)),
+    (cfg(), (records(16)[0], records(15)[1]), records(1, inter=384)),                  # scales of another count
+    (cfg(), records(16), records(1, inter=128)),                                       # shared_inter
+    (cfg(n_shared=2), records(16), records(1, inter=384)),
+    (cfg(), records(16), (records(1, inter=384)[0], records(1, inter=128)[1])),
+])
+def test_other_records_are_refused(calls, c, routed, shared):
+    w = cm.make_mx4_weights(*routed, *shared)
+    with pytest.raises(ValueError, match="record"):
+        cm.coli_mx4_forward(c, w, *layer_args())
+    assert not calls
+
+
+def test_weights_are_dense_bytes_on_the_gpu():
+    e, s = records(16)
+    for bad in (Stand(16, 3 * 128 * 256 // 2, index=-1), Stand(16, 3 * 128 * 256 // 2, strides=(1 << 20, 1)),
+                Stand(16, 3 * 128 * 256 // 2, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="experts"):
+            cm.make_mx4_weights(bad, s)
+        with pytest.raises(ValueError, match="expert_scales"):
+            cm.make_mx4_weights(e, bad)
+        with pytest.raises(ValueError, match="shared"):
+            cm.make_mx4_weights(e, s, bad, s)
+        with pytest.raises(ValueError, match="shared_scales"):
+            cm.make_mx4_weights(e, s, e, bad)
