@@ -292,13 +292,14 @@ def capture_stack_step(layers, xs, residual, topk_idx, topk_w, y, ws, add_output
 # keep their own cost to about that: one look at each tensor, plain integers
 # to ctypes, the raw handle of the current stream.
 _TYPES = {}
-_raw_stream = None
+_raw_stream = _F32 = _I32 = None
 
 
 def _torch_names():
-    global _raw_stream
+    global _raw_stream, _F32, _I32
     import torch
     _raw_stream = torch._C._cuda_getCurrentRawStream
+    _F32, _I32 = torch.float32, torch.int32
     _TYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float16: COLI_F16})
 
 
@@ -337,11 +338,12 @@ def _bytes(t, shape, name: str) -> int:
     return t.data_ptr()
 
 
-def _flat(t, shape, size: int, name: str) -> int:
-    """The address of a contiguous GPU tensor of `shape` with elements of `size` bytes."""
-    if t.shape != shape or t.element_size() != size or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)} with {size}-byte elements, "
-                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+def _flat(t, shape, dtype, name: str) -> int:
+    """The address of a contiguous GPU tensor of `shape` and `dtype`."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)}, not {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -382,10 +384,11 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
     else:
         G, (N, _) = 1, w_shape
         codes, scales = (N, k2), (N, k2 // 16)
+    yt = _type(y)
     rc = lib.coli_mx4_product(_bytes(x_codes, shape, "x_codes"), _bytes(x_scales, (P, k2 // 16), "x_scales"), P,
                               _bytes(w_codes, codes, "w_codes"), _bytes(w_scales, scales, "w_scales"), G, N, 2 * k2,
-                              None if offsets is None else _flat(offsets, (G + 1,), 4, "offsets"),
-                              y.data_ptr(), _type(y), _rows(y, (P, N), "y"), ws.data_ptr(), ws.numel(), _on(y, stream))
+                              None if offsets is None else _flat(offsets, (G + 1,), _I32, "offsets"),
+                              y.data_ptr(), yt, _rows(y, (P, N), "y"), ws.data_ptr(), ws.numel(), _on(y, stream))
     if rc:
         _check(rc, "coli_mx4_product")
 
@@ -440,16 +443,17 @@ def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_sca
     T, H = y.shape
     if H != c.hidden:
         raise ValueError(f"y must be [positions, {c.hidden}], not {tuple(y.shape)}")
+    yt = _type(y)
     if x_scales is None:
         xt, sp = _type(x), None
-        xp = _flat(x, (T, H), x.element_size(), "x")
+        xp = _flat(x, (T, H), x.dtype, "x")
     else:
         xp, xt, sp = _bytes(x, (T, H // 2), "x"), COLI_MX4, _bytes(x_scales, (T, H // 32), "x_scales")
     if weights.sizes is not None:
         _check_records(c, weights.sizes)
     k = c.top_k
-    rc = lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, _flat(topk_idx, (T, k), 4, "topk_idx"),
-                              _flat(topk_w, (T, k), 4, "topk_w"), _flat(y, (T, H), y.element_size(), "y"), _type(y),
+    rc = lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, _flat(topk_idx, (T, k), _I32, "topk_idx"),
+                              _flat(topk_w, (T, k), _F32, "topk_w"), _flat(y, (T, H), y.dtype, "y"), yt,
                               ws.data_ptr(), ws.numel(), _on(y, stream))
     if rc:
         _check(rc, "coli_mx4_forward")
@@ -473,7 +477,7 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
         if gate.dtype is not dtype:
             raise TypeError(f"gate must have x's type {dtype}, not {gate.dtype}")
         if gate.dim() == 1:
-            gp = _flat(gate, (H,), gate.element_size(), "gate")
+            gp = _flat(gate, (H,), dtype, "gate")
         else:
             gp, ldg = gate.data_ptr(), _rows(gate, shape, "gate")
     if x_out is not None:
@@ -485,7 +489,7 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
         if n_out.dtype is not dtype:
             nt = _type(n_out)
     args = NormArgs(x.data_ptr(), _rows(x, shape, "x"), yp, ldy, gp, ldg, xp, ldx, np, ldn,
-                    None if post_w is None else _flat(post_w, (H,), 4, "post_w"), None if pre_w is None else _flat(pre_w, (H,), 4, "pre_w"),
+                    None if post_w is None else _flat(post_w, (H,), _F32, "post_w"), None if pre_w is None else _flat(pre_w, (H,), _F32, "pre_w"),
                     None if codes is None else _bytes(codes, (T, H // 2), "codes"),
                     None if scales is None else _bytes(scales, (T, H // 32), "scales"), res_scale, eps, ty, nt)
     rc = lib.coli_moe_block_norm(args, T, H, _on(x, stream))

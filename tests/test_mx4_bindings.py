@@ -140,3 +140,23 @@ def test_weights_are_dense_bytes_on_the_gpu():
             cm.make_mx4_weights(e, s, bad, s)
         with pytest.raises(ValueError, match="shared_scales"):
             cm.make_mx4_weights(e, s, e, bad)
+
+
+# --------------------------------------------------------------------- the types
+def test_ids_weights_and_offsets_have_their_types(calls):
+    f, i = torch.float32, torch.int32
+    w = cm.make_mx4_weights(*records(16), *records(1, inter=384))
+    x, idx, tw, y, ws = layer_args()
+    for bad_idx, bad_w in ((tw, idx), (tw, tw), (idx, idx), (Stand(3, 4, dtype=torch.uint32), tw)):
+        with pytest.raises(TypeError, match="topk_"):
+            cm.coli_mx4_forward(cfg(), w, x, bad_idx, bad_w, y, ws)
+    with pytest.raises(TypeError, match="offsets"):
+        cm.coli_mx4_product(Stand(5, 32), Stand(5, 2), Stand(2, 8, 32), Stand(2, 8, 2), Stand(5, 8, dtype=f), Stand(8704), offsets=Stand(3, dtype=f))
+    h = Stand(3, 64, dtype=f)
+    for kw in (dict(post_w=Stand(64, dtype=i), y=h), dict(pre_w=Stand(64, dtype=i))):
+        with pytest.raises(TypeError, match=next(iter(kw))):
+            cm.coli_moe_block_norm(h, n_out=h, **kw)
+    assert not calls
+    cm.coli_mx4_product(Stand(5, 32), Stand(5, 2), Stand(2, 8, 32), Stand(2, 8, 2), Stand(5, 8, dtype=f), Stand(8704), offsets=Stand(3, dtype=i))
+    cm.coli_moe_block_norm(h, y=h, n_out=h, post_w=Stand(64, dtype=f), pre_w=Stand(64, dtype=f))
+    assert len(calls) == 2
