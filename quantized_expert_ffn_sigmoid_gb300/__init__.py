@@ -69,10 +69,11 @@ class StackLayer(ctypes.Structure):
 
 class Mx4Weights(ctypes.Structure):
     """Four addresses, as in C.  ``make_mx4_weights`` also leaves the bytes behind each of them in
-    ``sizes``, which ``coli_mx4_forward`` compares with the configuration; a struct filled by hand has none."""
+    ``sizes`` and their GPU in ``device``, which ``coli_mx4_forward`` compares with the call; a struct filled
+    by hand has neither."""
     _fields_ = [("experts", ctypes.c_void_p), ("expert_scales", ctypes.c_void_p),
                 ("shared", ctypes.c_void_p), ("shared_scales", ctypes.c_void_p)]
-    sizes = None
+    sizes = device = None
 
 
 class NormArgs(ctypes.Structure):
@@ -291,14 +292,17 @@ def capture_stack_step(layers, xs, residual, topk_idx, topk_w, y, ws, add_output
 # Single-position calls take a few microseconds on the GPU, so these bindings
 # keep their own cost to about that: one look at each tensor, plain integers
 # to ctypes, the raw handle of the current stream.
+#
+# The library launches on the current device, so the tensors of a call are all
+# on that one: anything else is refused here, before their addresses reach it.
 _TYPES = {}
-_raw_stream = _F32 = _I32 = None
+_raw_stream = _raw_device = _F32 = _I32 = None
 
 
 def _torch_names():
-    global _raw_stream, _F32, _I32
+    global _raw_stream, _raw_device, _F32, _I32
     import torch
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _F32, _I32 = torch.float32, torch.int32
     _TYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float16: COLI_F16})
 
@@ -312,46 +316,64 @@ def _type(t) -> int:
     return code
 
 
-def _on(t, stream) -> int:
-    """The stream to enqueue on: the given one, else the current one of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is None:
+def _on(dev: int, stream) -> int:
+    """The stream to enqueue on: the given one, else the current one; either of GPU `dev`, which must be the current device."""
+    if _raw_device is None:
         _torch_names()
-    return _raw_stream(t.get_device())
+    now = _raw_device()
+    if now != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{now}: make theirs current (torch.cuda.device)")
+    if stream is None:
+        return _raw_stream(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
 
 
-def _rows(t, shape, name: str):
-    """The row stride of a GPU tensor of `shape` (two dimensions) whose rows have consecutive elements."""
-    if t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor of shape {tuple(shape)}, not {tuple(t.shape)} on {t.device}")
+def _refuse(t, what: str, shape, name: str, dev: int):
+    gpu = f"GPU tensor on cuda:{dev}" if dev >= 0 else "GPU tensor"
+    raise ValueError(f"{name} must be a {what}{gpu} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, shape, name: str, dev: int):
+    """The row stride of a tensor of `shape` (two dimensions) on GPU `dev` whose rows have consecutive elements."""
+    if t.shape != shape or t.get_device() != dev or dev < 0:
+        _refuse(t, "", shape, name, dev)
     ld, step = t.stride()
     if step != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have consecutive elements in each row")
     return ld if shape[0] > 1 or ld > shape[1] else shape[1]
 
 
-def _bytes(t, shape, name: str) -> int:
-    """The address of a contiguous uint8 GPU tensor of `shape`."""
-    if t.shape != shape or t.element_size() != 1 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous uint8 GPU tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+def _bytes(t, shape, name: str, dev: int) -> int:
+    """The address of a contiguous uint8 tensor of `shape` on GPU `dev`."""
+    if t.shape != shape or t.element_size() != 1 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _refuse(t, "contiguous uint8 ", shape, name, dev)
     return t.data_ptr()
 
 
-def _flat(t, shape, dtype, name: str) -> int:
-    """The address of a contiguous GPU tensor of `shape` and `dtype`."""
+def _flat(t, shape, dtype, name: str, dev: int) -> int:
+    """The address of a contiguous tensor of `shape` and `dtype` on GPU `dev`."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)}, not {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _refuse(t, "contiguous ", shape, name, dev)
     return t.data_ptr()
+
+
+def _space(ws, dev: int):
+    """Address and bytes of a workspace on GPU `dev`."""
+    if ws.get_device() != dev or dev < 0 or not ws.is_contiguous():
+        _refuse(ws, "contiguous ", ws.shape, "ws", dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def coli_mx4_quantize(x, codes, scales, stream=None):
     """MX4 of the rows of x [T, K] (any row stride) into codes [T, K/2] and scales [T, K/32]."""
     T, K = shape = x.shape
-    rc = lib.coli_mx4_quantize(x.data_ptr(), _type(x), _rows(x, shape, "x"), T, K, _bytes(codes, (T, K // 2), "codes"),
-                               _bytes(scales, (T, K // 32), "scales"), _on(x, stream))
+    ty, dev = _type(x), x.get_device()
+    rc = lib.coli_mx4_quantize(x.data_ptr(), ty, _rows(x, shape, "x", dev), T, K, _bytes(codes, (T, K // 2), "codes", dev),
+                               _bytes(scales, (T, K // 32), "scales", dev), _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_quantize")
 
@@ -359,8 +381,9 @@ def coli_mx4_quantize(x, codes, scales, stream=None):
 def coli_mx4_dequantize(codes, scales, out, stream=None):
     """The values of codes [T, K/2] and scales [T, K/32] into out [T, K] (any row stride)."""
     T, K = shape = out.shape
-    rc = lib.coli_mx4_dequantize(_bytes(codes, (T, K // 2), "codes"), _bytes(scales, (T, K // 32), "scales"), T, K,
-                                 out.data_ptr(), _type(out), _rows(out, shape, "out"), _on(out, stream))
+    ty, dev = _type(out), out.get_device()
+    rc = lib.coli_mx4_dequantize(_bytes(codes, (T, K // 2), "codes", dev), _bytes(scales, (T, K // 32), "scales", dev), T, K,
+                                 out.data_ptr(), ty, _rows(out, shape, "out", dev), _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_dequantize")
 
@@ -384,11 +407,11 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
     else:
         G, (N, _) = 1, w_shape
         codes, scales = (N, k2), (N, k2 // 16)
-    yt = _type(y)
-    rc = lib.coli_mx4_product(_bytes(x_codes, shape, "x_codes"), _bytes(x_scales, (P, k2 // 16), "x_scales"), P,
-                              _bytes(w_codes, codes, "w_codes"), _bytes(w_scales, scales, "w_scales"), G, N, 2 * k2,
-                              None if offsets is None else _flat(offsets, (G + 1,), _I32, "offsets"),
-                              y.data_ptr(), yt, _rows(y, (P, N), "y"), ws.data_ptr(), ws.numel(), _on(y, stream))
+    yt, dev = _type(y), y.get_device()
+    rc = lib.coli_mx4_product(_bytes(x_codes, shape, "x_codes", dev), _bytes(x_scales, (P, k2 // 16), "x_scales", dev), P,
+                              _bytes(w_codes, codes, "w_codes", dev), _bytes(w_scales, scales, "w_scales", dev), G, N, 2 * k2,
+                              None if offsets is None else _flat(offsets, (G + 1,), _I32, "offsets", dev),
+                              y.data_ptr(), yt, _rows(y, (P, N), "y", dev), *_space(ws, dev), _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_product")
 
@@ -396,13 +419,13 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
 def make_mx4_weights(experts, expert_scales, shared=None, shared_scales=None) -> Mx4Weights:
     """An MX4 weights struct from contiguous uint8 GPU tensors (keep the tensors alive) that hold exactly
     the records of the configuration they are used with: all experts, or those of its shard."""
-    at, sizes = [], []
+    at, sizes, dev = [], [], experts.get_device()
     for name, t in (("experts", experts), ("expert_scales", expert_scales), ("shared", shared), ("shared_scales", shared_scales)):
         n = 0 if t is None else t.numel()
-        at.append(_bytes(t, t.shape, name) if n else None)
+        at.append(_bytes(t, t.shape, name, dev) if n else None)
         sizes.append(n)
     w = Mx4Weights(*at)
-    w.sizes = tuple(sizes)
+    w.sizes, w.device = tuple(sizes), dev
     return w
 
 
@@ -443,18 +466,20 @@ def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_sca
     T, H = y.shape
     if H != c.hidden:
         raise ValueError(f"y must be [positions, {c.hidden}], not {tuple(y.shape)}")
-    yt = _type(y)
+    yt, dev = _type(y), y.get_device()
     if x_scales is None:
         xt, sp = _type(x), None
-        xp = _flat(x, (T, H), x.dtype, "x")
+        xp = _flat(x, (T, H), x.dtype, "x", dev)
     else:
-        xp, xt, sp = _bytes(x, (T, H // 2), "x"), COLI_MX4, _bytes(x_scales, (T, H // 32), "x_scales")
+        xp, xt, sp = _bytes(x, (T, H // 2), "x", dev), COLI_MX4, _bytes(x_scales, (T, H // 32), "x_scales", dev)
     if weights.sizes is not None:
         _check_records(c, weights.sizes)
+        if weights.device != dev:
+            raise ValueError(f"the weights are on cuda:{weights.device}, y is not on that GPU but on {y.device}")
     k = c.top_k
-    rc = lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, _flat(topk_idx, (T, k), _I32, "topk_idx"),
-                              _flat(topk_w, (T, k), _F32, "topk_w"), _flat(y, (T, H), y.dtype, "y"), yt,
-                              ws.data_ptr(), ws.numel(), _on(y, stream))
+    rc = lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, _flat(topk_idx, (T, k), _I32, "topk_idx", dev),
+                              _flat(topk_w, (T, k), _F32, "topk_w", dev), _flat(y, (T, H), y.dtype, "y", dev), yt,
+                              *_space(ws, dev), _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_forward")
 
@@ -465,33 +490,33 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
     x [T, H]: writes whichever of x_out (may be x), n_out, codes + scales (MX4 of n) are given.
     ``gate`` is [H] or [T, H]."""
     T, H = shape = x.shape
-    dtype, ty = x.dtype, _type(x)
+    dtype, ty, dev = x.dtype, _type(x), x.get_device()
     yp = gp = xp = np = None
     ldy = ldg = ldx = ldn = 0
     nt = ty
     if y is not None:
         if y.dtype is not dtype:
             raise TypeError(f"y must have x's type {dtype}, not {y.dtype}")
-        yp, ldy = y.data_ptr(), _rows(y, shape, "y")
+        yp, ldy = y.data_ptr(), _rows(y, shape, "y", dev)
     if gate is not None:
         if gate.dtype is not dtype:
             raise TypeError(f"gate must have x's type {dtype}, not {gate.dtype}")
         if gate.dim() == 1:
-            gp = _flat(gate, (H,), dtype, "gate")
+            gp = _flat(gate, (H,), dtype, "gate", dev)
         else:
-            gp, ldg = gate.data_ptr(), _rows(gate, shape, "gate")
+            gp, ldg = gate.data_ptr(), _rows(gate, shape, "gate", dev)
     if x_out is not None:
         if x_out.dtype is not dtype:
             raise TypeError(f"x_out must have x's type {dtype}, not {x_out.dtype}")
-        xp, ldx = x_out.data_ptr(), _rows(x_out, shape, "x_out")
+        xp, ldx = x_out.data_ptr(), _rows(x_out, shape, "x_out", dev)
     if n_out is not None:
-        np, ldn = n_out.data_ptr(), _rows(n_out, shape, "n_out")
+        np, ldn = n_out.data_ptr(), _rows(n_out, shape, "n_out", dev)
         if n_out.dtype is not dtype:
             nt = _type(n_out)
-    args = NormArgs(x.data_ptr(), _rows(x, shape, "x"), yp, ldy, gp, ldg, xp, ldx, np, ldn,
-                    None if post_w is None else _flat(post_w, (H,), _F32, "post_w"), None if pre_w is None else _flat(pre_w, (H,), _F32, "pre_w"),
-                    None if codes is None else _bytes(codes, (T, H // 2), "codes"),
-                    None if scales is None else _bytes(scales, (T, H // 32), "scales"), res_scale, eps, ty, nt)
-    rc = lib.coli_moe_block_norm(args, T, H, _on(x, stream))
+    args = NormArgs(x.data_ptr(), _rows(x, shape, "x", dev), yp, ldy, gp, ldg, xp, ldx, np, ldn,
+                    None if post_w is None else _flat(post_w, (H,), _F32, "post_w", dev), None if pre_w is None else _flat(pre_w, (H,), _F32, "pre_w", dev),
+                    None if codes is None else _bytes(codes, (T, H // 2), "codes", dev),
+                    None if scales is None else _bytes(scales, (T, H // 32), "scales", dev), res_scale, eps, ty, nt)
+    rc = lib.coli_moe_block_norm(args, T, H, _on(dev, stream))
     if rc:
         _check(rc, "coli_moe_block_norm")

@@ -74,6 +74,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(cm, "lib", rec)
     cm._torch_names()
     monkeypatch.setattr(cm, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(cm, "_raw_device", lambda: 0, raising=False)
     return rec.calls
 
 
@@ -160,3 +161,90 @@ def test_ids_weights_and_offsets_have_their_types(calls):
     cm.coli_mx4_product(Stand(5, 32), Stand(5, 2), Stand(2, 8, 32), Stand(2, 8, 2), Stand(5, 8, dtype=f), Stand(8704), offsets=Stand(3, dtype=i))
     cm.coli_moe_block_norm(h, y=h, n_out=h, post_w=Stand(64, dtype=f), pre_w=Stand(64, dtype=f))
     assert len(calls) == 2
+
+
+# ------------------------------------------------------------------- the devices
+def every_call(index=0, other=None, at=None):
+    """One valid call of each entry point on GPU `index`; argument `other` of it on GPU `at`."""
+    f = torch.float32
+
+    def place(name, *shape, dtype=torch.uint8):
+        return Stand(*shape, dtype=dtype, index=at if name == other else index)
+
+    def layer(codes):
+        rec = [place(n, *t.shape) for n, t in zip(("experts", "expert_scales", "shared", "shared_scales"), (*records(16), *records(1, inter=384)))]
+        w = cm.make_mx4_weights(*rec)
+        x = place("x", 3, 128) if codes else place("x", 3, 256, dtype=f)
+        cm.coli_mx4_forward(cfg(), w, x, place("topk_idx", 3, 4, dtype=torch.int32), place("topk_w", 3, 4, dtype=f), place("y", 3, 256, dtype=f),
+                            place("ws", 1 << 20), x_scales=place("x_scales", 3, 8) if codes else None)
+
+    def norm():
+        h = lambda n: place(n, 3, 64, dtype=f)  # noqa: E731
+        cm.coli_moe_block_norm(h("x"), y=h("y"), gate=h("gate"), x_out=h("x_out"), n_out=h("n_out"), post_w=place("post_w", 64, dtype=f),
+                               pre_w=place("pre_w", 64, dtype=f), codes=place("codes", 3, 32), scales=place("scales", 3, 2))
+
+    def channel_gate():
+        cm.coli_moe_block_norm(place("x", 3, 64, dtype=f), y=place("y", 3, 64, dtype=f), gate=place("gate", 64, dtype=f),
+                               n_out=place("n_out", 3, 64, dtype=f))
+
+    return {
+        "quantize": (("x", "codes", "scales"),
+                     lambda: cm.coli_mx4_quantize(place("x", 3, 64, dtype=f), place("codes", 3, 32), place("scales", 3, 2))),
+        "dequantize": (("codes", "scales", "out"),
+                       lambda: cm.coli_mx4_dequantize(place("codes", 3, 32), place("scales", 3, 2), place("out", 3, 64, dtype=f))),
+        "product": (("x_codes", "x_scales", "w_codes", "w_scales", "y", "ws", "offsets"),
+                    lambda: cm.coli_mx4_product(place("x_codes", 5, 32), place("x_scales", 5, 2), place("w_codes", 2, 8, 32),
+                                                place("w_scales", 2, 8, 2), place("y", 5, 8, dtype=f), place("ws", 8704),
+                                                offsets=place("offsets", 3, dtype=torch.int32))),
+        "layer": (("experts", "expert_scales", "shared", "shared_scales", "x", "topk_idx", "topk_w", "y", "ws"), lambda: layer(False)),
+        "layer of codes": (("x", "x_scales"), lambda: layer(True)),
+        "norm": (("x", "y", "gate", "x_out", "n_out", "post_w", "pre_w", "codes", "scales"), norm),
+        "norm, channel gate": (("gate",), channel_gate),
+    }
+
+
+ARGUMENTS = [(call, name) for call, (names, _) in every_call().items() for name in names]
+
+
+@pytest.mark.parametrize("at", [1, -1])
+@pytest.mark.parametrize("call,name", ARGUMENTS)
+def test_every_argument_is_on_the_same_gpu(calls, monkeypatch, call, name, at):
+    monkeypatch.setattr(cm, "_raw_device", lambda: 0, raising=False)
+    every_call()[call][1]()
+    assert len(calls) == 1
+    with pytest.raises(ValueError, match="GPU"):
+        every_call(other=name, at=at)[call][1]()
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("call", list(every_call()))
+def test_the_tensors_gpu_is_the_current_one(calls, monkeypatch, call):
+    monkeypatch.setattr(cm, "_raw_device", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="current"):
+        every_call(index=1)[call][1]()
+    assert not calls
+    monkeypatch.setattr(cm, "_raw_device", lambda: 1, raising=False)
+    every_call(index=1)[call][1]()
+    assert len(calls) == 1
+
+
+def test_a_given_stream_is_of_the_same_gpu(calls, monkeypatch):
+    monkeypatch.setattr(cm, "_raw_device", lambda: 0, raising=False)
+    args = Stand(3, 64, dtype=torch.float32), Stand(3, 32), Stand(3, 2)
+    with pytest.raises(ValueError, match="stream"):
+        cm.coli_mx4_quantize(*args, stream=types.SimpleNamespace(cuda_stream=7, device_index=1))
+    assert not calls
+    cm.coli_mx4_quantize(*args, stream=types.SimpleNamespace(cuda_stream=7, device_index=0))
+    cm.coli_mx4_quantize(*args, stream=types.SimpleNamespace(cuda_stream=7))
+    assert len(calls) == 2
+
+
+def test_workspaces_are_dense(calls, monkeypatch):
+    monkeypatch.setattr(cm, "_raw_device", lambda: 0, raising=False)
+    sparse = Stand(8704, strides=(2,))
+    with pytest.raises(ValueError, match="ws"):
+        cm.coli_mx4_product(Stand(5, 32), Stand(5, 2), Stand(8, 32), Stand(8, 2), Stand(5, 8, dtype=torch.float32), sparse)
+    w = cm.make_mx4_weights(*records(16), *records(1, inter=384))
+    with pytest.raises(ValueError, match="ws"):
+        cm.coli_mx4_forward(cfg(), w, *layer_args()[:4], sparse)
+    assert not calls
