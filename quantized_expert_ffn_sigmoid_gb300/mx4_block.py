@@ -54,8 +54,9 @@ class Stack:
         self.codes = torch.empty(T, H // 2, dtype=torch.uint8, device=dev)
         self.scales = torch.empty(T, H // 32, dtype=torch.uint8, device=dev)
         self.y = torch.empty(T, H, dtype=dtype, device=dev)
-        self.idx = torch.empty(len(self.blocks), T, k, dtype=torch.int32, device=dev)
-        self.w = torch.empty(len(self.blocks), T, k, device=dev)
+        # an allocation each: the library wants its arrays 16-byte aligned, which slices of T * k words need not be
+        self.idx = [torch.empty(T, k, dtype=torch.int32, device=dev) for _ in self.blocks]
+        self.w = [torch.empty(T, k, device=dev) for _ in self.blocks]
         size = max(cm.coli_mx4_workspace_size(b.cfg, T) for b in self.blocks)
         if size == 0 or any(b.cfg.hidden != H or b.cfg.top_k != k for b in self.blocks):
             raise ValueError("blocks of one hidden size and top_k, within the layer's limits")
