@@ -42,12 +42,15 @@ class Block:
 
 class Stack:
     """Blocks run one after the other on the residual stream ``x`` [positions, hidden] (float32,
-    bfloat16 or float16), in place.  All buffers are allocated here, once."""
+    bfloat16 or float16), in place.  All buffers are allocated here, once.  The layers are whole:
+    shards of an expert-parallel layer are refused, since nothing here sums their parts."""
 
     def __init__(self, blocks, pre_w, positions: int, dtype, eps: float = 1e-6):
         import torch
         self.blocks, self.pre_w, self.eps = list(blocks), pre_w, eps
         cfg = self.blocks[0].cfg
+        if any(b.cfg.ep_size > 1 for b in self.blocks):
+            raise ValueError("whole layers, no expert-parallel shards: a shard's y is a part of the sum that the norm behind it needs")
         dev, H, T, k = pre_w.device, cfg.hidden, positions, max(b.cfg.top_k for b in self.blocks)
         self.x = torch.empty(T, H, dtype=dtype, device=dev)
         self.norm = torch.empty(T, H, device=dev)                       # the router reads float32
