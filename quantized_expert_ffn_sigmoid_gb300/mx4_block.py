@@ -51,7 +51,10 @@ class Stack:
         cfg = self.blocks[0].cfg
         if any(b.cfg.ep_size > 1 for b in self.blocks):
             raise ValueError("whole layers, no expert-parallel shards: a shard's y is a part of the sum that the norm behind it needs")
-        dev, H, T, k = pre_w.device, cfg.hidden, positions, max(b.cfg.top_k for b in self.blocks)
+        dev, H, T, k = pre_w.device, cfg.hidden, positions, cfg.top_k
+        sizes = [cm.coli_mx4_workspace_size(b.cfg, T) for b in self.blocks]   # 0: outside the layer's limits
+        if 0 in sizes or any(b.cfg.hidden != H or b.cfg.top_k != k for b in self.blocks):
+            raise ValueError("blocks of one hidden size and top_k, within the layer's limits")
         self.x = torch.empty(T, H, dtype=dtype, device=dev)
         self.norm = torch.empty(T, H, device=dev)                       # the router reads float32
         self.codes = torch.empty(T, H // 2, dtype=torch.uint8, device=dev)
@@ -60,10 +63,7 @@ class Stack:
         # an allocation each: the library wants its arrays 16-byte aligned, which slices of T * k words need not be
         self.idx = [torch.empty(T, k, dtype=torch.int32, device=dev) for _ in self.blocks]
         self.w = [torch.empty(T, k, device=dev) for _ in self.blocks]
-        size = max(cm.coli_mx4_workspace_size(b.cfg, T) for b in self.blocks)
-        if size == 0 or any(b.cfg.hidden != H or b.cfg.top_k != k for b in self.blocks):
-            raise ValueError("blocks of one hidden size and top_k, within the layer's limits")
-        self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        self.ws = torch.empty(max(sizes), dtype=torch.uint8, device=dev)
         cm.coli_moe_workspace_init(self.ws)
         self._weights = [b.weights() for b in self.blocks]
 

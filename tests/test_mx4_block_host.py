@@ -19,3 +19,9 @@ def test_shards_are_refused(rank, size):
     # a shard's layer leaves its part of y, which the norm behind it must not be given
     with pytest.raises(ValueError, match="shard"):
         mx4_block.Stack([block(), block(ep_rank=rank, ep_size=size)], torch.ones(256), 3, torch.float32)
+
+
+@pytest.mark.parametrize("kw", [dict(hidden=128), dict(top_k=3), dict(weight_bits=8)])
+def test_blocks_that_do_not_fit_are_refused(kw):
+    with pytest.raises(ValueError, match="blocks"):
+        mx4_block.Stack([block(), block(**kw)], torch.ones(256), 3, torch.float32)
