@@ -69,11 +69,11 @@ class StackLayer(ctypes.Structure):
 
 class Mx4Weights(ctypes.Structure):
     """Four addresses, as in C.  ``make_mx4_weights`` also leaves the bytes behind each of them in
-    ``sizes`` and their GPU in ``device``, which ``coli_mx4_forward`` compares with the call; a struct filled
-    by hand has neither."""
+    ``sizes`` and their GPU in ``device``, which ``coli_mx4_forward`` compares with the call, and holds the
+    tensors; a struct filled by hand has none of these."""
     _fields_ = [("experts", ctypes.c_void_p), ("expert_scales", ctypes.c_void_p),
                 ("shared", ctypes.c_void_p), ("shared_scales", ctypes.c_void_p)]
-    sizes = device = None
+    sizes = device = tensors = None
 
 
 class NormArgs(ctypes.Structure):
@@ -417,15 +417,15 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
 
 
 def make_mx4_weights(experts, expert_scales, shared=None, shared_scales=None) -> Mx4Weights:
-    """An MX4 weights struct from contiguous uint8 GPU tensors (keep the tensors alive) that hold exactly
-    the records of the configuration they are used with: all experts, or those of its shard."""
+    """An MX4 weights struct from contiguous uint8 GPU tensors that hold exactly the records of the
+    configuration they are used with: all experts, or those of its shard.  It keeps the tensors alive."""
     at, sizes, dev = [], [], experts.get_device()
     for name, t in (("experts", experts), ("expert_scales", expert_scales), ("shared", shared), ("shared_scales", shared_scales)):
         n = 0 if t is None else t.numel()
         at.append(_bytes(t, t.shape, name, dev) if n else None)
         sizes.append(n)
     w = Mx4Weights(*at)
-    w.sizes, w.device = tuple(sizes), dev
+    w.sizes, w.device, w.tensors = tuple(sizes), dev, (experts, expert_scales, shared, shared_scales)
     return w
 
 

@@ -1,7 +1,9 @@
 """The MX4 bindings look at every tensor before the library is called.  No GPU:
 stand-ins answer what the bindings ask of a tensor, and a recorder takes the
 library's place, so nothing is launched whatever passes."""
+import gc
 import types
+import weakref
 
 import pytest
 
@@ -141,6 +143,18 @@ def test_weights_are_dense_bytes_on_the_gpu():
             cm.make_mx4_weights(e, s, bad, s)
         with pytest.raises(ValueError, match="shared_scales"):
             cm.make_mx4_weights(e, s, e, bad)
+
+
+def test_the_struct_keeps_its_tensors_alive():
+    e, s = records(16)
+    seen = [weakref.ref(t) for t in (e, s)]
+    w = cm.make_mx4_weights(e, s)
+    del e, s
+    gc.collect()
+    assert all(r() is not None for r in seen)
+    del w
+    gc.collect()
+    assert all(r() is None for r in seen)
 
 
 # --------------------------------------------------------------------- the types
