@@ -318,11 +318,12 @@ def _type(t) -> int:
 
 def _on(dev: int, stream) -> int:
     """The stream to enqueue on: the given one, else the current one; either of GPU `dev`, which must be the current device."""
+    if dev < 0:
+        raise ValueError("the tensors must be GPU tensors")
     if _raw_device is None:
         _torch_names()
-    now = _raw_device()
-    if now != dev:
-        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{now}: make theirs current (torch.cuda.device)")
+    if _raw_device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_raw_device()}: make theirs current (torch.cuda.device)")
     if stream is None:
         return _raw_stream(dev)
     if getattr(stream, "device_index", dev) != dev:
@@ -331,48 +332,55 @@ def _on(dev: int, stream) -> int:
 
 
 def _refuse(t, what: str, shape, name: str, dev: int):
-    gpu = f"GPU tensor on cuda:{dev}" if dev >= 0 else "GPU tensor"
-    raise ValueError(f"{name} must be a {what}{gpu} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    if dev < 0:
+        raise ValueError("the tensors must be GPU tensors")
+    raise ValueError(f"{name} must be a {what}GPU tensor on cuda:{dev} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rows(t, shape, name: str, dev: int):
-    """The row stride of a tensor of `shape` (two dimensions) on GPU `dev` whose rows have consecutive elements."""
-    if t.shape != shape or t.get_device() != dev or dev < 0:
-        _refuse(t, "", shape, name, dev)
+def _pitch(t, shape, name: str):
+    """The row stride of a tensor of two dimensions whose rows have consecutive elements."""
     ld, step = t.stride()
     if step != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have consecutive elements in each row")
     return ld if shape[0] > 1 or ld > shape[1] else shape[1]
 
 
+# `dev` is the device of the tensor that gives a call its shape; _on looks at it last.
+def _rows(t, shape, name: str, dev: int):
+    """The row stride of a tensor of `shape` (two dimensions) on `dev`."""
+    if t.shape != shape or t.get_device() != dev:
+        _refuse(t, "", shape, name, dev)
+    return _pitch(t, shape, name)
+
+
 def _bytes(t, shape, name: str, dev: int) -> int:
-    """The address of a contiguous uint8 tensor of `shape` on GPU `dev`."""
-    if t.shape != shape or t.element_size() != 1 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+    """The address of a contiguous uint8 tensor of `shape` on `dev`."""
+    if t.shape != shape or t.element_size() != 1 or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, "contiguous uint8 ", shape, name, dev)
     return t.data_ptr()
 
 
 def _flat(t, shape, dtype, name: str, dev: int) -> int:
-    """The address of a contiguous tensor of `shape` and `dtype` on GPU `dev`."""
+    """The address of a contiguous tensor of `shape` and `dtype` on `dev`."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, "contiguous ", shape, name, dev)
     return t.data_ptr()
 
 
 def _space(ws, dev: int):
-    """Address and bytes of a workspace on GPU `dev`."""
-    if ws.get_device() != dev or dev < 0 or not ws.is_contiguous():
+    """Address and bytes of a workspace on `dev`."""
+    if ws.get_device() != dev or not ws.is_contiguous():
         _refuse(ws, "contiguous ", ws.shape, "ws", dev)
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def coli_mx4_quantize(x, codes, scales, stream=None):
     """MX4 of the rows of x [T, K] (any row stride) into codes [T, K/2] and scales [T, K/32]."""
     T, K = shape = x.shape
     ty, dev = _type(x), x.get_device()
-    rc = lib.coli_mx4_quantize(x.data_ptr(), ty, _rows(x, shape, "x", dev), T, K, _bytes(codes, (T, K // 2), "codes", dev),
+    rc = lib.coli_mx4_quantize(x.data_ptr(), ty, _pitch(x, shape, "x"), T, K, _bytes(codes, (T, K // 2), "codes", dev),
                                _bytes(scales, (T, K // 32), "scales", dev), _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_quantize")
@@ -383,7 +391,7 @@ def coli_mx4_dequantize(codes, scales, out, stream=None):
     T, K = shape = out.shape
     ty, dev = _type(out), out.get_device()
     rc = lib.coli_mx4_dequantize(_bytes(codes, (T, K // 2), "codes", dev), _bytes(scales, (T, K // 32), "scales", dev), T, K,
-                                 out.data_ptr(), ty, _rows(out, shape, "out", dev), _on(dev, stream))
+                                 out.data_ptr(), ty, _pitch(out, shape, "out"), _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_dequantize")
 
@@ -408,10 +416,13 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
         G, (N, _) = 1, w_shape
         codes, scales = (N, k2), (N, k2 // 16)
     yt, dev = _type(y), y.get_device()
+    if y.shape != (P, N):
+        _refuse(y, "", (P, N), "y", dev)
+    wp, wn = _space(ws, dev)
     rc = lib.coli_mx4_product(_bytes(x_codes, shape, "x_codes", dev), _bytes(x_scales, (P, k2 // 16), "x_scales", dev), P,
                               _bytes(w_codes, codes, "w_codes", dev), _bytes(w_scales, scales, "w_scales", dev), G, N, 2 * k2,
                               None if offsets is None else _flat(offsets, (G + 1,), _I32, "offsets", dev),
-                              y.data_ptr(), yt, _rows(y, (P, N), "y", dev), *_space(ws, dev), _on(dev, stream))
+                              y.data_ptr(), yt, _pitch(y, (P, N), "y"), wp, wn, _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_product")
 
@@ -420,6 +431,8 @@ def make_mx4_weights(experts, expert_scales, shared=None, shared_scales=None) ->
     """An MX4 weights struct from contiguous uint8 GPU tensors that hold exactly the records of the
     configuration they are used with: all experts, or those of its shard.  It keeps the tensors alive."""
     at, sizes, dev = [], [], experts.get_device()
+    if dev < 0:
+        raise ValueError(f"experts must be a contiguous uint8 GPU tensor, not on {experts.device}")
     for name, t in (("experts", experts), ("expert_scales", expert_scales), ("shared", shared), ("shared_scales", shared_scales)):
         n = 0 if t is None else t.numel()
         at.append(_bytes(t, t.shape, name, dev) if n else None)
@@ -466,6 +479,8 @@ def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_sca
     T, H = y.shape
     if H != c.hidden:
         raise ValueError(f"y must be [positions, {c.hidden}], not {tuple(y.shape)}")
+    if not y.is_contiguous():
+        raise ValueError("y must be contiguous")
     yt, dev = _type(y), y.get_device()
     if x_scales is None:
         xt, sp = _type(x), None
@@ -477,9 +492,10 @@ def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_sca
         if weights.device != dev:
             raise ValueError(f"the weights are on cuda:{weights.device}, y is not on that GPU but on {y.device}")
     k = c.top_k
+    wp, wn = _space(ws, dev)
     rc = lib.coli_mx4_forward(ctypes.byref(c), ctypes.byref(weights), xp, xt, sp, T, _flat(topk_idx, (T, k), _I32, "topk_idx", dev),
-                              _flat(topk_w, (T, k), _F32, "topk_w", dev), _flat(y, (T, H), y.dtype, "y", dev), yt,
-                              *_space(ws, dev), _on(dev, stream))
+                              _flat(topk_w, (T, k), _F32, "topk_w", dev), y.data_ptr(), yt,
+                              wp, wn, _on(dev, stream))
     if rc:
         _check(rc, "coli_mx4_forward")
 
@@ -513,7 +529,7 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
         np, ldn = n_out.data_ptr(), _rows(n_out, shape, "n_out", dev)
         if n_out.dtype is not dtype:
             nt = _type(n_out)
-    args = NormArgs(x.data_ptr(), _rows(x, shape, "x", dev), yp, ldy, gp, ldg, xp, ldx, np, ldn,
+    args = NormArgs(x.data_ptr(), _pitch(x, shape, "x"), yp, ldy, gp, ldg, xp, ldx, np, ldn,
                     None if post_w is None else _flat(post_w, (H,), _F32, "post_w", dev), None if pre_w is None else _flat(pre_w, (H,), _F32, "pre_w", dev),
                     None if codes is None else _bytes(codes, (T, H // 2), "codes", dev),
                     None if scales is None else _bytes(scales, (T, H // 32), "scales", dev), res_scale, eps, ty, nt)
