@@ -6,9 +6,15 @@
 // neighbouring lanes and its maximum two shuffles; a warp takes 2048
 // consecutive elements of one row, all loads of every lane in flight before
 // the first use.  8192 x 6144 bf16 there and back take 43.7 us (45.4 with
-// 1024 elements a warp, 50.3 with 512).  Calls too small to give every SM 64
-// such warps take 512 a warp: the shorter chain (one row of 6144 there and
-// back: 2.8 us against 3.7).
+// 1024 elements a warp, 50.2 with 512).  Two kinds of calls take 512 a warp:
+//   few       fewer than 32 long warps for every SM, where the shorter chain
+//             counts (6144 bf16 there and back, short and long warps: one row
+//             2.5 and 3.6 us, 1280 rows 10.6 and 11.4, 1792 rows 13.6 both,
+//             2432 rows 17.1 and 16.0)
+//   ragged    rows that would leave over a quarter of the long warps empty
+//             (52 M elements, short and long: K = 512 52 and 110 us, 1024 52
+//             and 66, 2560 52 and 58, 4128 56.5 both; but 1536 52.3 and 51.8,
+//             5120 52.2 and 49.5, 6176 55.1 and 53.2)
 #include "mx4_common.cuh"
 
 namespace {
@@ -92,7 +98,10 @@ unsigned grid_for(long long rows, int K, int units) {
   return (unsigned)(blocks < 0x7fffffffLL ? blocks : 0x7fffffffLL);
 }
 constexpr int FEW = 2, MANY = 8;  // units per lane
-bool many(long long rows, int K) { return rows * ((K + 256 * MANY - 1) / (256 * MANY)) >= 64LL * device_sms(); }
+bool many(long long rows, int K) {
+  const long long per_row = (K + 256 * MANY - 1) / (256 * MANY);
+  return rows * per_row >= 32LL * device_sms() && 4LL * K >= 3 * per_row * (256 * MANY);
+}
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
