@@ -237,10 +237,12 @@ __global__ void __launch_bounds__(256) mx4_prep_small(const coli_moe_cfg c, cons
 }
 
 // y[t] = sum_j w[t][j] o[row(t, j)] + sum_s o[shared row of t], in this order.
-// B rows' loads in flight per thread: 12 where there are few threads and one
-// round trip to L2 is what counts (one position: 39.8 us a layer call, 40.6
-// with 8), 3 where HBM is, so that the registers leave room for threads (2048
-// positions: 983 us, 1008 with 8, 1065 with 12).
+// B rows' loads in flight per thread: 12 up to two CTAs an SM, where one round
+// trip to L2 is what counts, 3 beyond, where bandwidth is and the registers
+// have to leave room for threads.  Layer calls of 8 experts and a shared one,
+// inter 128, with 12 and with 3: 48 CTAs 24.9 and 26.1 us, 128 26.1 and 27.3,
+// 256 30.9 and 32.0, 288 34.4 and 34.3, 384 36.8 and 35.8, 768 47.6 and 43.6,
+// 3072 100.5 and 82.0.
 template <int B>
 __global__ void __launch_bounds__(256) mx4_combine(const coli_moe_cfg c, const Mx4Layout L, const uint8_t* __restrict__ ws, int T,
                                                    const float* __restrict__ topk_w, void* __restrict__ y, int32_t y_type) {
@@ -309,7 +311,7 @@ cudaError_t launch_mx4_combine(const coli_moe_cfg& c, const Mx4Layout& L, const 
                                int32_t y_type, cudaStream_t st) {
   const long long blocks = ((long long)T * (c.hidden / 4) + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return blocks <= 4LL * device_sms() ? launch_pdl(mx4_combine<12>, (unsigned)blocks, 256, 0, st, c, L, ws, T, topk_w, y, y_type)
+  return blocks <= 2LL * device_sms() ? launch_pdl(mx4_combine<12>, (unsigned)blocks, 256, 0, st, c, L, ws, T, topk_w, y, y_type)
                                       : launch_pdl(mx4_combine<3>, (unsigned)blocks, 256, 0, st, c, L, ws, T, topk_w, y, y_type);
 }
 
