@@ -334,8 +334,9 @@ int coli_moe_forward_dump(const coli_moe_cfg* cfg, const coli_moe_weights* weigh
  * and saturated at 6.  A block holding an infinity or NaN gets b = 255 and
  * codes 0.
  *   x       [T] rows of K values of x_type (COLI_F32, _BF16, _F16), row t at
- *           element t * ldx; any ldx >= K (16-byte aligned rows are read in
- *           16-byte pieces, others value by value)
+ *           element t * ldx; any ldx >= K (rows that stay 16-byte aligned are
+ *           read in 16-byte pieces, others value by value; x itself is 16-byte
+ *           aligned like every pointer here)
  *   codes   [T][K/2] out;  scales [T][K/32] out
  * K % 32 == 0 (COLI_EINVAL otherwise).  T == 0 is a no-op. */
 int coli_mx4_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t T, int32_t K,
@@ -385,7 +386,9 @@ size_t coli_mx4_workspace_size(const coli_moe_cfg* cfg, int32_t max_T);
  *     o = Wd hq;  y[t] = sum_j topk_w[t][j] * o[t,j] + sum_s o_shared_s[t]
  * with fp32 accumulation, fp32 silu and a combine in fixed order.  cfg as for
  * coli_moe_forward with weight_bits 4 and group_size 0 (COLI_EINVAL
- * otherwise); expert-parallel shards as there.
+ * otherwise) and with its limits (hidden, inter and shared_inter multiples of
+ * 128, hidden up to 32768, inter and shared_inter up to 16384, 1024 experts,
+ * 32 slots, 8 shared experts); expert-parallel shards as there.
  *   x         [T][H] of x_type, or codes [T][H/2] with x_type COLI_MX4 and
  *             x_scales [T][H/32] (NULL otherwise)
  *   topk_idx  [T][k] int32 (-1: slot skipped);  topk_w [T][k] fp32
@@ -409,8 +412,9 @@ int coli_mx4_forward(const coli_moe_cfg* cfg, const coli_mx4_weights* weights,
  *   x_out   [T][H] of `type` (may be x itself), n_out [T][H] of n_type
  *           (`type` or COLI_F32), codes [T][H/2] with scales [T][H/32]
  *           (H % 32 == 0); each may be NULL, not all of them.
- * Any H from 1 to COLI_NORM_MAX_H and any strides; H % 8 == 0 with 16-byte
- * aligned rows is read in 16-byte pieces.  T == 0 is a no-op. */
+ * Any H from 1 to COLI_NORM_MAX_H and any strides; H % 8 == 0 with rows that
+ * stay 16-byte aligned is read in 16-byte pieces (the pointers themselves are
+ * 16-byte aligned).  T == 0 is a no-op. */
 #define COLI_NORM_MAX_H 16384
 typedef struct coli_moe_norm_args {
     const void*  x;       int64_t ldx;

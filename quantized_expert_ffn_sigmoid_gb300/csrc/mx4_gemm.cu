@@ -42,16 +42,17 @@
 //               of both latencies (1650 cycles).
 // Two accumulators, so a tile's epilogue overlaps the next tile's products.
 //
-// Bounds and measurements (one GB300; 6.68 TB/s copy and 1920 TFLOP/s bf16
-// measured there).  The layer of 256 experts, 6144 x 2048, 8 of them and a
-// shared one per position, streams its experts: 32 positions 471 us, 7.0 TB/s
-// of weights; 4 positions 102 us, 6.2 TB/s; one position 39.9 us, of which 27
+// Bounds and measurements (GB300; 6.68 TB/s copy and 1920 TFLOP/s bf16
+// measured; a range is what several of them gave).  The layer of 256 experts,
+// 6144 x 2048, 8 of them and a shared one per position, streams its experts:
+// 32 positions 463-487 us, 6.8 to 7.1 TB/s of weights; 4 positions 97-104 us,
+// 6.1 to 6.5 TB/s; one position 39-41 us, of which 27
 // are the weights' and the rest the dispatch and combine launches, the first
-// tile's latency and the end of the down items; 2048 positions 983 us, 779 for
+// tile's latency and the end of the down items; 2048 positions 985-1005 us, 779 for
 // the weights and 136 for o, which is written and read once.  Products of 8192
-// x 4096 x 6144: 103 us, 4.0 PFLOP/s; a stage takes 1100 cycles, of which the
+// x 4096 x 6144: 102-105 us, 4.0 PFLOP/s; a stage takes 1100 cycles, of which the
 // instructions 640, the rest the time until its 68 KB have arrived, which
-// three stages do not cover.  4096 rows over 32 groups, 4096 x 6144: 90 us,
+// three stages do not cover.  4096 rows over 32 groups, 4096 x 6144: 90-92 us,
 // 5.3 TB/s.
 // Every wait is bounded; an expired one sets COLI_STATUS_TIMEOUT and the rest
 // of the launch drains.
@@ -771,8 +772,8 @@ bool encode_bytes(CUtensorMap* m, const void* base, size_t row_bytes, size_t row
 // The tile for at most `most` activation rows per entry: the smallest that
 // holds them, up to 128, with as many stages as fit.  Wide tiles read a weight
 // once for more rows although entries may hold fewer on average: 2048
-// positions over 256 experts (64 rows each) take 1009 us with 128, 1161 with
-// 64; 4096 rows over 32 groups 91 us with 128, 124 with 64.
+// positions over 256 experts (64 rows each) take 990 us with 128, 1143 with
+// 64; 4096 rows over 32 groups 90 us with 128, 121 with 64.
 Mx4Tile tile_for(int most, int entries) {
   Mx4Tile T;
   T.n = most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : 128;
