@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(256) mx4_prep_small(const coli_moe_cfg c, cons
 // have to leave room for threads.  Layer calls of 8 experts and a shared one,
 // inter 128, with 12 and with 3: 48 CTAs 24.9 and 26.1 us, 128 26.1 and 27.3,
 // 256 30.9 and 32.0, 288 34.4 and 34.3, 384 36.8 and 35.8, 768 47.6 and 43.6,
-// 3072 100.5 and 82.0.
+// 1536 61.1 and 53.7.
 template <int B>
 __global__ void __launch_bounds__(256) mx4_combine(const coli_moe_cfg c, const Mx4Layout L, const uint8_t* __restrict__ ws, int T,
                                                    const float* __restrict__ topk_w, void* __restrict__ y, int32_t y_type) {
