@@ -337,6 +337,10 @@ def _refuse(t, what: str, shape, name: str, dev: int):
     raise ValueError(f"{name} must be a {what}GPU tensor on cuda:{dev} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _beyond(*sizes):
+    raise ValueError(f"sizes beyond 32 bits: {sizes}")
+
+
 def _pitch(t, shape, name: str):
     """The row stride of a tensor of two dimensions whose rows have consecutive elements."""
     ld, step = t.stride()
@@ -379,6 +383,8 @@ def _space(ws, dev: int):
 def coli_mx4_quantize(x, codes, scales, stream=None):
     """MX4 of the rows of x [T, K] (any row stride) into codes [T, K/2] and scales [T, K/32]."""
     T, K = shape = x.shape
+    if (T | K) >> 31:
+        _beyond(T, K)
     ty, dev = _type(x), x.get_device()
     rc = lib.coli_mx4_quantize(x.data_ptr(), ty, _pitch(x, shape, "x"), T, K, _bytes(codes, (T, K // 2), "codes", dev),
                                _bytes(scales, (T, K // 32), "scales", dev), _on(dev, stream))
@@ -389,6 +395,8 @@ def coli_mx4_quantize(x, codes, scales, stream=None):
 def coli_mx4_dequantize(codes, scales, out, stream=None):
     """The values of codes [T, K/2] and scales [T, K/32] into out [T, K] (any row stride)."""
     T, K = shape = out.shape
+    if (T | K) >> 31:
+        _beyond(T, K)
     ty, dev = _type(out), out.get_device()
     rc = lib.coli_mx4_dequantize(_bytes(codes, (T, K // 2), "codes", dev), _bytes(scales, (T, K // 32), "scales", dev), T, K,
                                  out.data_ptr(), ty, _pitch(out, shape, "out"), _on(dev, stream))
@@ -415,6 +423,8 @@ def coli_mx4_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, 
     else:
         G, (N, _) = 1, w_shape
         codes, scales = (N, k2), (N, k2 // 16)
+    if (P | G | N | 2 * k2) >> 31:
+        _beyond(P, G, N, 2 * k2)
     yt, dev = _type(y), y.get_device()
     if y.shape != (P, N):
         _refuse(y, "", (P, N), "y", dev)
@@ -459,6 +469,8 @@ def _check_records(c, sizes):
 
 
 def coli_mx4_workspace_size(cfg, max_T: int) -> int:
+    if max_T >> 31 > 0:
+        _beyond(max_T)
     return int(lib.coli_mx4_workspace_size(ctypes.byref(_cfg(cfg)), int(max_T)))
 
 
@@ -479,6 +491,8 @@ def coli_mx4_forward(cfg, weights: Mx4Weights, x, topk_idx, topk_w, y, ws, x_sca
     T, H = y.shape
     if H != c.hidden:
         raise ValueError(f"y must be [positions, {c.hidden}], not {tuple(y.shape)}")
+    if T >> 31:
+        _beyond(T)
     if not y.is_contiguous():
         raise ValueError("y must be contiguous")
     yt, dev = _type(y), y.get_device()
@@ -506,6 +520,8 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
     x [T, H]: writes whichever of x_out (may be x), n_out, codes + scales (MX4 of n) are given.
     ``gate`` is [H] or [T, H]."""
     T, H = shape = x.shape
+    if (T | H) >> 31:
+        _beyond(T, H)
     dtype, ty, dev = x.dtype, _type(x), x.get_device()
     yp = gp = xp = np = None
     ldy = ldg = ldx = ldn = 0

@@ -262,3 +262,29 @@ def test_workspaces_are_dense(calls, monkeypatch):
     with pytest.raises(ValueError, match="ws"):
         cm.coli_mx4_forward(cfg(), w, *layer_args()[:4], sparse)
     assert not calls
+
+
+# --------------------------------------------------------------------- the sizes
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 64])
+def test_sizes_beyond_32_bits_are_refused(calls, n):
+    # the library counts rows and values in int32: a larger size must not arrive there as its low half
+    f, u = torch.float32, lambda *s: Stand(*s)
+    w = cm.make_mx4_weights(*records(16), *records(1, inter=384))
+    x, idx, tw, y, ws = layer_args(T=n)
+    for call in (lambda: cm.coli_mx4_quantize(Stand(1, n, dtype=f), u(1, n // 2), u(1, n // 32)),
+                 lambda: cm.coli_mx4_quantize(Stand(n, 32, dtype=f), u(n, 16), u(n, 1)),
+                 lambda: cm.coli_mx4_dequantize(u(1, n // 2), u(1, n // 32), Stand(1, n, dtype=f)),
+                 lambda: cm.coli_mx4_dequantize(u(n, 16), u(n, 1), Stand(n, 32, dtype=f)),
+                 lambda: cm.coli_mx4_product(u(n, 16), u(n, 1), u(8, 16), u(8, 1), Stand(n, 8, dtype=f), u(8704)),
+                 lambda: cm.coli_mx4_product(u(1, 16), u(1, 1), u(n, 16), u(n, 1), Stand(1, n, dtype=f), u(8704)),
+                 lambda: cm.coli_mx4_product(u(1, n // 2), u(1, n // 32), u(8, n // 2), u(8, n // 32), Stand(1, 8, dtype=f), u(8704)),
+                 lambda: cm.coli_mx4_product(u(1, 16), u(1, 1), u(n, 1, 16), u(n, 1, 1), Stand(1, 1, dtype=f), u(8704),
+                                             offsets=Stand(n + 1, dtype=torch.int32)),
+                 lambda: cm.coli_mx4_forward(cfg(), w, x, idx, tw, y, ws),
+                 lambda: cm.coli_moe_block_norm(Stand(n, 1, dtype=f), n_out=Stand(n, 1, dtype=f)),
+                 lambda: cm.coli_moe_block_norm(Stand(1, n, dtype=f), n_out=Stand(1, n, dtype=f))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    with pytest.raises(ValueError, match="32 bits"):
+        cm.coli_mx4_workspace_size(cfg(), n)
+    assert not calls
