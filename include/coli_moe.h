@@ -433,6 +433,163 @@ typedef struct coli_moe_norm_args {
 } coli_moe_norm_args;
 int coli_moe_block_norm(const coli_moe_norm_args* args, int32_t T, int32_t H, cudaStream_t stream);
 
+/* ---- 8-bit codes with a scale for each token and each channel --------------
+ * The int8 container of the expert records above (int8 codes and one fp32 scale
+ * per output row: colibri v1.0 README, "What's implemented") against activations
+ * that carry one scale per position, and the steps between a router's logits and
+ * the layer's output, each on its own: selection of experts, grouping of the
+ * routed pairs, codes of activations, products, weighted sum.  Together they
+ * are the expert layer for activations quantised per token. */
+
+/* Selection of experts from scores ("How it works (validated core mechanics)"
+ * of the GLM-5.2 write-up, as for coli_moe_route, and the variants of other
+ * families):
+ *     s = softmax(l) over all experts, or sigmoid(l);   v = s + bias
+ *     the topk_group best groups stay: by the sum of their two best v, or by
+ *     their best (ties to the lower group)
+ *     topk_idx = the top_k best v of them, descending (ties to the lower id)
+ *     topk_w = s of these, with renorm divided by their sum, times scaling
+ * Without a bias the logits themselves rank the experts, also where scores
+ * underflow to the same value.
+ *   x          logits [T] rows of n_experts values of `type` (COLI_F32, _BF16,
+ *              _F16) with row stride ldx; or, with router_w, the hidden state
+ *              [T][hidden] fp32 (ldx == hidden, hidden % 16 == 0), whose logits
+ *              x . router_w^T are computed in fp32 first
+ *   router_w   [n_experts][hidden] fp32, or NULL
+ *   bias       [n_experts] fp32, or NULL
+ *   topk_idx   [T][top_k] int32 out; topk_w [T][top_k] fp32 out
+ *   ws         a workspace prepared with coli_moe_workspace_init: with router_w
+ *              of coli_moe_select_workspace_size bytes; else 256 bytes, or NULL
+ *              (status bits are then lost)
+ * An expert whose logit or bias is -inf takes no part; it adds nothing to its
+ * group's score, and a position with fewer than top_k others gets id -1 and
+ * weight 0 in the slots that are left.  Weights whose sum is 0 stay 0.  Any other
+ * non-finite logit or bias gives a position ids -1 and weights 0 and sets
+ * COLI_STATUS_NONFINITE.  Limits: n_experts <= 1024, a multiple of n_groups <=
+ * 32, top_k <= 32 and <= the experts of topk_group groups.  T == 0 is a no-op. */
+#define COLI_SCORE_SIGMOID 0
+#define COLI_SCORE_SOFTMAX 1
+#define COLI_GROUP_TOP2    0
+#define COLI_GROUP_MAX     1
+typedef struct coli_moe_select_args {
+    const void*  x;
+    int64_t      ldx;
+    const float* router_w;
+    const float* bias;
+    int32_t*     topk_idx;
+    float*       topk_w;
+    void*        ws;
+    size_t       ws_bytes;
+    int32_t      type;
+    int32_t      hidden;
+    int32_t      n_experts;
+    int32_t      n_groups;
+    int32_t      topk_group;
+    int32_t      top_k;
+    int32_t      score;
+    int32_t      group_score;
+    int32_t      renorm;
+    float        scaling;
+} coli_moe_select_args;
+int coli_moe_select(const coli_moe_select_args* args, int32_t T, cudaStream_t stream);
+
+/* Bytes of workspace for coli_moe_select with router_w and up to max_T
+ * positions; 0 for sizes outside its limits. */
+size_t coli_moe_select_workspace_size(int32_t max_T, int32_t hidden, int32_t n_experts);
+
+/* The routed pairs in expert order (the batch union of "What's implemented"):
+ * pair (t, j) with id e = topk_idx[t][j] joins group e; groups ascend, and inside
+ * a group pairs keep the order of t * top_k + j.
+ *   topk_idx [T][top_k] int32 (-1: slot skipped)
+ *   offsets  [groups + 1] int32 out: first pair of each group, and the end
+ *   rows     [T * top_k] int32 out: position t of each pair; entries behind
+ *            the last pair are left as they were
+ *   slots    [T][top_k] int32 out: place of the pair, -1 for skipped slots
+ * With ep_size > 1 the groups are the experts of shard ep_rank (e mod ep_size ==
+ * ep_rank) as local records e / ep_size; slots of other shards are skipped.  Ids
+ * outside [-1, n_experts) are skipped and set COLI_STATUS_BADIDX.  ws: of
+ * coli_moe_group_workspace_size bytes, prepared with coli_moe_workspace_init.
+ * T == 0 writes the offsets (all 0). */
+int coli_moe_group(const int32_t* topk_idx, int32_t T, int32_t top_k, int32_t n_experts, int32_t ep_rank, int32_t ep_size,
+                   int32_t* offsets, int32_t* rows, int32_t* slots, void* ws, size_t ws_bytes, cudaStream_t stream);
+size_t coli_moe_group_workspace_size(int32_t max_T, int32_t top_k, int32_t n_experts);
+
+/* y[t] = add[t] + sum_j topk_w[t][j] * o[slots[t][j]], in fp32 and in this
+ * order, rounded once.
+ *   o      [P] rows of H values of o_type, row stride ldo
+ *   slots  [T][top_k] int32; slots outside [0, P) add nothing, whatever their
+ *          weight
+ *   add    [T] rows of y_type, row stride ld_add, or NULL; may be y itself
+ *   y      [T] rows of y_type, row stride ldy
+ * Any H, top_k and strides; rows that stay 16-byte aligned with H % 8 == 0 are
+ * read in 16-byte pieces.  T == 0 is a no-op. */
+int coli_moe_combine(const void* o, int32_t o_type, int64_t ldo, int32_t P, const int32_t* slots, const float* topk_w, int32_t T,
+                     int32_t top_k, int32_t H, const void* add, int64_t ld_add, void* y, int32_t y_type, int64_t ldy, cudaStream_t stream);
+
+/* 8-bit codes of rows with one scale a row: with A the row's largest magnitude,
+ * scale = A / 127 and code = value * 127 / A rounded to the nearest whole number,
+ * ties to even.  A row with A < 2^-100 gets scale 0 and codes 0, a row that
+ * holds an infinity or NaN scale NaN and codes 0.
+ *   x       [T] rows of x_type, row stride ldx; act COLI_ACT_NONE: K values;
+ *           COLI_ACT_SWIGLU: 2 K values, gate then up, and the row quantised is
+ *           silu(gate) * up in fp32
+ *   codes   [T] rows of K int8 out, row stride ldc (bytes behind K are left);
+ *   scales  [T] fp32 out
+ * Any K from 1 to COLI_I8_MAX_K.  T == 0 is a no-op. */
+#define COLI_ACT_NONE   0
+#define COLI_ACT_SWIGLU 1
+#define COLI_I8_MAX_K   131071
+int coli_i8_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t T, int32_t K, int32_t act, int8_t* codes, int64_t ldc, float* scales,
+                     cudaStream_t stream);
+
+/* out[t][k] = codes[t][k] * scales[t], rounded to out_type once from fp32. */
+int coli_i8_dequantize(const int8_t* codes, int64_t ldc, const float* scales, int32_t T, int32_t K, void* out, int32_t out_type, int64_t ldo,
+                       cudaStream_t stream);
+
+/* Products of 8-bit codes, grouped: row p of y belongs to group g with offsets[g]
+ * <= p < offsets[g+1] and, with r = rows[p] (rows NULL: r = p),
+ *     y[p][n] = x_scales[r] * w_scales[g][n] * sum_k x_codes[r][k] * w_codes[g][n][k].
+ * The sum is exact in 32-bit integers; it is rounded to fp32, scaled by x_scales,
+ * then by w_scales.
+ *   x_codes [x_rows] rows of K int8, row stride ldx;  x_scales [x_rows] fp32
+ *   rows    [P] int32 on the device, or NULL (P <= x_rows).  A row of y whose
+ *           activation row is outside [0, x_rows) is NaN and sets
+ *           COLI_STATUS_BADIDX
+ *   w_codes [G][N] rows of K int8, row stride ldw, group stride w_group (bytes);
+ *           w_scales [G][N] fp32, group stride w_scale_group (elements).  The
+ *           matrices of int8 expert records are such weights: gate and up of
+ *           all experts are [E][2 * inter] rows of hidden codes with w_group
+ *           3 * inter * hidden, down [E][hidden] rows of inter codes at
+ *           2 * inter * hidden of each record; their scales stand at 0 and at
+ *           2 * inter of every 2 * inter + hidden
+ *   offsets [G+1] int32 on the device, ascending; NULL: one group (G == 1) of all
+ *           P rows.  Groups may be empty; values are clamped to [0, P] and to
+ *           ascending order; rows of no group are not written
+ *   y       [P] rows of N values of y_type, row stride ldy
+ *   ws      prepared with coli_moe_workspace_init, of
+ *           coli_i8_product_workspace_size(P, K) bytes (status word)
+ * Any N >= 1 and any K from 1 to COLI_I8_MAX_K; ldx, ldw and w_group are multiples of
+ * 16 (COLI_EALIGN otherwise), so that every row begins on a 16-byte boundary. */
+#define COLI_I8_MAX_GROUPS 1024
+typedef struct coli_i8_product_args {
+    const int8_t*  x_codes;   int64_t ldx;
+    const float*   x_scales;
+    const int32_t* rows;
+    const int8_t*  w_codes;   int64_t ldw;   int64_t w_group;
+    const float*   w_scales;  int64_t w_scale_group;
+    const int32_t* offsets;
+    void*          y;         int64_t ldy;
+    void*          ws;        size_t  ws_bytes;
+    int32_t        x_rows;
+    int32_t        P;
+    int32_t        G;
+    int32_t        N;
+    int32_t        K;
+    int32_t        y_type;
+} coli_i8_product_args;
+int coli_i8_product(const coli_i8_product_args* args, cudaStream_t stream);
+size_t coli_i8_product_workspace_size(int32_t max_P, int32_t K);
+
 /* ---- no-allocation variant ----------------------------------------------
  * The pages have no counterpart to this entry point; it exists for callers
  * that cannot allocate device memory to pass a workspace -- a plain C or FFI

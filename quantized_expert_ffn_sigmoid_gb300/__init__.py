@@ -33,10 +33,15 @@ EXPORTS = (
     "coli_moe_stack_forward",
     "coli_mx4_quantize", "coli_mx4_dequantize", "coli_mx4_product", "coli_mx4_workspace_size",
     "coli_mx4_forward", "coli_moe_block_norm",
+    "coli_moe_select", "coli_moe_select_workspace_size", "coli_moe_group", "coli_moe_group_workspace_size", "coli_moe_combine",
+    "coli_i8_quantize", "coli_i8_dequantize", "coli_i8_product", "coli_i8_product_workspace_size",
 )
 STATIC_WS_BYTES = 24 << 20
 MX4_PRODUCT_WS_BYTES = 8704
 COLI_F32, COLI_BF16, COLI_F16, COLI_MX4 = 0, 1, 2, 3
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+GROUP_TOP2, GROUP_MAX = 0, 1
+ACT_NONE, ACT_SWIGLU = 0, 1
 
 
 class Cfg(ctypes.Structure):
@@ -86,6 +91,23 @@ class NormArgs(ctypes.Structure):
                 ("res_scale", ctypes.c_float), ("eps", ctypes.c_float), ("type", ctypes.c_int32), ("n_type", ctypes.c_int32)]
 
 
+class SelectArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("router_w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("topk_idx", ctypes.c_void_p), ("topk_w", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+                ("type", ctypes.c_int32), ("hidden", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scaling", ctypes.c_float)]
+
+
+class I8ProductArgs(ctypes.Structure):
+    _fields_ = [("x_codes", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scales", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("w_codes", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("w_group", ctypes.c_int64),
+                ("w_scales", ctypes.c_void_p), ("w_scale_group", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+                ("x_rows", ctypes.c_int32), ("P", ctypes.c_int32), ("G", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("y_type", ctypes.c_int32)]
+
+
 class WsLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in (
         "status", "n_entries", "entry_expert", "entry_count", "entry_offset", "pair_token",
@@ -122,6 +144,15 @@ def _load():
         "coli_mx4_workspace_size": ([CP, I32], ctypes.c_size_t),
         "coli_mx4_forward": ([CP, ctypes.POINTER(Mx4Weights), P, I32, P, I32, P, P, P, I32, P, S, P], ctypes.c_int),
         "coli_moe_block_norm": ([ctypes.POINTER(NormArgs), I32, I32, P], ctypes.c_int),
+        "coli_moe_select": ([ctypes.POINTER(SelectArgs), I32, P], ctypes.c_int),
+        "coli_moe_select_workspace_size": ([I32, I32, I32], ctypes.c_size_t),
+        "coli_moe_group": ([P, I32, I32, I32, I32, I32, P, P, P, P, S, P], ctypes.c_int),
+        "coli_moe_group_workspace_size": ([I32, I32, I32], ctypes.c_size_t),
+        "coli_moe_combine": ([P, I32, I64, I32, P, P, I32, I32, I32, P, I64, P, I32, I64, P], ctypes.c_int),
+        "coli_i8_quantize": ([P, I32, I64, I32, I32, I32, P, I64, P, P], ctypes.c_int),
+        "coli_i8_dequantize": ([P, I64, P, I32, I32, P, I32, I64, P], ctypes.c_int),
+        "coli_i8_product": ([ctypes.POINTER(I8ProductArgs), P], ctypes.c_int),
+        "coli_i8_product_workspace_size": ([I32, I32], ctypes.c_size_t),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -552,3 +583,201 @@ def coli_moe_block_norm(x, y=None, post_w=None, gate=None, res_scale=1.0, pre_w=
     rc = lib.coli_moe_block_norm(args, T, H, _on(dev, stream))
     if rc:
         _check(rc, "coli_moe_block_norm")
+
+
+# ------------------------------------------------- 8-bit codes, a scale a token and a channel
+_I8 = None
+
+
+def _codes8(t, shape, name: str, dev: int) -> int:
+    """The row stride of int8 codes of `shape` (two dimensions) on `dev`."""
+    if t.dtype is not _I8:
+        _i8_name(t, name)
+    return _rows(t, shape, name, dev)
+
+
+def _i8_name(t, name: str):
+    global _I8
+    import torch
+    _I8 = torch.int8
+    if t.dtype is not _I8:
+        raise TypeError(f"{name} must be torch.int8, not {t.dtype}")
+
+
+def _workspace_of(n: int, where: str, device):
+    import torch
+    if n == 0:
+        raise ColiError(COLI_EINVAL, where)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    coli_moe_workspace_init(ws)
+    return ws
+
+
+def _size32(*sizes):
+    if any(v >> 31 for v in sizes):
+        _beyond(*sizes)
+
+
+def coli_moe_select_workspace_size(max_T: int, hidden: int, n_experts: int) -> int:
+    _size32(max_T, hidden, n_experts)
+    return int(lib.coli_moe_select_workspace_size(int(max_T), int(hidden), int(n_experts)))
+
+
+def new_select_workspace(max_T: int, hidden: int, n_experts: int, device="cuda"):
+    """Allocate (with torch) and initialise a workspace for coli_moe_select with a router weight."""
+    return _workspace_of(coli_moe_select_workspace_size(max_T, hidden, n_experts), "coli_moe_select_workspace_size", device)
+
+
+def coli_moe_select(x, topk_idx, topk_w, router_w=None, bias=None, score=SCORE_SOFTMAX, n_groups=1, topk_group=1, group_score=GROUP_TOP2,
+                    renorm=True, scaling=1.0, ws=None, stream=None):
+    """The top_k experts of each position and their weights: from logits x [T, E] (any row stride), or with
+    ``router_w`` [E, H] (float32) from the hidden state x [T, H] (float32), whose logits need a workspace ``ws``
+    (new_select_workspace).  topk_idx [T, k] int32 and topk_w [T, k] float32 are written."""
+    T, width = shape = x.shape
+    ty, dev = _type(x), x.get_device()
+    if router_w is None:
+        E, H, ldx, rp = width, 0, _pitch(x, shape, "x"), None
+    else:
+        E, H = router_w.shape[0], width
+        rp = _flat(router_w, (E, H), _F32, "router_w", dev)
+        _flat(x, shape, _F32, "x", dev)
+        ldx = H
+    k = topk_idx.shape[1]
+    if (T | E | H | k | n_groups | topk_group) >> 31:
+        _beyond(T, E, H, k, n_groups, topk_group)
+    wp, wn = (None, 0) if ws is None else _space(ws, dev)
+    args = SelectArgs(x.data_ptr(), ldx, rp, None if bias is None else _flat(bias, (E,), _F32, "bias", dev),
+                      _flat(topk_idx, (T, k), _I32, "topk_idx", dev), _flat(topk_w, (T, k), _F32, "topk_w", dev), wp, wn, ty, H, E, n_groups, topk_group, k,
+                      score, group_score, 1 if renorm else 0, scaling)
+    rc = lib.coli_moe_select(args, T, _on(dev, stream))
+    if rc:
+        _check(rc, "coli_moe_select")
+
+
+def coli_moe_group_workspace_size(max_T: int, top_k: int, n_experts: int) -> int:
+    _size32(max_T, top_k, n_experts)
+    return int(lib.coli_moe_group_workspace_size(int(max_T), int(top_k), int(n_experts)))
+
+
+def new_group_workspace(max_T: int, top_k: int, n_experts: int, device="cuda"):
+    """Allocate (with torch) and initialise a workspace for coli_moe_group."""
+    return _workspace_of(coli_moe_group_workspace_size(max_T, top_k, n_experts), "coli_moe_group_workspace_size", device)
+
+
+def coli_moe_group(topk_idx, offsets, rows, slots, ws, n_experts=None, ep_rank=0, ep_size=0, stream=None):
+    """The routed pairs of topk_idx [T, k] in expert order: offsets [groups + 1], rows [T * k] (position of each
+    pair; behind the last one left as it was) and slots [T, k] (place of each pair, -1 where skipped) are written,
+    all int32.  ``n_experts`` is needed for a shard of ``ep_size`` (the groups are its own experts)."""
+    T, k = shape = topk_idx.shape
+    dev = topk_idx.get_device()
+    if _I32 is None:
+        _torch_names()
+    groups = offsets.shape[0] - 1
+    E = groups if n_experts is None else n_experts
+    if (T | k | E | ep_rank | ep_size) >> 31:
+        _beyond(T, k, E, ep_rank, ep_size)
+    want = E if ep_size <= 1 else (E - ep_rank + ep_size - 1) // ep_size
+    if groups != want:
+        raise ValueError(f"offsets must hold {want + 1} values for {want} experts, not {groups + 1}")
+    wp, wn = _space(ws, dev)
+    rc = lib.coli_moe_group(_flat(topk_idx, shape, _I32, "topk_idx", dev), T, k, E, ep_rank, ep_size, _flat(offsets, (groups + 1,), _I32, "offsets", dev),
+                            _flat(rows, (T * k,), _I32, "rows", dev), _flat(slots, shape, _I32, "slots", dev), wp, wn, _on(dev, stream))
+    if rc:
+        _check(rc, "coli_moe_group")
+
+
+def coli_moe_combine(o, slots, topk_w, y, add=None, stream=None):
+    """y[t] = add[t] + sum over j of topk_w[t, j] * o[slots[t, j]]: o [P, H], slots [T, k] int32 (places outside
+    [0, P) add nothing), topk_w [T, k] float32, y [T, H] and ``add`` [T, H] (may be y) of one type."""
+    T, H = shape = y.shape
+    P, k = o.shape[0], slots.shape[1]
+    if (T | H | P | k) >> 31:
+        _beyond(T, H, P, k)
+    ot, yt, dev = _type(o), _type(y), y.get_device()
+    ap, lda = None, 0
+    if add is not None:
+        if add.dtype is not y.dtype:
+            raise TypeError(f"add must have y's type {y.dtype}, not {add.dtype}")
+        ap, lda = add.data_ptr(), _rows(add, shape, "add", dev)
+    rc = lib.coli_moe_combine(o.data_ptr(), ot, _rows(o, (P, H), "o", dev), P, _flat(slots, (T, k), _I32, "slots", dev),
+                              _flat(topk_w, (T, k), _F32, "topk_w", dev), T, k, H, ap, lda, y.data_ptr(), yt, _pitch(y, shape, "y"), _on(dev, stream))
+    if rc:
+        _check(rc, "coli_moe_combine")
+
+
+def coli_i8_quantize(x, codes, scales, swiglu=False, stream=None):
+    """8-bit codes [T, K] (int8, any row stride) and scales [T] (float32) of the rows of x [T, K], or with
+    ``swiglu`` of silu(gate) * up for rows x [T, 2 K] of gate and up values."""
+    T, K = shape = codes.shape
+    if (T | K) >> 31:
+        _beyond(T, K)
+    ty, dev = _type(x), x.get_device()
+    rc = lib.coli_i8_quantize(x.data_ptr(), ty, _rows(x, (T, 2 * K) if swiglu else shape, "x", dev), T, K, 1 if swiglu else 0,
+                              codes.data_ptr(), _codes8(codes, shape, "codes", dev), _flat(scales, (T,), _F32, "scales", dev), _on(dev, stream))
+    if rc:
+        _check(rc, "coli_i8_quantize")
+
+
+def coli_i8_dequantize(codes, scales, out, stream=None):
+    """The values of codes [T, K] (int8, any row stride) and scales [T] into out [T, K] (any row stride)."""
+    T, K = shape = out.shape
+    if (T | K) >> 31:
+        _beyond(T, K)
+    ty, dev = _type(out), out.get_device()
+    rc = lib.coli_i8_dequantize(codes.data_ptr(), _codes8(codes, shape, "codes", dev), _flat(scales, (T,), _F32, "scales", dev), T, K,
+                                out.data_ptr(), ty, _pitch(out, shape, "out"), _on(dev, stream))
+    if rc:
+        _check(rc, "coli_i8_dequantize")
+
+
+def coli_i8_product_workspace_size(max_P: int, K: int) -> int:
+    _size32(max_P, K)
+    return int(lib.coli_i8_product_workspace_size(int(max_P), int(K)))
+
+
+def new_i8_product_workspace(max_P: int, K: int, device="cuda"):
+    """Allocate (with torch) and initialise a workspace for coli_i8_product with up to max_P rows."""
+    return _workspace_of(coli_i8_product_workspace_size(max_P, K), "coli_i8_product_workspace_size", device)
+
+
+def coli_i8_product(x_codes, x_scales, w_codes, w_scales, y, ws, offsets=None, rows=None, stream=None):
+    """y[p] = w[group of p] x[rows[p]] for codes x_codes [X, K] with x_scales [X], and w_codes [G, N, K] (or [N, K])
+    with w_scales [G, N] (or [N]), whose groups may stand at any stride (views of expert records); ``offsets``
+    [G + 1] int32 gives each group's first row of y [P, N] (None: one group), ``rows`` [P] int32 each row's
+    activation row (None: the row itself).  Rows of codes begin on 16-byte boundaries."""
+    X, K = x_shape = x_codes.shape
+    P, N = y.shape
+    yt, dev = _type(y), y.get_device()
+    if w_codes.dim() == 3:
+        G, Nw, Kw = w_codes.shape
+        wg, ldw, step = w_codes.stride()
+    else:
+        G, (Nw, Kw) = 1, w_codes.shape
+        wg, (ldw, step) = 0, w_codes.stride()
+    if (X | K | P | N | G) >> 31:
+        _beyond(X, K, P, N, G)
+    if Nw != N or Kw != K or w_codes.get_device() != dev:
+        _refuse(w_codes, "int8 ", (G, N, K), "w_codes", dev)
+    if w_codes.dtype is not _I8:
+        _i8_name(w_codes, "w_codes")
+    if step != 1 and K > 1:
+        raise ValueError("w_codes must have consecutive elements in each row")
+    if N == 1 and ldw < K:
+        ldw = -(-K // 16) * 16  # one row a group: its stride is not used
+    if w_scales.dtype is not _F32:
+        raise TypeError(f"w_scales must be torch.float32, not {w_scales.dtype}")
+    if w_scales.shape != ((G, N) if w_codes.dim() == 3 else (N,)) or w_scales.get_device() != dev:
+        _refuse(w_scales, "", (G, N) if w_codes.dim() == 3 else (N,), "w_scales", dev)
+    if w_scales.stride()[-1] != 1 and N > 1:
+        raise ValueError("w_scales must have consecutive elements in each row")
+    ldx = _codes8(x_codes, x_shape, "x_codes", dev)
+    if X <= 1 and ldx % 16:
+        ldx = -(-K // 16) * 16  # one row: its stride is not used
+    wp, wn = _space(ws, dev)
+    args = I8ProductArgs(x_codes.data_ptr(), ldx, _flat(x_scales, (X,), _F32, "x_scales", dev),
+                         None if rows is None else _flat(rows, (P,), _I32, "rows", dev), w_codes.data_ptr(), ldw, wg if G > 1 else 0,
+                         w_scales.data_ptr(), w_scales.stride()[0] if G > 1 else 0, None if offsets is None else _flat(offsets, (G + 1,), _I32, "offsets", dev),
+                         y.data_ptr(), _pitch(y, (P, N), "y"), wp, wn, X, P, G, N, K, yt)
+    rc = lib.coli_i8_product(args, _on(dev, stream))
+    if rc:
+        _check(rc, "coli_i8_product")

@@ -1,0 +1,551 @@
+// Products of 8-bit codes grouped by expert, on the tensor cores.
+//
+// Mathematics (i8_product.cu has the whole of it).  This target has no integer
+// tensor instruction, but codes are exact in fp16 and their products (at most
+// 2^14) and sums exact in fp32 up to 2^24: over 1024 of them.  So
+// tcgen05.mma kind::f16 sums runs of 1024 codes in tensor memory, and the runs
+// are added as 32-bit integers in registers: the exact sum for any K.
+//
+// Operands.  Weights are the M side (128 rows a tile), widened to fp16 by
+// converter warps on their way from shared to tensor memory, where the
+// instruction reads them: they are read from HBM as single bytes, once for all
+// activation rows of a tile.  Activations are the N side, widened once per call
+// in the workspace (i8_widen, which also gathers the rows of y) and fetched by TMA.
+//
+// One persistent CTA an SM, 20 warps meeting at mbarriers, every wait bounded:
+//   warp 0       TMA of weight codes, slots of 128 rows x 128 codes;
+//   warp 1       TMA of activations, slots of up to NT rows x 64 codes;
+//   warp 2       MMA issuer, blocks of K = 64;
+//   warps 4-11   converters, two sets of four (a warp for each lane quarter)
+//                that take the blocks in turn: a block's way through registers
+//                takes longer than its products;
+//   warps 12-19  epilogue: runs of 1024 codes into integer registers, at the
+//                end the scales and y.
+// Tensor memory: three accumulators of 128 columns (while one is read the
+// products go on in another) and four blocks of widened weights.
+#include "i8_product.cuh"
+#include "tcgen05.cuh"
+#include "tensormap.cuh"
+
+namespace colimoe {
+namespace {
+
+constexpr int IG_M = 128;                    // weight rows of a tile
+constexpr int IG_WK = 128, IG_BK = 64;       // codes of a weight slot's row, of a block
+constexpr uint32_t IG_WSLOT = IG_M * IG_WK;  // 16 KB
+constexpr int IG_AS = 4;                     // blocks of widened weights in tensor memory
+constexpr uint32_t IG_ACOL = 3 * 128;        // their first column
+constexpr int IG_RUN = 1024 / IG_BK;         // blocks of an exact run
+constexpr int IG_MB = 8;                     // weight tiles that share activation tiles while they are in L2
+constexpr int IG_THREADS = 640;
+constexpr int IG_RCTL = 40, IG_RCONV = 56, IG_REPI = 160;
+constexpr int IG_MAX_SMEM = 227 * 1024;
+constexpr int IG_MAXW = 10, IG_MAXB = 12;
+
+// NT: activation rows of a tile at most.  Slots fill 208 KB.
+template <int NT>
+struct IgShape {
+  static constexpr int NW = NT == 32 ? 10 : NT == 64 ? 8 : NT == 128 ? 5 : 3;
+  static constexpr int NB = NT == 32 ? 12 : NT == 64 ? 10 : NT == 128 ? 8 : 5;
+  static constexpr uint32_t BSLOT = NT * IG_BK * 2;
+  static constexpr uint32_t BARS = NW * IG_WSLOT + NB * BSLOT;
+  static constexpr uint32_t TABLES = BARS + 512;
+  static constexpr int COLS = NT == 256 ? 128 : NT / 2;  // columns of an epilogue warp
+};
+template <int NT>
+constexpr size_t ig_smem(int G) { return IgShape<NT>::TABLES + 8 * (size_t)(G + 1) + 1024; }
+
+struct IgMaps {
+  CUtensorMap w;     // weight codes [G][N][K]
+  CUtensorMap x[4];  // widened activations, boxes of 64 codes x 16, 32, 64, 128 rows
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy) : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem], issued by the lane whose `leader` is set
+__device__ __forceinline__ void umma_f16_if(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader) : "memory");
+}
+
+// Which accumulator a half of the tile uses and which comes next.  Every role
+// follows the same sequence: `turn` when a half's run ends.
+struct IgSlots {
+  int cur0 = 0, cur1 = 1, spare = 2;
+  uint32_t uses = 0;  // bit s: parity of the runs that accumulator s has held
+  template <int H>
+  __device__ __forceinline__ void turn(bool halves) {
+    const int old = H == 0 ? cur0 : cur1;
+    uses ^= 1u << old;
+    if (H == 0) cur0 = spare; else cur1 = spare;
+    spare = old;
+    if (!halves) {  // one half: all three in rotation
+      spare = cur1;
+      cur1 = old;
+    }
+  }
+};
+
+struct IgItem {
+  int g, row0, ntok, n0;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__ IgMaps maps, const I8Params A, const uint32_t off_xs) {
+  using S = IgShape<NT>;
+  constexpr int NW = S::NW, NB = S::NB;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<size_t>(sm_raw), 1024));
+  uint8_t* sm_b = sm + NW * IG_WSLOT;
+  uint64_t* full_w = reinterpret_cast<uint64_t*>(sm + S::BARS);  // [NW] weight codes landed
+  uint64_t* empty_w = full_w + IG_MAXW;                          // [NW] all converters have read them
+  uint64_t* full_b = empty_w + IG_MAXW;                          // [NB] activations landed
+  uint64_t* done = full_b + IG_MAXB;                             // [NB] the block's products are complete
+  uint64_t* a_full = done + IG_MAXB;                             // [IG_AS] a block of weights is in tensor memory
+  uint64_t* d_full = a_full + IG_AS;                             // [3] a run is complete
+  uint64_t* d_empty = d_full + 3;                                // [3] it has been read
+  uint64_t* fin = d_empty + 3;
+  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(fin + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_taddr + 1);
+  int* s_row0 = reinterpret_cast<int*>(sm + S::TABLES);          // [G + 1] first row of a group
+  int* s_tiles = s_row0 + A.G + 1;                               // [G + 1] activation tiles before it
+  uint32_t* status = reinterpret_cast<uint32_t*>(A.ws);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nblk = (A.K + IG_BK - 1) / IG_BK;
+  const int mt = (A.N + IG_M - 1) / IG_M;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NW; ++i) {
+      mbar_init(&full_w[i], 1);
+      mbar_init(&empty_w[i], 8);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&full_b[i], 1);
+      mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < IG_AS; ++i) mbar_init(&a_full[i], 4);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], NT == 256 ? 4 : 8);
+    }
+    mbar_init(fin, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)), "n"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 3) {
+    // first rows and tiles of the groups, in ascending order
+    int run = 0, top = 0;
+    for (int base = 0; base <= A.G; base += 32) {
+      const int u = base + lane;
+      int a = u <= A.G ? i8_offset(A, u) : 0, b = u < A.G ? i8_offset(A, u + 1) : 0;
+      a = max(a, top);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, a, o);
+        if (lane >= o) a = max(a, v);
+      }
+      top = __shfl_sync(0xffffffffu, a, 31);
+      const int tiles = u < A.G ? (max(a, b) - a + NT - 1) / NT : 0;
+      int inc = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (u <= A.G) {
+        s_row0[u] = a;
+        s_tiles[u] = run + inc - tiles;
+      }
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t taddr = *s_taddr;
+  const int items = s_tiles[A.G] * mt;
+
+  // Items of a group: IG_MB weight tiles for each activation tile, so that the
+  // CTAs at work together share both operands in L2.
+  auto item_at = [&](int item) {
+    const int q = item / mt;
+    int lo = 0, hi = A.G - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_tiles[mid] <= q) lo = mid; else hi = mid - 1;
+    }
+    const int t0 = s_tiles[lo], ntn = s_tiles[lo + 1] - t0, local = item - t0 * mt;
+    const int mb = local / (IG_MB * ntn), in = local - mb * IG_MB * ntn, width = min(IG_MB, mt - mb * IG_MB);
+    const int nt = in / width;
+    IgItem it;
+    it.g = lo;
+    it.row0 = s_row0[lo] + nt * NT;
+    it.ntok = min(NT, s_row0[lo + 1] - it.row0);
+    it.n0 = (mb * IG_MB + in - nt * width) * IG_M;
+    return it;
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<IG_RCTL>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------- TMA of weights
+      const uint64_t stream = policy_evict_first();
+      uint32_t gs = 0;
+      bool go = true;
+      for (int item = blockIdx.x; item < items && go; item += gridDim.x) {
+        const IgItem it = item_at(item);
+        const bool once = s_tiles[it.g + 1] - s_tiles[it.g] == 1;  // read for one activation tile alone
+        for (int st = 0; 2 * st < nblk; ++st, ++gs) {
+          const uint32_t s = gs % NW;
+          if (!gwait(&empty_w[s], ((gs / NW) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
+          mbar_arrive_expect_tx(&full_w[s], IG_WSLOT);
+          if (once) tma_load_3d_hint(sm + s * IG_WSLOT, &maps.w, st * IG_WK, it.n0, it.g, &full_w[s], stream);
+          else tma_load_3d(sm + s * IG_WSLOT, &maps.w, st * IG_WK, it.n0, it.g, &full_w[s]);
+        }
+      }
+      // every copy issued has landed before the CTA can exit
+      for (uint32_t k = gs > (uint32_t)NW ? gs - NW : 0; k < gs; ++k)
+        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full_w[k % NW], (k / NW) & 1u); ++i) {
+        }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------ TMA of activations
+      fence_proxy_async_global();  // (the widened rows were written by ordinary stores of the kernel before)
+      uint32_t gs = 0;
+      bool go = true;
+      for (int item = blockIdx.x; item < items && go; item += gridDim.x) {
+        const IgItem it = item_at(item);
+        const int n16 = (it.ntok + 15) / 16;
+        for (int j = 0; j < nblk; ++j, ++gs) {
+          const uint32_t s = gs % NB;
+          if (!gwait(&done[s], ((gs / NB) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
+          mbar_arrive_expect_tx(&full_b[s], (uint32_t)n16 * 2048);
+          int row = 0;
+          for (int left = n16; left > 0;) {  // the rows in boxes of 128, 64, 32, 16
+            const int i = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
+            tma_load_2d(sm_b + s * S::BSLOT + row * 128, &maps.x[i], j * IG_BK, it.row0 + row, &full_b[s]);
+            row += 16 << i;
+            left -= 1 << i;
+          }
+        }
+      }
+      for (uint32_t k = gs > (uint32_t)NB ? gs - NB : 0; k < gs; ++k)
+        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full_b[k % NB], (k / NB) & 1u); ++i) {
+        }
+    } else if (warp == 2) {
+      // -------------------------------------------------------- MMA issuer
+      // (the whole warp runs the loop, one elected lane issues: operands stay
+      // in uniform registers)
+      const uint32_t leader = elect_one();
+      IgSlots D;
+      uint32_t gb = 0;
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const IgItem it = item_at(item);
+        const bool halves = NT == 256 && it.ntok > 128;
+        const uint32_t id0 = umma_idesc((min(it.ntok, 128) + 15) & ~15), id1 = umma_idesc((max(it.ntok - 128, 16) + 15) & ~15);
+        bool fresh0 = true, fresh1 = true, ok = true;
+        for (int j = 0; j < nblk; ++j, ++gb) {
+          const uint32_t s = gb % NB, a = gb % IG_AS;
+          if (fresh0) ok = ok && gwait(&d_empty[D.cur0], (D.uses >> D.cur0 & 1u) ^ 1u, status, s_abort);
+          ok = ok && gwait(&full_b[s], (gb / NB) & 1u, status, s_abort) && gwait(&a_full[a], (gb / IG_AS) & 1u, status, s_abort);
+          const uint32_t ac = taddr + IG_ACOL + a * 32;
+          const uint64_t db = umma_desc_sw128(smem_u32(sm_b) + s * S::BSLOT);
+          if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
+            tmem_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_f16_if(taddr + D.cur0 * 128, ac + 8 * k, db + 2 * k, id0, (uint32_t)(k > 0 || !fresh0), leader);
+          }
+          fresh0 = false;
+          if (NT == 256 && halves) {
+            if (fresh1) ok = ok && gwait(&d_empty[D.cur1], (D.uses >> D.cur1 & 1u) ^ 1u, status, s_abort);
+            if (ok) {
+              tmem_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_f16_if(taddr + D.cur1 * 128, ac + 8 * k, db + 128 * 128 / 16 + 2 * k, id1, (uint32_t)(k > 0 || !fresh1), leader);
+            }
+            fresh1 = false;
+          }
+          umma_commit_if(&done[s], leader);
+          const bool last = j + 1 == nblk;
+          if (last || (j + 1) % IG_RUN == 0) {
+            umma_commit_if(&d_full[D.cur0], leader);
+            D.turn<0>(halves);
+            fresh0 = true;
+          }
+          if (NT == 256 && halves && (last || (j + 1) % IG_RUN == IG_RUN / 2)) {  // half a run apart, so that one
+            umma_commit_if(&d_full[D.cur1], leader);                            // spare accumulator serves both
+            D.turn<1>(halves);
+            fresh1 = true;
+          }
+        }
+      }
+      // every MMA issued has completed before the accumulators are freed
+      umma_commit_if(fin, leader);
+      for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(fin, 0u); ++i) {
+      }
+    }
+  } else if (warp < 12) {
+    setmaxnreg_dec<IG_RCONV>();
+    // ---------------------------------------------------------- converters
+    const int set = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
+    uint32_t gs = 0, gb = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+      for (int st = 0; 2 * st < nblk; ++st, ++gs) {
+        const uint32_t s = gs % NW;
+        gwait(&full_w[s], (gs / NW) & 1u, status, s_abort);
+        const int j = 2 * st + set;
+        uint4 w[4];
+        if (j < nblk) {
+          const uint8_t* row = sm + s * IG_WSLOT + r * IG_WK;  // 16-byte unit c of row r at unit c ^ (r % 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(row + 16 * ((4 * set + i) ^ (r & 7)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty_w[s]);
+        if (j >= nblk) continue;
+        const uint32_t b = gb + j, a = b % IG_AS;
+        const uint32_t ta = taddr + ((uint32_t)(32 * q) << 16) + IG_ACOL + a * 32;
+        uint32_t o[16];
+        cvt_int8x8(w[0].x, w[0].y, o);
+        cvt_int8x8(w[0].z, w[0].w, o + 4);
+        cvt_int8x8(w[1].x, w[1].y, o + 8);
+        cvt_int8x8(w[1].z, w[1].w, o + 12);
+        // the block that held these columns is done (that phase cannot have been
+        // overtaken: the next block in its slot needs this one's weights first)
+        if (b >= (uint32_t)IG_AS) gwait(&done[(b - IG_AS) % NB], ((b - IG_AS) / NB) & 1u, status, s_abort);
+        tmem_fence_after();
+        __syncwarp();
+        tmem_st16(ta, o);
+        cvt_int8x8(w[2].x, w[2].y, o);
+        cvt_int8x8(w[2].z, w[2].w, o + 4);
+        cvt_int8x8(w[3].x, w[3].y, o + 8);
+        cvt_int8x8(w[3].z, w[3].w, o + 12);
+        tmem_st16(ta + 16, o);
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a_full[a]);
+      }
+      gb += nblk;
+    }
+  } else {
+    setmaxnreg_inc<IG_REPI>();
+    // ------------------------------------------------------------ epilogue
+    constexpr int COLS = S::COLS;
+    const int set = (warp - 12) >> 2, q = warp & 3;
+    const float* xs = reinterpret_cast<const float*>(A.ws + off_xs);
+    IgSlots D;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+      const IgItem it = item_at(item);
+      const bool halves = NT == 256 && it.ntok > 128;
+      const int half = NT == 256 ? set : 0;           // whose runs this warp reads
+      const int col0 = NT == 256 ? set * 128 : set * COLS;
+      const int cols = min(max(it.ntok - col0, 0), COLS);
+      int acc[COLS];
+#pragma unroll
+      for (int i = 0; i < COLS; ++i) acc[i] = 0;
+      auto read_run = [&](int slot) {
+        gwait(&d_full[slot], D.uses >> slot & 1u, status, s_abort);
+        tmem_fence_after();
+        __syncwarp();
+        const uint32_t t = taddr + ((uint32_t)(32 * q) << 16) + slot * 128 + (NT == 256 ? 0 : col0);
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16)
+          if (c < cols) {
+            uint32_t v[16];
+            tmem_ld16_nowait(t + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(v[i]));
+          }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_empty[slot]);
+      };
+      // the ends of runs in their order: half 0 at 16, 32, ... blocks, half 1 at 8, 24, ..., both at the end
+      for (int c = IG_RUN / 2; c < nblk; c += IG_RUN / 2) {
+        if (c % IG_RUN == 0) {
+          if (half == 0) read_run(D.cur0);
+          D.turn<0>(halves);
+        } else if (halves) {
+          if (half == 1) read_run(D.cur1);
+          D.turn<1>(halves);
+        }
+      }
+      if (half == 0) read_run(D.cur0);
+      D.turn<0>(halves);
+      if (halves) {
+        if (half == 1) read_run(D.cur1);
+        D.turn<1>(halves);
+      }
+      const int n = it.n0 + 32 * q + lane;
+      const bool live = n < A.N;
+      const float sw = live ? __ldg(A.ws_ + it.g * A.wsgroup + n) : 0.f;
+      const long long at = (long long)(it.row0 + col0) * A.ldy + n;
+      auto store = [&](auto* y) {
+        using TY = std::remove_pointer_t<decltype(y)>;
+        y += at;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16)
+          if (c < cols) {
+            const float sx = c + (lane & 15) < cols ? __ldcg(xs + it.row0 + col0 + c + (lane & 15)) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float v = i8_value(acc[c + i], __shfl_sync(0xffffffffu, sx, i), sw);
+              if (live && c + i < cols) y[(c + i) * A.ldy] = from_f32<TY>(v);
+            }
+          }
+      };
+      if (A.y_type == COLI_F32) store(static_cast<float*>(A.y));
+      else if (A.y_type == COLI_BF16) store(static_cast<__nv_bfloat16*>(A.y));
+      else store(static_cast<__half*>(A.y));
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512) : "memory");
+}
+
+// The rows of y: fp16 copies of their activation codes, zero up to kp, and
+// their scales.  A warp a row.  A row out of range gets scale NaN.
+constexpr int WD_T = 256;
+__global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb) {
+  __shared__ int s_lo, s_hi;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    s_lo = A.offsets ? i8_offset(A, 0) : 0;
+    s_hi = A.offsets ? 0 : A.P;
+  }
+  __syncthreads();
+  if (A.offsets) {  // rows of any group: up to the largest offset
+    int hi = 0;
+    for (int g = threadIdx.x; g <= A.G; g += WD_T) hi = max(hi, i8_offset(A, g));
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) atomicMax(&s_hi, hi);
+    __syncthreads();
+  }
+  const int hi = s_hi;
+  for (long long p = s_lo + (long long)blockIdx.x * (WD_T / 32) + warp; p < hi; p += (long long)gridDim.x * (WD_T / 32)) {
+    const int row = A.rows ? __ldcg(A.rows + p) : (int)p;
+    const bool ok = row >= 0 && row < A.X;
+    if (lane == 0) {
+      xs[p] = ok ? __ldcg(A.xs + row) : __uint_as_float(0x7fc00000u);
+      if (!ok) atomicOr(reinterpret_cast<uint32_t*>(A.ws), COLI_STATUS_BADIDX);
+    }
+    const int8_t* src = A.x + (ok ? row : 0) * A.ldx;
+    uint4* dst = xb + p * (kp / 8);
+#pragma unroll 4
+    for (int u = lane; u < kp / 16; u += 32) {
+      const int n = ok ? A.K - 16 * u : 0;
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (n >= 16) {
+        c = __ldcg(reinterpret_cast<const uint4*>(src + 16 * u));
+      } else if (n > 0) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < n) w[i >> 2] |= (uint32_t)(uint8_t)src[16 * u + i] << (8 * (i & 3));
+        c = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      uint32_t o[8];
+      cvt_int8x8(c.x, c.y, o);
+      cvt_int8x8(c.z, c.w, o + 4);
+      dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+bool encode_weights(CUtensorMap* m, const I8Params& A) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)A.K, (cuuint64_t)A.N, (cuuint64_t)A.G};
+  const cuuint64_t strides[2] = {(cuuint64_t)A.ldw, (cuuint64_t)(A.G > 1 ? A.wgroup : A.ldw)};
+  const cuuint32_t box[3] = {IG_WK, IG_M, 1}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(A.w), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_rows_f16(CUtensorMap* m, const void* base, int kp, int rows, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kp, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kp * 2};
+  const cuuint32_t box[2] = {IG_BK, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Once a device: the shared-memory limit, and that the warps' register split
+// fits in what a CTA is launched with (setmaxnreg.inc would otherwise wait for
+// registers that never come).
+template <int NT>
+cudaError_t check_kernel() {
+  static std::atomic<uint64_t> checked{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (checked.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(i8_gemm<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, IG_MAX_SMEM);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa{};
+  if ((e = cudaFuncGetAttributes(&fa, i8_gemm<NT>)) != cudaSuccess) return e;
+  const int need = 128 * IG_RCTL + 256 * IG_RCONV + 256 * IG_REPI;
+  if (fa.numRegs * IG_THREADS < need || fa.numRegs < IG_RCONV || fa.numRegs > IG_REPI || fa.maxThreadsPerBlock < IG_THREADS)
+    return cudaErrorInvalidConfiguration;
+  checked.fetch_or(1ull << dev, std::memory_order_release);
+  return cudaSuccess;
+}
+
+template <int NT>
+cudaError_t launch_nt(const IgMaps& maps, const I8Params& A, int sms, cudaStream_t st) {
+  const cudaError_t e = check_kernel<NT>();
+  if (e != cudaSuccess) return e;
+  // (at most: a partial tile per group that can have rows)
+  const long long tiles = (long long)A.P / NT + (A.G < A.P ? A.G : A.P), items = tiles * ((A.N + IG_M - 1) / IG_M);
+  if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_pdl(i8_gemm<NT>, (unsigned)(items < sms ? items : sms), IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs());
+}
+
+}  // namespace
+
+cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int kp = (int)i8_kp(A.K);
+  float* xs = reinterpret_cast<float*>(A.ws + i8_off_xs());
+  uint8_t* xb = A.ws + i8_off_xb(A.P);
+  IgMaps maps;
+  bool ok = encode_weights(&maps.w, A);
+  for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
+  if (!ok) return cudaErrorInvalidValue;
+  const long long wide = ((long long)A.P + WD_T / 32 - 1) / (WD_T / 32);
+  const cudaError_t e = launch_pdl(i8_widen, (unsigned)(wide < 8LL * sms ? wide : 8LL * sms), WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
+  if (e != cudaSuccess) return e;
+  if (A.P <= 32) return launch_nt<32>(maps, A, sms, st);
+  if (A.P <= 64) return launch_nt<64>(maps, A, sms, st);
+  if (A.P < 192LL * A.G) return launch_nt<128>(maps, A, sms, st);
+  return launch_nt<256>(maps, A, sms, st);
+}
+
+}  // namespace colimoe

@@ -1,0 +1,44 @@
+// Parameters and workspace of the products of 8-bit codes.
+#pragma once
+#include "mx4_common.cuh"
+
+namespace colimoe {
+
+struct I8Params {
+  const int8_t* x;            // activation codes, X rows of pitch ldx
+  long long ldx;
+  const float* xs;            // [X]
+  int X;
+  const int32_t* rows;        // [P] activation row of each row of y; null: the row itself
+  int P;
+  const int8_t* w;            // weight codes: group g at g * wgroup, its rows of pitch ldw
+  long long ldw, wgroup;
+  const float* ws_;           // their scales: group g at g * wsgroup
+  long long wsgroup;
+  int G, N, K;
+  const int32_t* offsets;     // [G + 1], or null (one group)
+  void* y;
+  int32_t y_type;
+  long long ldy;
+  uint8_t* ws;                // status word at 0
+};
+
+constexpr int I8_FEW = 8;     // up to this many rows: the streaming kernel
+
+// Workspace behind the header: fp16 copies of the activation rows of y, padded
+// to kp codes, and their scales.
+inline long long i8_kp(int K) { return ((long long)K + 63) / 64 * 64; }
+inline size_t i8_off_xs() { return WS_HEADER_BYTES; }
+inline size_t i8_off_xb(int P) { return align_up(i8_off_xs() + 4 * (size_t)P, 256); }
+inline size_t i8_ws_bytes(int P, int K) { return align_up(i8_off_xb(P) + 2 * (size_t)P * (size_t)i8_kp(K), 256); }
+
+// First row of group g: offsets clamped to [0, P]; ascending by running maximum
+__device__ __forceinline__ int i8_offset(const I8Params& A, int g) { return A.offsets ? min(max(__ldcg(A.offsets + g), 0), A.P) : g * A.P; }
+
+// One element of y: the integer sum, then the scales, in fp32
+__device__ __forceinline__ float i8_value(int sum, float sx, float sw) { return __int2float_rn(sum) * sx * sw; }
+
+cudaError_t launch_i8_stream(const I8Params& A, cudaStream_t st);
+cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st);
+
+}  // namespace colimoe

@@ -143,21 +143,6 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uin
       "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "r"(leader) : "memory");
 }
-__device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t leader) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-      ::"r"(smem_u32(bar)), "r"(leader) : "memory");
-}
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -276,21 +261,6 @@ __device__ __forceinline__ void swiglu_cols(float* ex, int bar, uint32_t tmem, i
       }
     }
   }
-}
-
-// A bounded wait that gives up at once after any wait of the CTA has expired
-// (the abort flag), so that a broken pipeline drains.  Without a suspend-time
-// hint, with which a thread wakes late, and not polling, which takes issue
-// slots from the epilogue: one position took 45.3 us against 47.2 with the
-// scale writers and the MMA warp polling.
-__device__ __forceinline__ bool gwait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
-  for (uint32_t i = 0; i < SPIN_LIMIT; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-  }
-  *abort = 1;
-  atomicOr(status, COLI_STATUS_TIMEOUT);
-  return false;
 }
 
 // Waits until the entry's gate/up items are complete (bounded, as gwait).

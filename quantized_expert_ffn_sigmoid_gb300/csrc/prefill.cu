@@ -97,11 +97,6 @@ __host__ __device__ constexpr size_t pf_off_bar(int bits) {
 }
 __host__ __device__ constexpr size_t pf_smem(int bits) { return pf_off_bar(bits) + 512; }
 
-// kind::f16, fp16 x fp16 -> fp32, both K-major, M = 128
-__device__ __forceinline__ uint32_t umma_idesc(int n) {
-  return (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(PF_M >> 4) << 24);
-}
-
 // D[tmem] (+)= A[tmem] x B[smem descriptor]
 __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t idesc,
                                             uint32_t acc) {
@@ -110,23 +105,6 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
       "setp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(tmem_d), "r"(tmem_a), "l"(db), "r"(idesc), "r"(acc) : "memory");
-}
-
-template <uint32_t N>
-__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <uint32_t N>
-__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-__device__ __forceinline__ uint32_t hsub2_u32(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
 }
 
 // 8 packed int4 codes (one 32-bit word, stored as code + 8) -> 8 fp16 in the
@@ -141,17 +119,6 @@ __device__ __forceinline__ void cvt_int4x8(uint32_t w, uint32_t* o) {
   o[2] = hsub2_u32(prmt(hi, k, 0x4140u), off);
   o[3] = hsub2_u32(prmt(hi, k, 0x4342u), off);
 }
-// 8 int8 codes (two words) -> 8 fp16 in storage order: the byte with its sign
-// bit flipped is code + 128; 0x6400 | that is 1024 + code + 128; minus 1152.
-__device__ __forceinline__ void cvt_int8x8(uint32_t w0, uint32_t w1, uint32_t* o) {
-  const uint32_t x0 = w0 ^ 0x80808080u, x1 = w1 ^ 0x80808080u;
-  const uint32_t k = 0x64646464u, off = 0x64806480u;
-  o[0] = hsub2_u32(prmt(x0, k, 0x4140u), off);
-  o[1] = hsub2_u32(prmt(x0, k, 0x4342u), off);
-  o[2] = hsub2_u32(prmt(x1, k, 0x4140u), off);
-  o[3] = hsub2_u32(prmt(x1, k, 0x4342u), off);
-}
-
 // fp16 activation codes and transposed scales of every pair: xb[p] =
 // fp16(qx[token(p)]) in the workspace's code order, xs_t[b][p] = dx[token(p)][b].
 // xb lives in the per-pair output region, which the down pass overwrites only

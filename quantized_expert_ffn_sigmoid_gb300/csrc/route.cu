@@ -245,4 +245,29 @@ cudaError_t launch_route(const float* x, int T, int H, const float* wr, int E, i
   return launch_select(part, ks, T, E, G, topk_group, k, rsf, bias, topk_idx, topk_w, status, st);
 }
 
+// The logits kernels alone: partial sums of K ranges in part[splits][T][E].
+cudaError_t launch_route_partials(const float* x, int T, int H, const float* wr, int E, float* part, uint32_t* status, int* splits, cudaStream_t st) {
+  if (T <= ROUTE_GEMV_MAX_T) {
+    int n = GEMV_SPLITS;
+    while (n > 1 && (H / 4) % (n * 32)) n /= 2;
+    *splits = n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((E + 7) / 8, n);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // (the kernel loads E floats of the bias that its selection would use: those of wr do as well)
+    return cudaLaunchKernelEx(&cfg, route_fused, x, T, H, wr, E, n, part, 1, 1, 1, 1.f, wr, (int32_t*)nullptr, (float*)nullptr, status,
+                              (uint32_t*)nullptr, 0);
+  }
+  *splits = route_ksplits(T, H, E);
+  dim3 grid((E + 63) / 64, (T + 63) / 64, *splits);
+  route_logits_tiled<<<grid, 256, 0, st>>>(x, T, H, wr, E, part, H / *splits);
+  return cudaGetLastError();
+}
+
 }  // namespace colimoe

@@ -1,0 +1,308 @@
+// Selection of experts from scores: softmax or sigmoid, a bias for balance,
+// groups, top-k, weights from the unbiased scores.
+//
+// Mathematics, per position with logits l[e]:
+//     s = softmax(l) or 1 / (1 + exp(-l));   v = s + bias
+//     group score = the best v of the group, or the sum of its two best
+//     the topk_group best groups stay (ties to the lower group)
+//     the top_k best v of these, ties to the lower id;  w = s_sel [/ sum s_sel] * scaling
+// An expert whose logit or bias is -inf takes no part.  Without a bias the
+// logits rank the experts: scores are monotone in them, and where scores
+// underflow or saturate to one value the logits still tell them apart.
+//
+// One warp a position, E / 32 experts a lane (expert lane + 32 i) in registers.
+// Scores become integers of the same order (0: takes no part), so that a round
+// of the top-k is two warp reductions (redux): the largest key, then the lowest
+// id that has it.  Groups of whole warps take the same reductions; others are
+// scanned by one lane each in shared memory.  All sums are fp32.
+#include "mx4_common.cuh"
+
+namespace colimoe {
+cudaError_t launch_route_partials(const float* x, int T, int H, const float* wr, int E, float* part, uint32_t* status, int* splits, cudaStream_t st);
+
+namespace {
+
+struct SelectParams {
+  const void* x;      // logits, or the router product's partial sums [splits][T][E]
+  long long ldx;
+  int splits;
+  const float* bias;
+  int T, E, G, per, keep, k, softmax, top2, renorm;
+  uint32_t gmul;      // e / per as (e * gmul) >> 20: exact for e < 1024
+  float scaling;
+  int32_t* idx;
+  float* w;
+  uint32_t* status;   // may be null
+};
+
+// floats as unsigned integers of the same order; -0 counts as +0
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+
+// V: experts a lane; PART: x holds partial sums of the router product
+template <int V, typename TY, bool PART>
+__global__ void __launch_bounds__(256) select_kernel(const SelectParams P) {
+  extern __shared__ float sm_sel[];  // [warps][E] scores, where groups are not whole warps
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int E = P.E;
+  const float NONE = -INFINITY;
+  float b[V];
+  bool bias_bad = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
+    b[i] = P.bias && e < E ? __ldg(P.bias + e) : 0.f;
+    bias_bad |= !(b[i] < INFINITY);
+  }
+  pdl_wait();
+  pdl_trigger();
+  for (long long t = (long long)blockIdx.x * warps + warp; t < P.T; t += (long long)gridDim.x * warps) {
+    float l[V], s[V];
+    if (PART) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = 0.f;
+      const float* p = static_cast<const float*>(P.x) + t * E;
+      for (int z = 0; z < P.splits; ++z, p += (long long)P.T * E)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (lane + 32 * i < E) l[i] += __ldcg(p + lane + 32 * i);
+    } else {
+      const TY* p = static_cast<const TY*>(P.x) + t * P.ldx;
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < E ? to_f32(p[lane + 32 * i]) : NONE;
+    }
+    bool bad = bias_bad;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (PART && lane + 32 * i >= E) l[i] = NONE;
+      bad |= !(l[i] < INFINITY);
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      if (lane < P.k) {
+        P.idx[t * P.k + lane] = -1;
+        P.w[t * P.k + lane] = 0.f;
+      }
+      if (lane == 0 && P.status) atomicOr(P.status, COLI_STATUS_NONFINITE);
+      continue;
+    }
+    if (P.softmax) {
+      float m = NONE, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+      m = warp_max(m);
+      if (m == NONE) m = 0.f;  // no expert takes part
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[i] = expf(l[i] - m);
+        sum += s[i];
+      }
+      sum = warp_sum(sum);
+      const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] *= inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {  // no overflow on either side
+        const float x = expf(-fabsf(l[i])), q = __fdividef(1.f, 1.f + x);
+        s[i] = l[i] >= 0.f ? q : x * q;
+      }
+    }
+    uint32_t key[V];
+    if (P.keep < P.G) {
+      float mine = NONE;  // lane g: score of group g
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float v = l[i] == NONE ? NONE : s[i] + b[i];
+        key[i] = v == NONE ? 0u : order_key(v);
+      }
+      if (P.per % 32 == 0) {
+        const int span = P.per / 32;
+        uint32_t a1 = 0, a2 = 0;  // the group's two best
+        int g = 0, in = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const uint32_t m1 = __reduce_max_sync(0xffffffffu, key[i]);
+          const uint32_t who = __ballot_sync(0xffffffffu, key[i] == m1);
+          const uint32_t m2 = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? 0u : key[i]);
+          a2 = max(max(a2, m2), min(a1, m1));
+          a1 = max(a1, m1);
+          if (++in == span) {
+            if (lane == g) mine = a1 == 0 ? NONE : key_value(a1) + (P.top2 && a2 ? key_value(a2) : 0.f);
+            a1 = a2 = 0;
+            in = 0;
+            ++g;
+          }
+        }
+      } else {
+        float* row = sm_sel + warp * E;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (lane + 32 * i < E) row[lane + 32 * i] = l[i] == NONE ? NONE : s[i] + b[i];
+        __syncwarp();
+        if (lane < P.G) {
+          float a1 = NONE, a2 = NONE;
+          for (int j = 0; j < P.per; ++j) {
+            const float v = row[lane * P.per + j];
+            a2 = fmaxf(a2, fminf(a1, v));
+            a1 = fmaxf(a1, v);
+          }
+          mine = a1 + (P.top2 && a2 != NONE ? a2 : 0.f);
+        }
+        __syncwarp();
+      }
+      const uint32_t mk = lane < P.G && mine != NONE ? order_key(mine) : 0u;
+      int before = 0;
+      for (int g = 0; g < P.G; ++g) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mk, g);
+        before += other > mk || (other == mk && g < lane);
+      }
+      const uint32_t kept = __ballot_sync(0xffffffffu, lane < P.G && before < P.keep);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t g = ((uint32_t)(lane + 32 * i) * P.gmul) >> 20;
+        if (!P.bias && key[i]) key[i] = order_key(l[i]);
+        if (g >= 32 || !(kept >> g & 1u)) key[i] = 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float v = P.bias ? s[i] + b[i] : l[i];
+        key[i] = l[i] == NONE || v == NONE ? 0u : order_key(v);
+      }
+    }
+    int my_id = -1;
+    float my_w = 0.f, sum = 0.f;
+    for (int j = 0; j < P.k; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) best = max(best, key[i]);
+      best = __reduce_max_sync(0xffffffffu, best);
+      if (best == 0u) break;  // no more experts take part
+      uint32_t id = 0xffffu;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (key[i] == best) id = lane + 32 * i;
+      id = __reduce_min_sync(0xffffffffu, id);
+      const int at = id >> 5;
+      float sv = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == at) {
+          sv = s[i];
+          if (lane == (int)(id & 31u)) key[i] = 0u;
+        }
+      sv = __shfl_sync(0xffffffffu, sv, id & 31u);
+      sum += sv;
+      if (lane == j) {
+        my_id = (int)id;
+        my_w = sv;
+      }
+    }
+    if (P.renorm) my_w = sum > 0.f ? __fdiv_rn(my_w, sum) : 0.f;
+    if (lane < P.k) {
+      P.idx[t * P.k + lane] = my_id;
+      P.w[t * P.k + lane] = my_w * P.scaling;
+    }
+  }
+}
+
+template <typename TY, bool PART>
+cudaError_t launch_select_t(const SelectParams& P, cudaStream_t st) {
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int warps = P.T <= 4 * sms ? 1 : 4;
+  long long grid = ((long long)P.T + warps - 1) / warps;
+  if (grid > 16LL * sms) grid = 16LL * sms;
+  const size_t smem = P.keep < P.G && P.per % 32 ? (size_t)warps * P.E * 4 : 0;
+  auto go = [&](auto kernel) { return launch_pdl(kernel, (unsigned)grid, 32u * warps, smem, st, P); };
+  if (P.E <= 32) return go(select_kernel<1, TY, PART>);
+  if (P.E <= 64) return go(select_kernel<2, TY, PART>);
+  if (P.E <= 128) return go(select_kernel<4, TY, PART>);
+  if (P.E <= 256) return go(select_kernel<8, TY, PART>);
+  if (P.E <= 512) return go(select_kernel<16, TY, PART>);
+  return go(select_kernel<32, TY, PART>);
+}
+
+int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+size_t partial_bytes(int T, int H, int E) {
+  const size_t splits = T <= ROUTE_GEMV_MAX_T ? (size_t)GEMV_SPLITS : (size_t)route_ksplits(T, H, E);
+  return splits * (size_t)T * (size_t)E * 4;
+}
+
+}  // namespace
+}  // namespace colimoe
+
+using namespace colimoe;
+
+extern "C" size_t coli_moe_select_workspace_size(int32_t max_T, int32_t hidden, int32_t n_experts) {
+  if (max_T < 0 || hidden < 1 || hidden % 16 || n_experts < 1 || n_experts > MAX_E) return 0;
+  // (fewer positions can take more splits, and then more room in all)
+  const size_t few = partial_bytes(max_T < ROUTE_GEMV_MAX_T ? max_T : ROUTE_GEMV_MAX_T, hidden, n_experts);
+  size_t most = few;
+  // splits fall with the number of 64-row tiles: the largest product is at the end of some tile
+  for (long long t = 64; t < (long long)max_T + 64 && most < (size_t)-1; t += 64) {
+    const int T = (int)(t < max_T ? t : max_T);
+    const size_t n = partial_bytes(T, hidden, n_experts);
+    if (n > most) most = n;
+    if (route_ksplits(T, hidden, n_experts) == 1) {  // from here on it grows with T
+      const size_t last = (size_t)max_T * n_experts * 4;
+      if (last > most) most = last;
+      break;
+    }
+  }
+  return align_up(WS_HEADER_BYTES + most, 256);
+}
+
+extern "C" int coli_moe_select(const coli_moe_select_args* a, int32_t T, cudaStream_t stream) {
+  if (!a || T < 0) return COLI_EINVAL;
+  if (a->n_experts < 1 || a->n_groups < 1 || a->top_k < 1) return COLI_EINVAL;
+  if (a->n_experts > MAX_E || a->n_groups > MAX_GROUPS || a->top_k > MAX_TOPK) return COLI_EUNSUPPORTED;
+  if (a->n_experts % a->n_groups || a->topk_group < 1 || a->topk_group > a->n_groups) return COLI_EINVAL;
+  if (a->top_k > a->topk_group * (a->n_experts / a->n_groups)) return COLI_EINVAL;
+  if ((a->score != COLI_SCORE_SIGMOID && a->score != COLI_SCORE_SOFTMAX) || (a->group_score != COLI_GROUP_TOP2 && a->group_score != COLI_GROUP_MAX))
+    return COLI_EINVAL;
+  if (!(a->scaling == a->scaling)) return COLI_EINVAL;
+  const bool product = a->router_w != nullptr;
+  if (product ? a->type != COLI_F32 || a->hidden < 1 || a->hidden % 16 || a->ldx != a->hidden : !float_type(a->type) || a->ldx < a->n_experts)
+    return COLI_EINVAL;
+  if (T == 0) return COLI_OK;
+  if (!a->x || !a->topk_idx || !a->topk_w || (product && !a->ws)) return COLI_EINVAL;
+  const void* ptrs[] = {a->x, a->router_w, a->bias, a->topk_idx, a->topk_w, a->ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return COLI_EALIGN;
+  if (a->ws && a->ws_bytes < 256) return COLI_EWORKSPACE;
+  if (product && a->ws_bytes < WS_HEADER_BYTES + partial_bytes(T, a->hidden, a->n_experts)) return COLI_EWORKSPACE;
+  SelectParams P{};
+  P.x = a->x;
+  P.ldx = a->ldx;
+  P.bias = a->bias;
+  P.T = T;
+  P.E = a->n_experts;
+  P.G = a->n_groups;
+  P.per = a->n_experts / a->n_groups;
+  P.keep = a->topk_group;
+  P.k = a->top_k;
+  P.softmax = a->score == COLI_SCORE_SOFTMAX;
+  P.top2 = a->group_score == COLI_GROUP_TOP2;
+  P.renorm = a->renorm != 0;
+  P.gmul = (1u << 20) / (uint32_t)P.per + 1u;
+  P.scaling = a->scaling;
+  P.idx = a->topk_idx;
+  P.w = a->topk_w;
+  P.status = static_cast<uint32_t*>(a->ws);
+  if (product) {
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->ws) + WS_HEADER_BYTES);
+    const cudaError_t e = launch_route_partials(static_cast<const float*>(a->x), T, a->hidden, a->router_w, a->n_experts, part, P.status, &P.splits, stream);
+    if (e != cudaSuccess) return COLI_ECUDA;
+    P.x = part;
+    return rc_of(launch_select_t<float, true>(P, stream));
+  }
+  if (a->type == COLI_F32) return rc_of(launch_select_t<float, false>(P, stream));
+  if (a->type == COLI_BF16) return rc_of(launch_select_t<__nv_bfloat16, false>(P, stream));
+  return rc_of(launch_select_t<__half, false>(P, stream));
+}

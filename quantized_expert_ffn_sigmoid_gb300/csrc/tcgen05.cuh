@@ -113,4 +113,67 @@ __device__ __forceinline__ bool pf_wait_poll(uint64_t* bar, uint32_t parity, uin
   return false;
 }
 
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// A commit issued by the lane whose `leader` is set, executed by a whole converged warp.
+__device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(leader) : "memory");
+}
+// A bounded wait that gives up at once after any wait of the CTA has expired
+// (the abort flag), so that a broken pipeline drains.  Without a suspend-time
+// hint, with which a thread wakes late, and not polling, which takes issue
+// slots from the epilogue: one position took 45.3 us against 47.2 with the
+// scale writers and the MMA warp polling.
+__device__ __forceinline__ bool gwait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+  for (uint32_t i = 0; i < SPIN_LIMIT; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  atomicOr(status, COLI_STATUS_TIMEOUT);
+  return false;
+}
+
+// kind::f16, fp16 x fp16 -> fp32, both K-major, M = 128
+__device__ __forceinline__ uint32_t umma_idesc(int n) {
+  return (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <uint32_t N>
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2_u32(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// 8 int8 codes (two words) -> 8 fp16 in storage order: the byte with its sign
+// bit flipped is code + 128; 0x6400 | that is 1024 + code + 128; minus 1152.
+__device__ __forceinline__ void cvt_int8x8(uint32_t w0, uint32_t w1, uint32_t* o) {
+  const uint32_t x0 = w0 ^ 0x80808080u, x1 = w1 ^ 0x80808080u;
+  const uint32_t k = 0x64646464u, off = 0x64806480u;
+  o[0] = hsub2_u32(prmt(x0, k, 0x4140u), off);
+  o[1] = hsub2_u32(prmt(x0, k, 0x4342u), off);
+  o[2] = hsub2_u32(prmt(x1, k, 0x4140u), off);
+  o[3] = hsub2_u32(prmt(x1, k, 0x4342u), off);
+}
+
 }  // namespace colimoe
