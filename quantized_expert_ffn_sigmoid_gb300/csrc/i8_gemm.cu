@@ -14,8 +14,8 @@
 //
 // One persistent CTA an SM, 20 warps meeting at mbarriers, every wait bounded:
 //   warp 0       TMA of weight codes, slots of 128 rows x 128 codes;
-//   warp 1       TMA of activations, slots of up to NT rows x 64 codes;
-//   warp 2       MMA issuer, blocks of K = 64;
+//   warp 1       TMA of activations, slots of up to NT rows x BK codes;
+//   warp 2       MMA issuer, blocks of BK codes;
 //   warps 4-11   converters, two sets of four (a warp for each lane quarter)
 //                that take the blocks in turn: a block's way through registers
 //                takes longer than its products;
@@ -31,26 +31,30 @@ namespace colimoe {
 namespace {
 
 constexpr int IG_M = 128;                    // weight rows of a tile
-constexpr int IG_WK = 128, IG_BK = 64;       // codes of a weight slot's row, of a block
+constexpr int IG_WK = 128;                   // codes of a weight slot's row
 constexpr uint32_t IG_WSLOT = IG_M * IG_WK;  // 16 KB
-constexpr int IG_AS = 4;                     // blocks of widened weights in tensor memory
-constexpr uint32_t IG_ACOL = 3 * 128;        // their first column
-constexpr int IG_RUN = 1024 / IG_BK;         // blocks of an exact run
+constexpr int IG_RUN = 1024;                 // codes of an exact run
 constexpr int IG_MB = 8;                     // weight tiles that share activation tiles while they are in L2
 constexpr int IG_THREADS = 640;
 constexpr int IG_RCTL = 40, IG_RCONV = 56, IG_REPI = 160;
 constexpr int IG_MAX_SMEM = 227 * 1024;
 constexpr int IG_MAXW = 10, IG_MAXB = 12;
 
-// NT: activation rows of a tile at most.  Slots fill 208 KB.
+// NT: activation rows of a tile at most; BK: codes of a block, the unit in
+// which operands pass to the MMA warp.  Slots fill 208 KB.
 template <int NT>
 struct IgShape {
-  static constexpr int NW = NT == 32 ? 10 : NT == 64 ? 8 : NT == 128 ? 5 : 3;
-  static constexpr int NB = NT == 32 ? 12 : NT == 64 ? 10 : NT == 128 ? 8 : 5;
-  static constexpr uint32_t BSLOT = NT * IG_BK * 2;
+  static constexpr int BK = NT <= 64 ? 256 : NT == 128 ? 128 : 64;
+  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 5 : 3;
+  static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 4 : 5;
+  static constexpr uint32_t BSLOT = NT * BK * 2;
   static constexpr uint32_t BARS = NW * IG_WSLOT + NB * BSLOT;
   static constexpr uint32_t TABLES = BARS + 512;
   static constexpr int COLS = NT == 256 ? 128 : NT / 2;  // columns of an epilogue warp
+  // tensor memory: accumulators, then AS blocks of widened weights
+  static constexpr int ACCS = NT == 256 ? 3 : 2, ACCW = NT < 128 ? NT : 128;
+  static constexpr int ACOL = NT == 256 ? 384 : 256, AW = BK / 2, AS = (512 - ACOL) / AW;
+  static_assert(ACCS * ACCW <= ACOL && AS >= 2 && AS <= NB, "tensor memory");
 };
 template <int NT>
 constexpr size_t ig_smem(int G) { return IgShape<NT>::TABLES + 8 * (size_t)(G + 1) + 1024; }
@@ -82,6 +86,7 @@ __device__ __forceinline__ void umma_f16_if(uint32_t d, uint32_t a, uint64_t b, 
 
 // Which accumulator a half of the tile uses and which comes next.  Every role
 // follows the same sequence: `turn` when a half's run ends.
+template <int N>
 struct IgSlots {
   int cur0 = 0, cur1 = 1, spare = 2;
   uint32_t uses = 0;  // bit s: parity of the runs that accumulator s has held
@@ -89,6 +94,10 @@ struct IgSlots {
   __device__ __forceinline__ void turn(bool halves) {
     const int old = H == 0 ? cur0 : cur1;
     uses ^= 1u << old;
+    if (N == 2) {  // no halves: two accumulators in turn
+      cur0 ^= 1;
+      return;
+    }
     if (H == 0) cur0 = spare; else cur1 = spare;
     spare = old;
     if (!halves) {  // one half: all three in rotation
@@ -105,16 +114,15 @@ struct IgItem {
 template <int NT>
 __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__ IgMaps maps, const I8Params A, const uint32_t off_xs) {
   using S = IgShape<NT>;
-  constexpr int NW = S::NW, NB = S::NB;
+  constexpr int NW = S::NW, NB = S::NB, BK = S::BK;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<size_t>(sm_raw), 1024));
   uint8_t* sm_b = sm + NW * IG_WSLOT;
   uint64_t* full_w = reinterpret_cast<uint64_t*>(sm + S::BARS);  // [NW] weight codes landed
   uint64_t* empty_w = full_w + IG_MAXW;                          // [NW] all converters have read them
-  uint64_t* full_b = empty_w + IG_MAXW;                          // [NB] activations landed
+  uint64_t* full_b = empty_w + IG_MAXW;                          // [NB] a block: activations landed, weights in tensor memory
   uint64_t* done = full_b + IG_MAXB;                             // [NB] the block's products are complete
-  uint64_t* a_full = done + IG_MAXB;                             // [IG_AS] a block of weights is in tensor memory
-  uint64_t* d_full = a_full + IG_AS;                             // [3] a run is complete
+  uint64_t* d_full = done + IG_MAXB;                             // [3] a run is complete
   uint64_t* d_empty = d_full + 3;                                // [3] it has been read
   uint64_t* fin = d_empty + 3;
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(fin + 1);
@@ -122,8 +130,9 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   int* s_row0 = reinterpret_cast<int*>(sm + S::TABLES);          // [G + 1] first row of a group
   int* s_tiles = s_row0 + A.G + 1;                               // [G + 1] activation tiles before it
   uint32_t* status = reinterpret_cast<uint32_t*>(A.ws);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nblk = (A.K + IG_BK - 1) / IG_BK;
+  // (broadcast, so that the compiler knows them to be the same in every lane of a warp)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int nblk = (A.K + BK - 1) / BK;
   const int mt = (A.N + IG_M - 1) / IG_M;
 
   if (threadIdx.x == 0) {
@@ -132,10 +141,9 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       mbar_init(&empty_w[i], 8);
     }
     for (int i = 0; i < NB; ++i) {
-      mbar_init(&full_b[i], 1);
+      mbar_init(&full_b[i], 1 + 4 * (BK / 64));
       mbar_init(&done[i], 1);
     }
-    for (int i = 0; i < IG_AS; ++i) mbar_init(&a_full[i], 4);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&d_full[i], 1);
       mbar_init(&d_empty[i], NT == 256 ? 4 : 8);
@@ -180,8 +188,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t taddr = *s_taddr;
-  const int items = s_tiles[A.G] * mt;
+  const uint32_t taddr = __shfl_sync(0xffffffffu, *s_taddr, 0);
+  const int items = __shfl_sync(0xffffffffu, s_tiles[A.G] * mt, 0);
 
   // Items of a group: IG_MB weight tiles for each activation tile, so that the
   // CTAs at work together share both operands in L2.
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       for (int item = blockIdx.x; item < items && go; item += gridDim.x) {
         const IgItem it = item_at(item);
         const bool once = s_tiles[it.g + 1] - s_tiles[it.g] == 1;  // read for one activation tile alone
-        for (int st = 0; 2 * st < nblk; ++st, ++gs) {
+        for (int st = 0; st < (nblk * BK + IG_WK - 1) / IG_WK; ++st, ++gs) {  // (beyond K: zeros)
           const uint32_t s = gs % NW;
           if (!gwait(&empty_w[s], ((gs / NW) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
           mbar_arrive_expect_tx(&full_w[s], IG_WSLOT);
@@ -221,7 +229,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           else tma_load_3d(sm + s * IG_WSLOT, &maps.w, st * IG_WK, it.n0, it.g, &full_w[s]);
         }
       }
-      // every copy issued has landed before the CTA can exit
+      // every copy issued has landed before the CTA can exit (after an abort a
+      // phase may lack the other warps' arrivals: the wait is bounded)
       for (uint32_t k = gs > (uint32_t)NW ? gs - NW : 0; k < gs; ++k)
         for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full_w[k % NW], (k / NW) & 1u); ++i) {
         }
@@ -236,11 +245,13 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         for (int j = 0; j < nblk; ++j, ++gs) {
           const uint32_t s = gs % NB;
           if (!gwait(&done[s], ((gs / NB) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
-          mbar_arrive_expect_tx(&full_b[s], (uint32_t)n16 * 2048);
+          mbar_arrive_expect_tx(&full_b[s], (uint32_t)n16 * 2048 * (BK / 64));
           int row = 0;
           for (int left = n16; left > 0;) {  // the rows in boxes of 128, 64, 32, 16
             const int i = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
-            tma_load_2d(sm_b + s * S::BSLOT + row * 128, &maps.x[i], j * IG_BK, it.row0 + row, &full_b[s]);
+#pragma unroll
+            for (int c = 0; c < BK / 64; ++c)
+              tma_load_2d(sm_b + s * S::BSLOT + c * (NT * 128) + row * 128, &maps.x[i], j * BK + 64 * c, it.row0 + row, &full_b[s]);
             row += 16 << i;
             left -= 1 << i;
           }
@@ -253,48 +264,59 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       // -------------------------------------------------------- MMA issuer
       // (the whole warp runs the loop, one elected lane issues: operands stay
       // in uniform registers)
+      // A block waits at one barrier, looked at while the block before is under
+      // way: this loop, not the instructions, is what small tiles wait for.
       const uint32_t leader = elect_one();
-      IgSlots D;
-      uint32_t gb = 0;
+      const uint64_t db0 = umma_desc_sw128(smem_u32(sm_b));
+      IgSlots<S::ACCS> D;
+      uint32_t s = 0, ph = 0, a = 0;
+      bool ready = false, ok = true;
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const IgItem it = item_at(item);
-        const bool halves = NT == 256 && it.ntok > 128;
-        const uint32_t id0 = umma_idesc((min(it.ntok, 128) + 15) & ~15), id1 = umma_idesc((max(it.ntok - 128, 16) + 15) & ~15);
-        bool fresh0 = true, fresh1 = true, ok = true;
-        for (int j = 0; j < nblk; ++j, ++gb) {
-          const uint32_t s = gb % NB, a = gb % IG_AS;
-          if (fresh0) ok = ok && gwait(&d_empty[D.cur0], (D.uses >> D.cur0 & 1u) ^ 1u, status, s_abort);
-          ok = ok && gwait(&full_b[s], (gb / NB) & 1u, status, s_abort) && gwait(&a_full[a], (gb / IG_AS) & 1u, status, s_abort);
-          const uint32_t ac = taddr + IG_ACOL + a * 32;
-          const uint64_t db = umma_desc_sw128(smem_u32(sm_b) + s * S::BSLOT);
-          if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
-            tmem_fence_after();
+        const int ntok = __shfl_sync(0xffffffffu, item_at(item).ntok, 0);
+        const bool halves = NT == 256 && ntok > 128;
+        const uint32_t id0 = umma_idesc((min(ntok, 128) + 15) & ~15), id1 = umma_idesc((max(ntok - 128, 16) + 15) & ~15);
+        uint32_t acc0 = 0, acc1 = 0;  // whether the run has begun
+        int left = IG_RUN / BK;       // blocks to the end of half 0's run
+        for (int j = nblk; j > 0; --j) {
+          if (acc0 == 0) ok = __all_sync(0xffffffffu, gwait(&d_empty[D.cur0], (D.uses >> D.cur0 & 1u) ^ 1u, status, s_abort)) && ok;
+          if (!ready) ok = __all_sync(0xffffffffu, gwait(&full_b[s], ph, status, s_abort)) && ok;
+          const uint32_t go = ok ? leader : 0u;  // (aborted: the results are flagged invalid; issue nothing)
+          const uint32_t ac = taddr + S::ACOL + a * S::AW, d0 = taddr + D.cur0 * S::ACCW;
+          const uint64_t db = db0 + s * (S::BSLOT >> 4);
+          tmem_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f16_if(taddr + D.cur0 * 128, ac + 8 * k, db + 2 * k, id0, (uint32_t)(k > 0 || !fresh0), leader);
-          }
-          fresh0 = false;
+          for (int k = 0; k < BK / 16; ++k)
+            umma_f16_if(d0, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), id0, k ? 1u : acc0, go);
+          acc0 = 1;
           if (NT == 256 && halves) {
-            if (fresh1) ok = ok && gwait(&d_empty[D.cur1], (D.uses >> D.cur1 & 1u) ^ 1u, status, s_abort);
-            if (ok) {
+            if (acc1 == 0) {
+              ok = __all_sync(0xffffffffu, gwait(&d_empty[D.cur1], (D.uses >> D.cur1 & 1u) ^ 1u, status, s_abort)) && ok;
               tmem_fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_f16_if(taddr + D.cur1 * 128, ac + 8 * k, db + 128 * 128 / 16 + 2 * k, id1, (uint32_t)(k > 0 || !fresh1), leader);
             }
-            fresh1 = false;
+            const uint32_t d1 = taddr + D.cur1 * S::ACCW;
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              umma_f16_if(d1, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 128 * 128 / 16 + 2 * (k & 3), id1, k ? 1u : acc1, ok ? go : 0u);
+            acc1 = 1;
           }
           umma_commit_if(&done[s], leader);
-          const bool last = j + 1 == nblk;
-          if (last || (j + 1) % IG_RUN == 0) {
-            umma_commit_if(&d_full[D.cur0], leader);
-            D.turn<0>(halves);
-            fresh0 = true;
+          a = (a + 1) % S::AS;
+          if (++s == (uint32_t)NB) {
+            s = 0;
+            ph ^= 1u;
           }
-          if (NT == 256 && halves && (last || (j + 1) % IG_RUN == IG_RUN / 2)) {  // half a run apart, so that one
-            umma_commit_if(&d_full[D.cur1], leader);                            // spare accumulator serves both
-            D.turn<1>(halves);
-            fresh1 = true;
+          ready = __all_sync(0xffffffffu, mbar_test_wait(&full_b[s], ph));
+          --left;
+          if (left == 0 || j == 1) {
+            umma_commit_if(&d_full[D.cur0], leader);
+            D.template turn<0>(halves);
+            acc0 = 0;
+            left = IG_RUN / BK;
+          }
+          if (NT == 256 && halves && (left == IG_RUN / BK / 2 || j == 1)) {  // half a run apart, so that one spare
+            umma_commit_if(&d_full[D.cur1], leader);                    // accumulator serves both
+            D.template turn<1>(halves);
+            acc1 = 0;
           }
         }
       }
@@ -309,21 +331,18 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     const int set = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
     uint32_t gs = 0, gb = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-      for (int st = 0; 2 * st < nblk; ++st, ++gs) {
+      for (int c = set; c < nblk * (BK / 64) + set; c += 2, ++gs) {  // chunks of 64 codes
         const uint32_t s = gs % NW;
         gwait(&full_w[s], (gs / NW) & 1u, status, s_abort);
-        const int j = 2 * st + set;
         uint4 w[4];
-        if (j < nblk) {
-          const uint8_t* row = sm + s * IG_WSLOT + r * IG_WK;  // 16-byte unit c of row r at unit c ^ (r % 8)
+        const uint8_t* row = sm + s * IG_WSLOT + r * IG_WK;  // 16-byte unit c of row r at unit c ^ (r % 8)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(row + 16 * ((4 * set + i) ^ (r & 7)));
-        }
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(row + 16 * ((4 * set + i) ^ (r & 7)));
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty_w[s]);
-        if (j >= nblk) continue;
-        const uint32_t b = gb + j, a = b % IG_AS;
-        const uint32_t ta = taddr + ((uint32_t)(32 * q) << 16) + IG_ACOL + a * 32;
+        if (BK == 64 && c >= nblk) continue;  // the slot's second half is behind the last block
+        const uint32_t b = gb + c / (BK / 64);
+        const uint32_t ta = taddr + ((uint32_t)(32 * q) << 16) + S::ACOL + (b % S::AS) * S::AW + c % (BK / 64) * 32;
         uint32_t o[16];
         cvt_int8x8(w[0].x, w[0].y, o);
         cvt_int8x8(w[0].z, w[0].w, o + 4);
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         cvt_int8x8(w[1].z, w[1].w, o + 12);
         // the block that held these columns is done (that phase cannot have been
         // overtaken: the next block in its slot needs this one's weights first)
-        if (b >= (uint32_t)IG_AS) gwait(&done[(b - IG_AS) % NB], ((b - IG_AS) / NB) & 1u, status, s_abort);
+        if (b >= (uint32_t)S::AS) gwait(&done[(b - S::AS) % NB], ((b - S::AS) / NB) & 1u, status, s_abort);
         tmem_fence_after();
         __syncwarp();
         tmem_st16(ta, o);
@@ -343,7 +362,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&a_full[a]);
+        if (lane == 0) mbar_arrive(&full_b[b % NB]);
       }
       gb += nblk;
     }
@@ -353,7 +372,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     constexpr int COLS = S::COLS;
     const int set = (warp - 12) >> 2, q = warp & 3;
     const float* xs = reinterpret_cast<const float*>(A.ws + off_xs);
-    IgSlots D;
+    IgSlots<S::ACCS> D;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
       const IgItem it = item_at(item);
       const bool halves = NT == 256 && it.ntok > 128;
@@ -364,10 +383,10 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0;
       auto read_run = [&](int slot) {
-        gwait(&d_full[slot], D.uses >> slot & 1u, status, s_abort);
+        pf_wait(&d_full[slot], D.uses >> slot & 1u, status, s_abort);  // (long: suspended, out of the other warps' way)
         tmem_fence_after();
         __syncwarp();
-        const uint32_t t = taddr + ((uint32_t)(32 * q) << 16) + slot * 128 + (NT == 256 ? 0 : col0);
+        const uint32_t t = taddr + ((uint32_t)(32 * q) << 16) + slot * S::ACCW + (NT == 256 ? 0 : col0);
 #pragma unroll
         for (int c = 0; c < COLS; c += 16)
           if (c < cols) {
@@ -381,21 +400,22 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_empty[slot]);
       };
-      // the ends of runs in their order: half 0 at 16, 32, ... blocks, half 1 at 8, 24, ..., both at the end
-      for (int c = IG_RUN / 2; c < nblk; c += IG_RUN / 2) {
+      // the ends of runs in their order: half 0 after 1024, 2048, ... codes, half 1 after 512, 1536, ..., both at the end
+      constexpr int STEP = NT == 256 ? IG_RUN / 2 : IG_RUN;
+      for (int c = STEP; c < nblk * BK; c += STEP) {
         if (c % IG_RUN == 0) {
           if (half == 0) read_run(D.cur0);
-          D.turn<0>(halves);
+          D.template turn<0>(halves);
         } else if (halves) {
           if (half == 1) read_run(D.cur1);
-          D.turn<1>(halves);
+          D.template turn<1>(halves);
         }
       }
       if (half == 0) read_run(D.cur0);
-      D.turn<0>(halves);
+      D.template turn<0>(halves);
       if (halves) {
         if (half == 1) read_run(D.cur1);
-        D.turn<1>(halves);
+        D.template turn<1>(halves);
       }
       const int n = it.n0 + 32 * q + lane;
       const bool live = n < A.N;
@@ -492,7 +512,7 @@ bool encode_rows_f16(CUtensorMap* m, const void* base, int kp, int rows, int box
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)kp, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)kp * 2};
-  const cuuint32_t box[2] = {IG_BK, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
