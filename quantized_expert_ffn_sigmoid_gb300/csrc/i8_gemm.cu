@@ -74,14 +74,13 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* m
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;"
       ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy) : "memory");
 }
-// D[tmem] (+)= A[tmem] x B[smem], issued by the lane whose `leader` is set
-__device__ __forceinline__ void umma_f16_if(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
+// D[tmem] (+)= A[tmem] x B[smem]
+__device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "setp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader) : "memory");
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
 // Which accumulator a half of the tile uses and which comes next.  Every role
@@ -262,10 +261,10 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         }
     } else if (warp == 2) {
       // -------------------------------------------------------- MMA issuer
-      // (the whole warp runs the loop, one elected lane issues: operands stay
-      // in uniform registers)
-      // A block waits at one barrier, looked at while the block before is under
-      // way: this loop, not the instructions, is what small tiles wait for.
+      // (one elected lane issues a block's instructions inside a branch: 21
+      // cycles an instruction; issued by a predicated lane of the whole warp
+      // behind a wait they took 57, with operands copied one by one.  A block
+      // waits at one barrier, looked at while the block before is under way)
       const uint32_t leader = elect_one();
       const uint64_t db0 = umma_desc_sw128(smem_u32(sm_b));
       IgSlots<S::ACCS> D;
@@ -278,50 +277,57 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         uint32_t acc0 = 0, acc1 = 0;  // whether the run has begun
         int left = IG_RUN / BK;       // blocks to the end of half 0's run
         for (int j = nblk; j > 0; --j) {
-          if (acc0 == 0) ok = __all_sync(0xffffffffu, gwait(&d_empty[D.cur0], (D.uses >> D.cur0 & 1u) ^ 1u, status, s_abort)) && ok;
-          if (!ready) ok = __all_sync(0xffffffffu, gwait(&full_b[s], ph, status, s_abort)) && ok;
-          const uint32_t go = ok ? leader : 0u;  // (aborted: the results are flagged invalid; issue nothing)
+          if (acc0 == 0) ok = gwait(&d_empty[D.cur0], (D.uses >> D.cur0 & 1u) ^ 1u, status, s_abort) && ok;
+          if (!ready) ok = gwait(&full_b[s], ph, status, s_abort) && ok;
           const uint32_t ac = taddr + S::ACOL + a * S::AW, d0 = taddr + D.cur0 * S::ACCW;
           const uint64_t db = db0 + s * (S::BSLOT >> 4);
           tmem_fence_after();
-#pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_f16_if(d0, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), id0, k ? 1u : acc0, go);
-          acc0 = 1;
-          if (NT == 256 && halves) {
-            if (acc1 == 0) {
-              ok = __all_sync(0xffffffffu, gwait(&d_empty[D.cur1], (D.uses >> D.cur1 & 1u) ^ 1u, status, s_abort)) && ok;
-              tmem_fence_after();
-            }
-            const uint32_t d1 = taddr + D.cur1 * S::ACCW;
-#pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              umma_f16_if(d1, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 128 * 128 / 16 + 2 * (k & 3), id1, k ? 1u : acc1, ok ? go : 0u);
-            acc1 = 1;
+          if (NT == 256 && halves && acc1 == 0) {
+            ok = gwait(&d_empty[D.cur1], (D.uses >> D.cur1 & 1u) ^ 1u, status, s_abort) && ok;
+            tmem_fence_after();
           }
-          umma_commit_if(&done[s], leader);
+          __syncwarp();
+          --left;
+          const bool end0 = left == 0 || j == 1, end1 = NT == 256 && halves && (left == IG_RUN / BK / 2 || j == 1);
+          if (leader) {
+            if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k)
+                umma_f16(d0, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), id0, k ? 1u : acc0);
+              if (NT == 256 && halves) {
+                const uint32_t d1 = taddr + D.cur1 * S::ACCW;
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k)
+                  umma_f16(d1, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 128 * 128 / 16 + 2 * (k & 3), id1, k ? 1u : acc1);
+              }
+            }
+            umma_commit(&done[s]);
+            if (end0) umma_commit(&d_full[D.cur0]);
+            if (end1) umma_commit(&d_full[D.cur1]);
+          }
+          __syncwarp();
+          acc0 = 1;
+          acc1 = 1;
           a = (a + 1) % S::AS;
           if (++s == (uint32_t)NB) {
             s = 0;
             ph ^= 1u;
           }
-          ready = __all_sync(0xffffffffu, mbar_test_wait(&full_b[s], ph));
-          --left;
-          if (left == 0 || j == 1) {
-            umma_commit_if(&d_full[D.cur0], leader);
+          ready = mbar_test_wait(&full_b[s], ph);
+          if (end0) {
             D.template turn<0>(halves);
             acc0 = 0;
             left = IG_RUN / BK;
           }
-          if (NT == 256 && halves && (left == IG_RUN / BK / 2 || j == 1)) {  // half a run apart, so that one spare
-            umma_commit_if(&d_full[D.cur1], leader);                    // accumulator serves both
+          if (end1) {  // half a run apart, so that one spare accumulator serves both
             D.template turn<1>(halves);
             acc1 = 0;
           }
         }
       }
       // every MMA issued has completed before the accumulators are freed
-      umma_commit_if(fin, leader);
+      if (leader) umma_commit(fin);
+      __syncwarp();
       for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(fin, 0u); ++i) {
       }
     }
