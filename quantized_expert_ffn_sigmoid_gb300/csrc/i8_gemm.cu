@@ -36,26 +36,27 @@ constexpr uint32_t IG_WSLOT = IG_M * IG_WK;  // 16 KB
 constexpr int IG_RUN = 1024;                 // codes of an exact run
 constexpr int IG_MB = 8;                     // weight tiles that share activation tiles while they are in L2
 constexpr int IG_THREADS = 640;
-constexpr int IG_RCTL = 40, IG_RCONV = 56, IG_REPI = 160;
+constexpr int IG_RCTL = 32, IG_RCONV = 64, IG_REPI = 160;
 constexpr int IG_MAX_SMEM = 227 * 1024;
-constexpr int IG_MAXW = 10, IG_MAXB = 12;
+constexpr int IG_MAXW = 9, IG_MAXB = 5;
 
 // NT: activation rows of a tile at most; BK: codes of a block, the unit in
 // which operands pass to the MMA warp.  Slots fill 208 KB.
 template <int NT>
 struct IgShape {
-  static constexpr int BK = NT <= 64 ? 256 : NT == 128 ? 128 : 64;
+  static constexpr int BK = NT == 256 ? 64 : NT == 128 ? 128 : 256;
   static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 5 : 3;
   static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 4 : 5;
   static constexpr uint32_t BSLOT = NT * BK * 2;
   static constexpr uint32_t BARS = NW * IG_WSLOT + NB * BSLOT;
   static constexpr uint32_t TABLES = BARS + 512;
-  static constexpr int COLS = NT == 256 ? 128 : NT / 2;  // columns of an epilogue warp
+  static constexpr int COLS = NT / 2;                          // columns of an epilogue warp
+  static constexpr int KSTEP = BK < IG_WK ? IG_WK : BK;        // K is filled up with zeros to a multiple of this
   // tensor memory: accumulators, then AS blocks of widened weights
-  static constexpr int ACCS = NT == 256 ? 3 : 2, ACCW = NT < 128 ? NT : 128;
-  static constexpr int ACOL = NT == 256 ? 384 : 256, AW = BK / 2, AS = (512 - ACOL) / AW;
-  static_assert(ACCS * ACCW <= ACOL && AS >= 2 && AS <= NB, "tensor memory");
+  static constexpr int ACCS = NT == 256 ? 1 : 2, AW = BK / 2, AS = NT <= 64 ? 2 : 4;
+  static_assert(ACCS * NT <= 256 && AS * AW <= 256 && AS <= NB, "tensor memory");
 };
+constexpr int IG_ACOL = 256;                 // first column of the widened weights
 template <int NT>
 constexpr size_t ig_smem(int G) { return IgShape<NT>::TABLES + 8 * (size_t)(G + 1) + 1024; }
 
@@ -74,6 +75,11 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* m
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;"
       ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy) : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 // D[tmem] (+)= A[tmem] x B[smem]
 __device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -83,72 +89,51 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uin
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
-// Which accumulator a half of the tile uses and which comes next.  Every role
-// follows the same sequence: `turn` when a half's run ends.
-template <int N>
-struct IgSlots {
-  int cur0 = 0, cur1 = 1, spare = 2;
-  uint32_t uses = 0;  // bit s: parity of the runs that accumulator s has held
-  template <int H>
-  __device__ __forceinline__ void turn(bool halves) {
-    const int old = H == 0 ? cur0 : cur1;
-    uses ^= 1u << old;
-    if (N == 2) {  // no halves: two accumulators in turn
-      cur0 ^= 1;
-      return;
-    }
-    if (H == 0) cur0 = spare; else cur1 = spare;
-    spare = old;
-    if (!halves) {  // one half: all three in rotation
-      spare = cur1;
-      cur1 = old;
-    }
-  }
-};
-
 struct IgItem {
   int g, row0, ntok, n0;
 };
 
 template <int NT>
-__global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__ IgMaps maps, const I8Params A, const uint32_t off_xs) {
+__global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__ IgMaps maps, const I8Params A, const uint32_t off_xs, const int wide) {
   using S = IgShape<NT>;
   constexpr int NW = S::NW, NB = S::NB, BK = S::BK;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<size_t>(sm_raw), 1024));
   uint8_t* sm_b = sm + NW * IG_WSLOT;
   uint64_t* full_w = reinterpret_cast<uint64_t*>(sm + S::BARS);  // [NW] weight codes landed
-  uint64_t* empty_w = full_w + IG_MAXW;                          // [NW] all converters have read them
-  uint64_t* full_b = empty_w + IG_MAXW;                          // [NB] a block: activations landed, weights in tensor memory
-  uint64_t* done = full_b + IG_MAXB;                             // [NB] the block's products are complete
-  uint64_t* d_full = done + IG_MAXB;                             // [3] a run is complete
-  uint64_t* d_empty = d_full + 3;                                // [3] it has been read
-  uint64_t* fin = d_empty + 3;
+  uint64_t* empty_w = full_w + IG_MAXW;                          // [NW] the converters have read them
+  uint64_t* full = empty_w + IG_MAXW;                            // [NB] a block: activations landed, weights in tensor memory
+  uint64_t* done = full + IG_MAXB;                               // [NB] its products are complete
+  uint64_t* d_full = done + IG_MAXB;                             // [ACCS] a run is complete
+  uint64_t* d_empty = d_full + 2;                                // [ACCS] it has been read
+  uint64_t* fin = d_empty + 2;
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_taddr + 1);
+  uint32_t* s_most = s_taddr + 2;
   int* s_row0 = reinterpret_cast<int*>(sm + S::TABLES);          // [G + 1] first row of a group
   int* s_tiles = s_row0 + A.G + 1;                               // [G + 1] activation tiles before it
   uint32_t* status = reinterpret_cast<uint32_t*>(A.ws);
   // (broadcast, so that the compiler knows them to be the same in every lane of a warp)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int nblk = (A.K + BK - 1) / BK;
+  const int ksteps = (A.K + S::KSTEP - 1) / S::KSTEP, nblk = ksteps * (S::KSTEP / BK), nw = ksteps * (S::KSTEP / IG_WK);
   const int mt = (A.N + IG_M - 1) / IG_M;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NW; ++i) {
       mbar_init(&full_w[i], 1);
-      mbar_init(&empty_w[i], 8);
+      mbar_init(&empty_w[i], 4);
     }
     for (int i = 0; i < NB; ++i) {
-      mbar_init(&full_b[i], 1 + 4 * (BK / 64));
+      mbar_init(&full[i], 1 + 4 * (BK > IG_WK ? BK / IG_WK : 1));
       mbar_init(&done[i], 1);
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < S::ACCS; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], NT == 256 ? 4 : 8);
+      mbar_init(&d_empty[i], 8);
     }
     mbar_init(fin, 1);
     *s_abort = 0;
+    *s_most = 0;
     fence_barrier_init();
   }
   if (warp == 2) {
@@ -184,9 +169,21 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
+  if (NT == 256) {
+    // the largest sum of magnitudes of any activation row (a value for each CTA of i8_widen)
+    const uint32_t* most = reinterpret_cast<const uint32_t*>(A.ws + off_xs) - I8_WIDEN_CTAS;
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < wide; i += IG_THREADS) m = max(m, __ldcg(most + i));
+    m = __reduce_max_sync(0xffffffffu, m);
+    __syncthreads();  // (s_most is 0)
+    if (lane == 0) atomicMax(s_most, m);
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  // codes of an exact run: all of them where no sum with weights of magnitude
+  // up to 128 can pass 2^24
+  const int run = NT == 256 && *s_most <= (1u << 24) / 128 ? 1 << 30 : IG_RUN;
   const uint32_t taddr = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int items = __shfl_sync(0xffffffffu, s_tiles[A.G] * mt, 0);
 
@@ -220,7 +217,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       for (int item = blockIdx.x; item < items && go; item += gridDim.x) {
         const IgItem it = item_at(item);
         const bool once = s_tiles[it.g + 1] - s_tiles[it.g] == 1;  // read for one activation tile alone
-        for (int st = 0; st < (nblk * BK + IG_WK - 1) / IG_WK; ++st, ++gs) {  // (beyond K: zeros)
+        for (int st = 0; st < nw; ++st, ++gs) {
           const uint32_t s = gs % NW;
           if (!gwait(&empty_w[s], ((gs / NW) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
           mbar_arrive_expect_tx(&full_w[s], IG_WSLOT);
@@ -244,20 +241,20 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         for (int j = 0; j < nblk; ++j, ++gs) {
           const uint32_t s = gs % NB;
           if (!gwait(&done[s], ((gs / NB) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
-          mbar_arrive_expect_tx(&full_b[s], (uint32_t)n16 * 2048 * (BK / 64));
+          mbar_arrive_expect_tx(&full[s], (uint32_t)n16 * 2048 * (BK / 64));
           int row = 0;
           for (int left = n16; left > 0;) {  // the rows in boxes of 128, 64, 32, 16
             const int i = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
 #pragma unroll
             for (int c = 0; c < BK / 64; ++c)
-              tma_load_2d(sm_b + s * S::BSLOT + c * (NT * 128) + row * 128, &maps.x[i], j * BK + 64 * c, it.row0 + row, &full_b[s]);
+              tma_load_2d(sm_b + s * S::BSLOT + c * (NT * 128) + row * 128, &maps.x[i], j * BK + 64 * c, it.row0 + row, &full[s]);
             row += 16 << i;
             left -= 1 << i;
           }
         }
       }
       for (uint32_t k = gs > (uint32_t)NB ? gs - NB : 0; k < gs; ++k)
-        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full_b[k % NB], (k / NB) & 1u); ++i) {
+        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full[k % NB], (k / NB) & 1u); ++i) {
         }
     } else if (warp == 2) {
       // -------------------------------------------------------- MMA issuer
@@ -267,61 +264,44 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       // waits at one barrier, looked at while the block before is under way)
       const uint32_t leader = elect_one();
       const uint64_t db0 = umma_desc_sw128(smem_u32(sm_b));
-      IgSlots<S::ACCS> D;
-      uint32_t s = 0, ph = 0, a = 0;
+      uint32_t s = 0, ph = 0, a = 0, d = 0, dph = 1;
       bool ready = false, ok = true;
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int ntok = __shfl_sync(0xffffffffu, item_at(item).ntok, 0);
-        const bool halves = NT == 256 && ntok > 128;
-        const uint32_t id0 = umma_idesc((min(ntok, 128) + 15) & ~15), id1 = umma_idesc((max(ntok - 128, 16) + 15) & ~15);
-        uint32_t acc0 = 0, acc1 = 0;  // whether the run has begun
-        int left = IG_RUN / BK;       // blocks to the end of half 0's run
+        const uint32_t idesc = umma_idesc((item_at(item).ntok + 15) & ~15);
+        uint32_t acc = 0;          // whether the run has begun
+        int left = run / BK;       // blocks to its end
         for (int j = nblk; j > 0; --j) {
-          if (acc0 == 0) ok = gwait(&d_empty[D.cur0], (D.uses >> D.cur0 & 1u) ^ 1u, status, s_abort) && ok;
-          if (!ready) ok = gwait(&full_b[s], ph, status, s_abort) && ok;
-          const uint32_t ac = taddr + S::ACOL + a * S::AW, d0 = taddr + D.cur0 * S::ACCW;
+          if (acc == 0) ok = gwait(&d_empty[d], dph, status, s_abort) && ok;
+          if (!ready) ok = gwait(&full[s], ph, status, s_abort) && ok;
+          const bool end = --left == 0 || j == 1;
+          const uint32_t dc = taddr + d * NT, ac = taddr + IG_ACOL + a * S::AW;
           const uint64_t db = db0 + s * (S::BSLOT >> 4);
           tmem_fence_after();
-          if (NT == 256 && halves && acc1 == 0) {
-            ok = gwait(&d_empty[D.cur1], (D.uses >> D.cur1 & 1u) ^ 1u, status, s_abort) && ok;
-            tmem_fence_after();
-          }
           __syncwarp();
-          --left;
-          const bool end0 = left == 0 || j == 1, end1 = NT == 256 && halves && (left == IG_RUN / BK / 2 || j == 1);
           if (leader) {
             if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
-                umma_f16(d0, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), id0, k ? 1u : acc0);
-              if (NT == 256 && halves) {
-                const uint32_t d1 = taddr + D.cur1 * S::ACCW;
-#pragma unroll
-                for (int k = 0; k < BK / 16; ++k)
-                  umma_f16(d1, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 128 * 128 / 16 + 2 * (k & 3), id1, k ? 1u : acc1);
-              }
+                umma_f16(dc, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), idesc, k ? 1u : acc);
             }
             umma_commit(&done[s]);
-            if (end0) umma_commit(&d_full[D.cur0]);
-            if (end1) umma_commit(&d_full[D.cur1]);
+            if (end) umma_commit(&d_full[d]);
           }
           __syncwarp();
-          acc0 = 1;
-          acc1 = 1;
-          a = (a + 1) % S::AS;
           if (++s == (uint32_t)NB) {
             s = 0;
             ph ^= 1u;
           }
-          ready = mbar_test_wait(&full_b[s], ph);
-          if (end0) {
-            D.template turn<0>(halves);
-            acc0 = 0;
-            left = IG_RUN / BK;
-          }
-          if (end1) {  // half a run apart, so that one spare accumulator serves both
-            D.template turn<1>(halves);
-            acc1 = 0;
+          ready = mbar_test_wait(&full[s], ph);
+          a = (a + 1) % S::AS;
+          acc = 1;
+          if (end) {
+            acc = 0;
+            left = run / BK;
+            if (++d == (uint32_t)S::ACCS) {
+              d = 0;
+              dph ^= 1u;
+            }
           }
         }
       }
@@ -334,94 +314,87 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   } else if (warp < 12) {
     setmaxnreg_dec<IG_RCONV>();
     // ---------------------------------------------------------- converters
+    // One after the other the CTA's blocks of 128 rows x 128 codes, the sets in
+    // turn: a row a lane, all its loads before the first conversion.
     const int set = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
-    uint32_t gs = 0, gb = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-      for (int c = set; c < nblk * (BK / 64) + set; c += 2, ++gs) {  // chunks of 64 codes
-        const uint32_t s = gs % NW;
-        gwait(&full_w[s], (gs / NW) & 1u, status, s_abort);
-        uint4 w[4];
-        const uint8_t* row = sm + s * IG_WSLOT + r * IG_WK;  // 16-byte unit c of row r at unit c ^ (r % 8)
+    const uint32_t total = (uint32_t)(items > (int)blockIdx.x ? (items - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0) * (uint32_t)nw;
+    const uint32_t src = smem_u32(sm) + r * IG_WK, sw = (r & 7) * 16;  // 16-byte unit c of row r is at unit c ^ (r % 8)
+    const uint32_t dst = taddr + ((uint32_t)(32 * q) << 16) + IG_ACOL;
+    constexpr int PER = BK < IG_WK ? IG_WK / BK : 1;  // blocks of a slot, or
+    constexpr int OF = BK > IG_WK ? BK / IG_WK : 1;   // slots of a block
+    uint32_t s = set, sph = 0;
+    for (uint32_t g = set; g < total; g += 2) {
+      gwait(&full_w[s], sph, status, s_abort);
+      uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(row + 16 * ((4 * set + i) ^ (r & 7)));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty_w[s]);
-        if (BK == 64 && c >= nblk) continue;  // the slot's second half is behind the last block
-        const uint32_t b = gb + c / (BK / 64);
-        const uint32_t ta = taddr + ((uint32_t)(32 * q) << 16) + S::ACOL + (b % S::AS) * S::AW + c % (BK / 64) * 32;
-        uint32_t o[16];
-        cvt_int8x8(w[0].x, w[0].y, o);
-        cvt_int8x8(w[0].z, w[0].w, o + 4);
-        cvt_int8x8(w[1].x, w[1].y, o + 8);
-        cvt_int8x8(w[1].z, w[1].w, o + 12);
-        // the block that held these columns is done (that phase cannot have been
-        // overtaken: the next block in its slot needs this one's weights first)
-        if (b >= (uint32_t)S::AS) gwait(&done[(b - S::AS) % NB], ((b - S::AS) / NB) & 1u, status, s_abort);
-        tmem_fence_after();
-        __syncwarp();
-        tmem_st16(ta, o);
-        cvt_int8x8(w[2].x, w[2].y, o);
-        cvt_int8x8(w[2].z, w[2].w, o + 4);
-        cvt_int8x8(w[3].x, w[3].y, o + 8);
-        cvt_int8x8(w[3].z, w[3].w, o + 12);
-        tmem_st16(ta + 16, o);
-        tmem_wait_st();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full_b[b % NB]);
+      for (int i = 0; i < 8; ++i) w[i] = lds128(src + s * IG_WSLOT + ((16 * i) ^ sw));
+      // the block that held these columns is done (that phase cannot have been
+      // overtaken: the next block in its slot needs this one's weights first)
+      const uint32_t b = PER > 1 ? g * PER : g / OF;
+      if (b + PER > (uint32_t)S::AS) {
+        const uint32_t before = b + PER - 1 - S::AS;  // (done in order: the last of PER)
+        gwait(&done[before % NB], (before / NB) & 1u, status, s_abort);
       }
-      gb += nblk;
+      tmem_fence_after();
+      __syncwarp();
+      const uint32_t at = dst + (b % S::AS) * S::AW + (OF > 1 ? g % OF * (IG_WK / 2) : 0);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t o[16];
+        cvt_int8x8(w[2 * h].x, w[2 * h].y, o);
+        cvt_int8x8(w[2 * h].z, w[2 * h].w, o + 4);
+        cvt_int8x8(w[2 * h + 1].x, w[2 * h + 1].y, o + 8);
+        cvt_int8x8(w[2 * h + 1].z, w[2 * h + 1].w, o + 12);
+        tmem_st16(at + 16 * h, o);  // (the blocks of a slot stand side by side)
+      }
+      if (lane == 0) mbar_arrive(&empty_w[s]);  // (every lane's loads are complete: its stores used them)
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mbar_arrive(&full[(b + i) % NB]);
+      s += 2;
+      if (s >= (uint32_t)NW) {
+        s -= NW;
+        sph ^= 1u;
+      }
     }
   } else {
     setmaxnreg_inc<IG_REPI>();
     // ------------------------------------------------------------ epilogue
     constexpr int COLS = S::COLS;
-    const int set = (warp - 12) >> 2, q = warp & 3;
+    const int set = (warp - 12) >> 2, q = warp & 3, col0 = set * COLS;
     const float* xs = reinterpret_cast<const float*>(A.ws + off_xs);
-    IgSlots<S::ACCS> D;
+    uint32_t d = 0, dph = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
       const IgItem it = item_at(item);
-      const bool halves = NT == 256 && it.ntok > 128;
-      const int half = NT == 256 ? set : 0;           // whose runs this warp reads
-      const int col0 = NT == 256 ? set * 128 : set * COLS;
       const int cols = min(max(it.ntok - col0, 0), COLS);
       int acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0;
-      auto read_run = [&](int slot) {
-        pf_wait(&d_full[slot], D.uses >> slot & 1u, status, s_abort);  // (long: suspended, out of the other warps' way)
+      for (int c = 0; c < nblk * BK; c += run) {
+        pf_wait(&d_full[d], dph, status, s_abort);  // (long: suspended, out of the other warps' way)
         tmem_fence_after();
         __syncwarp();
-        const uint32_t t = taddr + ((uint32_t)(32 * q) << 16) + slot * S::ACCW + (NT == 256 ? 0 : col0);
+        const uint32_t t = taddr + ((uint32_t)(32 * q) << 16) + d * NT + col0;
 #pragma unroll
-        for (int c = 0; c < COLS; c += 16)
-          if (c < cols) {
+        for (int i = 0; i < COLS; i += 16)
+          if (i < cols) {
             uint32_t v[16];
-            tmem_ld16_nowait(t + c, v);
+            tmem_ld16_nowait(t + i, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(v[i]));
+            for (int k = 0; k < 16; ++k) acc[i + k] += __float2int_rn(__uint_as_float(v[k]));
           }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&d_empty[slot]);
-      };
-      // the ends of runs in their order: half 0 after 1024, 2048, ... codes, half 1 after 512, 1536, ..., both at the end
-      constexpr int STEP = NT == 256 ? IG_RUN / 2 : IG_RUN;
-      for (int c = STEP; c < nblk * BK; c += STEP) {
-        if (c % IG_RUN == 0) {
-          if (half == 0) read_run(D.cur0);
-          D.template turn<0>(halves);
-        } else if (halves) {
-          if (half == 1) read_run(D.cur1);
-          D.template turn<1>(halves);
+        if (lane == 0) mbar_arrive(&d_empty[d]);
+        if (++d == (uint32_t)S::ACCS) {
+          d = 0;
+          dph ^= 1u;
         }
-      }
-      if (half == 0) read_run(D.cur0);
-      D.template turn<0>(halves);
-      if (halves) {
-        if (half == 1) read_run(D.cur1);
-        D.template turn<1>(halves);
+        if (run > IG_RUN) break;  // (no overflow of c)
       }
       const int n = it.n0 + 32 * q + lane;
       const bool live = n < A.N;
@@ -452,17 +425,29 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512) : "memory");
 }
 
+// sum + the magnitudes of four codes
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w, uint32_t sum) {
+  const uint32_t neg = (w >> 7) & 0x01010101u;
+  const uint32_t mag = (w ^ (neg * 0xffu)) + neg;  // (per byte: -128 becomes 128)
+  uint32_t d;
+  asm("dp4a.u32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(mag), "r"(0x01010101u), "r"(sum));
+  return d;
+}
+
 // The rows of y: fp16 copies of their activation codes, zero up to kp, and
-// their scales.  A warp a row.  A row out of range gets scale NaN.
+// their scales; and for each CTA the largest sum of a row's magnitudes.  A warp
+// a row.  A row out of range gets scale NaN.
 constexpr int WD_T = 256;
-__global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb) {
+__global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb, uint32_t* __restrict__ most) {
   __shared__ int s_lo, s_hi;
+  __shared__ uint32_t s_most;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) {
     s_lo = A.offsets ? i8_offset(A, 0) : 0;
     s_hi = A.offsets ? 0 : A.P;
+    s_most = 0;
   }
   __syncthreads();
   if (A.offsets) {  // rows of any group: up to the largest offset
@@ -473,6 +458,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
     __syncthreads();
   }
   const int hi = s_hi;
+  uint32_t top = 0;
   for (long long p = s_lo + (long long)blockIdx.x * (WD_T / 32) + warp; p < hi; p += (long long)gridDim.x * (WD_T / 32)) {
     const int row = A.rows ? __ldcg(A.rows + p) : (int)p;
     const bool ok = row >= 0 && row < A.X;
@@ -482,6 +468,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
     }
     const int8_t* src = A.x + (ok ? row : 0) * A.ldx;
     uint4* dst = xb + p * (kp / 8);
+    uint32_t sum = 0;
 #pragma unroll 4
     for (int u = lane; u < kp / 16; u += 32) {
       const int n = ok ? A.K - 16 * u : 0;
@@ -495,13 +482,18 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
           if (i < n) w[i >> 2] |= (uint32_t)(uint8_t)src[16 * u + i] << (8 * (i & 3));
         c = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      sum = magnitudes(c.x, magnitudes(c.y, magnitudes(c.z, magnitudes(c.w, sum))));
       uint32_t o[8];
       cvt_int8x8(c.x, c.y, o);
       cvt_int8x8(c.z, c.w, o + 4);
       dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
       dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    top = max(top, __reduce_add_sync(0xffffffffu, sum));
   }
+  if (lane == 0) atomicMax(&s_most, top);
+  __syncthreads();
+  if (threadIdx.x == 0) most[blockIdx.x] = s_most;
 }
 
 bool encode_weights(CUtensorMap* m, const I8Params& A) {
@@ -544,13 +536,13 @@ cudaError_t check_kernel() {
 }
 
 template <int NT>
-cudaError_t launch_nt(const IgMaps& maps, const I8Params& A, int sms, cudaStream_t st) {
+cudaError_t launch_nt(const IgMaps& maps, const I8Params& A, int sms, int wide, cudaStream_t st) {
   const cudaError_t e = check_kernel<NT>();
   if (e != cudaSuccess) return e;
   // (at most: a partial tile per group that can have rows)
   const long long tiles = (long long)A.P / NT + (A.G < A.P ? A.G : A.P), items = tiles * ((A.N + IG_M - 1) / IG_M);
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(i8_gemm<NT>, (unsigned)(items < sms ? items : sms), IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs());
+  return launch_pdl(i8_gemm<NT>, (unsigned)(items < sms ? items : sms), IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs(), wide);
 }
 
 }  // namespace
@@ -565,13 +557,13 @@ cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   bool ok = encode_weights(&maps.w, A);
   for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
   if (!ok) return cudaErrorInvalidValue;
-  const long long wide = ((long long)A.P + WD_T / 32 - 1) / (WD_T / 32);
-  const cudaError_t e = launch_pdl(i8_widen, (unsigned)(wide < 8LL * sms ? wide : 8LL * sms), WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
+  const int most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = (A.P + WD_T / 32 - 1) / (WD_T / 32), wide = all < most ? all : most;
+  const cudaError_t e = launch_pdl(i8_widen, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb), reinterpret_cast<uint32_t*>(xs) - I8_WIDEN_CTAS);
   if (e != cudaSuccess) return e;
-  if (A.P <= 32) return launch_nt<32>(maps, A, sms, st);
-  if (A.P <= 64) return launch_nt<64>(maps, A, sms, st);
-  if (A.P < 192LL * A.G) return launch_nt<128>(maps, A, sms, st);
-  return launch_nt<256>(maps, A, sms, st);
+  if (A.P <= 32) return launch_nt<32>(maps, A, sms, wide, st);
+  if (A.P <= 64) return launch_nt<64>(maps, A, sms, wide, st);
+  if (A.P < 192LL * A.G) return launch_nt<128>(maps, A, sms, wide, st);
+  return launch_nt<256>(maps, A, sms, wide, st);
 }
 
 }  // namespace colimoe
