@@ -14,7 +14,7 @@
 //
 // One persistent CTA an SM, 20 warps meeting at mbarriers, every wait bounded:
 //   warp 0       TMA of weight codes, slots of 128 rows x 128 codes;
-//   warp 1       TMA of activations, slots of up to NT rows x BK codes;
+//   warps 1, 3   TMA of activations, slots of up to NT rows x BK codes;
 //   warp 2       MMA issuer, blocks of BK codes;
 //   warps 4-11   converters, two sets of four (a warp for each lane quarter)
 //                that take the blocks in turn: a block's way through registers
@@ -45,15 +45,15 @@ constexpr int IG_MAXW = 9, IG_MAXB = 5;
 template <int NT>
 struct IgShape {
   static constexpr int BK = NT == 256 ? 64 : NT == 128 ? 128 : 256;
-  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 5 : 3;
-  static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 4 : 5;
+  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 7 : 3;
+  static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 3 : 5;
   static constexpr uint32_t BSLOT = NT * BK * 2;
   static constexpr uint32_t BARS = NW * IG_WSLOT + NB * BSLOT;
   static constexpr uint32_t TABLES = BARS + 512;
   static constexpr int COLS = NT / 2;                          // columns of an epilogue warp
   static constexpr int KSTEP = BK < IG_WK ? IG_WK : BK;        // K is filled up with zeros to a multiple of this
   // tensor memory: accumulators, then AS blocks of widened weights
-  static constexpr int ACCS = NT == 256 ? 1 : 2, AW = BK / 2, AS = NT <= 64 ? 2 : 4;
+  static constexpr int ACCS = NT == 256 ? 1 : 2, AW = BK / 2, AS = NT <= 64 ? 2 : NT == 128 ? 3 : 4;
   static_assert(ACCS * NT <= 256 && AS * AW <= 256 && AS <= NB, "tensor memory");
 };
 constexpr int IG_ACOL = 256;                 // first column of the widened weights
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       mbar_init(&empty_w[i], 4);
     }
     for (int i = 0; i < NB; ++i) {
-      mbar_init(&full[i], 1 + 4 * (BK > IG_WK ? BK / IG_WK : 1));
+      mbar_init(&full[i], 2 + 4 * (BK > IG_WK ? BK / IG_WK : 1));
       mbar_init(&done[i], 1);
     }
     for (int i = 0; i < S::ACCS; ++i) {
@@ -230,23 +230,30 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       for (uint32_t k = gs > (uint32_t)NW ? gs - NW : 0; k < gs; ++k)
         for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full_w[k % NW], (k / NW) & 1u); ++i) {
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if ((warp == 1 || warp == 3) && lane == 0) {
       // ------------------------------------------------ TMA of activations
+      // Each warp takes half of a slot (one thread issues a box of 16 KB every
+      // 380 cycles): every other 64 codes, or the tile's rows before or from 128 on.
       fence_proxy_async_global();  // (the widened rows were written by ordinary stores of the kernel before)
+      const int half = warp >> 1;
       uint32_t gs = 0;
       bool go = true;
       for (int item = blockIdx.x; item < items && go; item += gridDim.x) {
         const IgItem it = item_at(item);
-        const int n16 = (it.ntok + 15) / 16;
+        const int all = (it.ntok + 15) / 16, first = BK == 64 && half ? 8 : 0, n16 = BK == 64 ? min(max(all - first, 0), 8) : all;
         for (int j = 0; j < nblk; ++j, ++gs) {
           const uint32_t s = gs % NB;
           if (!gwait(&done[s], ((gs / NB) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
-          mbar_arrive_expect_tx(&full[s], (uint32_t)n16 * 2048 * (BK / 64));
-          int row = 0;
+          if (n16 == 0) {
+            mbar_arrive(&full[s]);
+            continue;
+          }
+          mbar_arrive_expect_tx(&full[s], (uint32_t)n16 * 2048 * (BK == 64 ? 1 : BK / 128));
+          int row = 16 * first;
           for (int left = n16; left > 0;) {  // the rows in boxes of 128, 64, 32, 16
             const int i = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
 #pragma unroll
-            for (int c = 0; c < BK / 64; ++c)
+            for (int c = BK == 64 ? 0 : half; c < BK / 64; c += 2)
               tma_load_2d(sm_b + s * S::BSLOT + c * (NT * 128) + row * 128, &maps.x[i], j * BK + 64 * c, it.row0 + row, &full[s]);
             row += 16 << i;
             left -= 1 << i;
