@@ -33,7 +33,8 @@ namespace {
 constexpr int IG_M = 128;                    // weight rows of a tile
 constexpr int IG_WK = 128;                   // codes of a weight slot's row
 constexpr uint32_t IG_WSLOT = IG_M * IG_WK;  // 16 KB
-constexpr int IG_RUN = 1024;                 // codes of an exact run
+constexpr int IG_RUN = 512;                  // codes of a run that is exact whatever they are: 512 * 128 * 255 < 2^24
+constexpr uint32_t IG_MOST = (1u << 24) / 255;  // largest sum of an activation row's magnitudes with which all of K is
 constexpr int IG_MB = 8;                     // weight tiles that share activation tiles while they are in L2
 constexpr int IG_THREADS = 640;
 constexpr int IG_RCTL = 32, IG_RCONV = 64, IG_REPI = 160;
@@ -79,6 +80,17 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+// 8 codes (two words) -> 8 fp16 of value (code + 128) 2^-24: the subnormal whose
+// bits are the code with its sign bit flipped.  Integer instructions alone:
+// with fp16 subtractions among them (which make the plain code) these warps take
+// every issue slot, and the MMA warp beside them 780 cycles a block instead of 510.
+__device__ __forceinline__ void biased8(uint32_t w0, uint32_t w1, uint32_t* o) {
+  const uint32_t x0 = w0 ^ 0x80808080u, x1 = w1 ^ 0x80808080u;
+  o[0] = prmt(x0, 0u, 0x4140u);
+  o[1] = prmt(x0, 0u, 0x4342u);
+  o[2] = prmt(x1, 0u, 0x4140u);
+  o[3] = prmt(x1, 0u, 0x4342u);
 }
 // D[tmem] (+)= A[tmem] x B[smem]
 __device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -169,9 +181,9 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
-  if (NT == 256) {
+  {
     // the largest sum of magnitudes of any activation row (a value for each CTA of i8_widen)
-    const uint32_t* most = reinterpret_cast<const uint32_t*>(A.ws + off_xs) - I8_WIDEN_CTAS;
+    const uint32_t* most = reinterpret_cast<const uint32_t*>(A.ws + WS_HEADER_BYTES);
     uint32_t m = 0;
     for (int i = threadIdx.x; i < wide; i += IG_THREADS) m = max(m, __ldcg(most + i));
     m = __reduce_max_sync(0xffffffffu, m);
@@ -181,9 +193,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  // codes of an exact run: all of them where no sum with weights of magnitude
-  // up to 128 can pass 2^24
-  const int run = NT == 256 && *s_most <= (1u << 24) / 128 ? 1 << 30 : IG_RUN;
+  const int run = *s_most <= IG_MOST ? 1 << 30 : IG_RUN;
   const uint32_t taddr = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int items = __shfl_sync(0xffffffffu, s_tiles[A.G] * mt, 0);
 
@@ -271,6 +281,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       // waits at one barrier, looked at while the block before is under way)
       const uint32_t leader = elect_one();
       const uint64_t db0 = umma_desc_sw128(smem_u32(sm_b));
+      constexpr int TAIL = NT == 256 ? 1 : 2;
       uint32_t s = 0, ph = 0, a = 0, d = 0, dph = 1;
       bool ready = false, ok = true;
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -281,25 +292,29 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           if (acc == 0) ok = gwait(&d_empty[d], dph, status, s_abort) && ok;
           if (!ready) ok = gwait(&full[s], ph, status, s_abort) && ok;
           const bool end = --left == 0 || j == 1;
-          const uint32_t dc = taddr + d * NT, ac = taddr + IG_ACOL + a * S::AW;
+          const uint32_t dc = taddr + d * NT, ac = taddr + IG_ACOL + a * S::AW, old = s;
           const uint64_t db = db0 + s * (S::BSLOT >> 4);
+          auto issue = [&](int from, int to) {
+#pragma unroll
+            for (int k = from; k < to; ++k)
+              umma_f16(dc, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), idesc, k ? 1u : acc);
+          };
           tmem_fence_after();
           __syncwarp();
-          if (leader) {
-            if (ok) {  // (aborted: the results are flagged invalid; issue nothing)
-#pragma unroll
-              for (int k = 0; k < BK / 16; ++k)
-                umma_f16(dc, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), idesc, k ? 1u : acc);
-            }
-            umma_commit(&done[s]);
-            if (end) umma_commit(&d_full[d]);
-          }
-          __syncwarp();
+          if (leader && ok) issue(0, BK / 16 - TAIL);  // (aborted: the results are flagged invalid; nothing is issued)
+          // behind the last TAIL instructions, which are still under way then,
+          // the next block follows without a gap
           if (++s == (uint32_t)NB) {
             s = 0;
             ph ^= 1u;
           }
           ready = mbar_test_wait(&full[s], ph);
+          if (leader) {
+            if (ok) issue(BK / 16 - TAIL, BK / 16);
+            umma_commit(&done[old]);
+            if (end) umma_commit(&d_full[d]);
+          }
+          __syncwarp();
           a = (a + 1) % S::AS;
           acc = 1;
           if (end) {
@@ -348,10 +363,10 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         uint32_t o[16];
-        cvt_int8x8(w[2 * h].x, w[2 * h].y, o);
-        cvt_int8x8(w[2 * h].z, w[2 * h].w, o + 4);
-        cvt_int8x8(w[2 * h + 1].x, w[2 * h + 1].y, o + 8);
-        cvt_int8x8(w[2 * h + 1].z, w[2 * h + 1].w, o + 12);
+        biased8(w[2 * h].x, w[2 * h].y, o);
+        biased8(w[2 * h].z, w[2 * h].w, o + 4);
+        biased8(w[2 * h + 1].x, w[2 * h + 1].y, o + 8);
+        biased8(w[2 * h + 1].z, w[2 * h + 1].w, o + 12);
         tmem_st16(at + 16 * h, o);  // (the blocks of a slot stand side by side)
       }
       if (lane == 0) mbar_arrive(&empty_w[s]);  // (every lane's loads are complete: its stores used them)
@@ -373,11 +388,12 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     constexpr int COLS = S::COLS;
     const int set = (warp - 12) >> 2, q = warp & 3, col0 = set * COLS;
     const float* xs = reinterpret_cast<const float*>(A.ws + off_xs);
+    const uint32_t* xsum = reinterpret_cast<const uint32_t*>(xs) + A.P;
     uint32_t d = 0, dph = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
       const IgItem it = item_at(item);
       const int cols = min(max(it.ntok - col0, 0), COLS);
-      int acc[COLS];
+      uint32_t acc[COLS];  // (modulo 2^32, in which the end result fits)
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0;
       for (int c = 0; c < nblk * BK; c += run) {
@@ -392,7 +408,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
             tmem_ld16_nowait(t + i, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) acc[i + k] += __float2int_rn(__uint_as_float(v[k]));
+            for (int k = 0; k < 16; ++k) acc[i + k] += (uint32_t)__float2int_rn(__uint_as_float(v[k]) * 16777216.f);
           }
         tmem_fence_before();
         __syncwarp();
@@ -413,10 +429,12 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
 #pragma unroll
         for (int c = 0; c < COLS; c += 16)
           if (c < cols) {
-            const float sx = c + (lane & 15) < cols ? __ldcg(xs + it.row0 + col0 + c + (lane & 15)) : 0.f;
+            const int p = it.row0 + col0 + c + (lane & 15);
+            const float sx = c + (lane & 15) < cols ? __ldcg(xs + p) : 0.f;
+            const uint32_t bias = c + (lane & 15) < cols ? __ldcg(xsum + p) : 0u;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float v = i8_value(acc[c + i], __shfl_sync(0xffffffffu, sx, i), sw);
+              const float v = i8_value((int)(acc[c + i] - __shfl_sync(0xffffffffu, bias, i)), __shfl_sync(0xffffffffu, sx, i), sw);
               if (live && c + i < cols) y[(c + i) * A.ldy] = from_f32<TY>(v);
             }
           }
@@ -442,10 +460,10 @@ __device__ __forceinline__ uint32_t magnitudes(uint32_t w, uint32_t sum) {
 }
 
 // The rows of y: fp16 copies of their activation codes, zero up to kp, and
-// their scales; and for each CTA the largest sum of a row's magnitudes.  A warp
-// a row.  A row out of range gets scale NaN.
+// their scales, 128 times their sums; and for each CTA the largest sum of a
+// row's magnitudes.  A warp a row.  A row out of range gets scale NaN.
 constexpr int WD_T = 256;
-__global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb, uint32_t* __restrict__ most) {
+__global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb) {
   __shared__ int s_lo, s_hi;
   __shared__ uint32_t s_most;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -476,6 +494,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
     const int8_t* src = A.x + (ok ? row : 0) * A.ldx;
     uint4* dst = xb + p * (kp / 8);
     uint32_t sum = 0;
+    int plain = 0;
 #pragma unroll 4
     for (int u = lane; u < kp / 16; u += 32) {
       const int n = ok ? A.K - 16 * u : 0;
@@ -490,6 +509,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
         c = make_uint4(w[0], w[1], w[2], w[3]);
       }
       sum = magnitudes(c.x, magnitudes(c.y, magnitudes(c.z, magnitudes(c.w, sum))));
+      plain = dp4a_ss(c.x, 0x01010101u, dp4a_ss(c.y, 0x01010101u, dp4a_ss(c.z, 0x01010101u, dp4a_ss(c.w, 0x01010101u, plain))));
       uint32_t o[8];
       cvt_int8x8(c.x, c.y, o);
       cvt_int8x8(c.z, c.w, o + 4);
@@ -497,10 +517,12 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
       dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
     top = max(top, __reduce_add_sync(0xffffffffu, sum));
+    plain = __reduce_add_sync(0xffffffffu, plain);
+    if (lane == 0) reinterpret_cast<uint32_t*>(xs)[A.P + p] = 128u * (uint32_t)plain;
   }
   if (lane == 0) atomicMax(&s_most, top);
   __syncthreads();
-  if (threadIdx.x == 0) most[blockIdx.x] = s_most;
+  if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(A.ws + WS_HEADER_BYTES)[blockIdx.x] = s_most;
 }
 
 bool encode_weights(CUtensorMap* m, const I8Params& A) {
@@ -565,7 +587,7 @@ cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
   if (!ok) return cudaErrorInvalidValue;
   const int most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = (A.P + WD_T / 32 - 1) / (WD_T / 32), wide = all < most ? all : most;
-  const cudaError_t e = launch_pdl(i8_widen, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb), reinterpret_cast<uint32_t*>(xs) - I8_WIDEN_CTAS);
+  const cudaError_t e = launch_pdl(i8_widen, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
   if (e != cudaSuccess) return e;
   if (A.P <= 32) return launch_nt<32>(maps, A, sms, wide, st);
   if (A.P <= 64) return launch_nt<64>(maps, A, sms, wide, st);

@@ -26,11 +26,12 @@ struct I8Params {
 constexpr int I8_FEW = 8;     // up to this many rows: the streaming kernel
 
 // Workspace behind the header: a word for each CTA that widens activations,
-// the scales of the rows of y, fp16 copies of their activation rows padded to kp codes.
+// the scales of the rows of y, 128 times the sums of their codes, fp16 copies of
+// their activation rows padded to kp codes.
 constexpr int I8_WIDEN_CTAS = 1280;
 inline long long i8_kp(int K) { return ((long long)K + 63) / 64 * 64; }
 inline size_t i8_off_xs() { return WS_HEADER_BYTES + 4 * I8_WIDEN_CTAS; }
-inline size_t i8_off_xb(int P) { return align_up(i8_off_xs() + 4 * (size_t)P, 256); }
+inline size_t i8_off_xb(int P) { return align_up(i8_off_xs() + 8 * (size_t)P, 256); }
 inline size_t i8_ws_bytes(int P, int K) { return align_up(i8_off_xb(P) + 2 * (size_t)P * (size_t)i8_kp(K), 256); }
 
 // First row of group g: offsets clamped to [0, P]; ascending by running maximum
