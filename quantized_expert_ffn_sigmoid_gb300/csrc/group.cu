@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(CB_T) combine_kernel(const CombineParams P) {
   pdl_wait();
   pdl_trigger();
   const long long task = (long long)blockIdx.x * CB_T + threadIdx.x;
-  const long long t = task / P.units;
+  const long long t = task <= 0xffffffffLL ? (long long)((uint32_t)task / (uint32_t)P.units) : task / P.units;
   if (t >= P.T) return;
   const int h = (int)(task - t * P.units) * 8, n = P.H - h;
   const int32_t* slot = P.slots + t * P.k;

@@ -106,7 +106,8 @@ struct IgItem {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__ IgMaps maps, const I8Params A, const uint32_t off_xs, const int wide) {
+__global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__ IgMaps maps, const I8Params A, const uint32_t off_xs, const int wide,
+                                                           const int n_splits, uint32_t* __restrict__ part) {
   using S = IgShape<NT>;
   constexpr int NW = S::NW, NB = S::NB, BK = S::BK;
   extern __shared__ uint8_t sm_raw[];
@@ -127,7 +128,11 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   uint32_t* status = reinterpret_cast<uint32_t*>(A.ws);
   // (broadcast, so that the compiler knows them to be the same in every lane of a warp)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int ksteps = (A.K + S::KSTEP - 1) / S::KSTEP, nblk = ksteps * (S::KSTEP / BK), nw = ksteps * (S::KSTEP / IG_WK);
+  // With splits, this CTA takes one part of K of one tile (the grid holds all parts of all tiles)
+  const int splits = NT == 256 ? 1 : n_splits;
+  const int kall = (A.K + S::KSTEP - 1) / S::KSTEP, kpart = (kall + splits - 1) / splits;
+  const int k0 = splits > 1 ? (int)blockIdx.x % splits * kpart : 0, ksteps = splits > 1 ? min(kpart, kall - k0) : kall;
+  const int nblk = ksteps * (S::KSTEP / BK), nw = ksteps * (S::KSTEP / IG_WK);
   const int mt = (A.N + IG_M - 1) / IG_M;
 
   if (threadIdx.x == 0) {
@@ -196,6 +201,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   const int run = *s_most <= IG_MOST ? 1 << 30 : IG_RUN;
   const uint32_t taddr = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int items = __shfl_sync(0xffffffffu, s_tiles[A.G] * mt, 0);
+  const int first = (int)blockIdx.x / splits;  // (splits > 1: the only item)
+  const int step = splits > 1 ? 1 << 30 : (int)gridDim.x;
 
   // Items of a group: IG_MB weight tiles for each activation tile, so that the
   // CTAs at work together share both operands in L2.
@@ -224,15 +231,15 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       const uint64_t stream = policy_evict_first();
       uint32_t gs = 0;
       bool go = true;
-      for (int item = blockIdx.x; item < items && go; item += gridDim.x) {
+      for (int item = first; item < items && go; item += step) {
         const IgItem it = item_at(item);
         const bool once = s_tiles[it.g + 1] - s_tiles[it.g] == 1;  // read for one activation tile alone
         for (int st = 0; st < nw; ++st, ++gs) {
           const uint32_t s = gs % NW;
           if (!gwait(&empty_w[s], ((gs / NW) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
           mbar_arrive_expect_tx(&full_w[s], IG_WSLOT);
-          if (once) tma_load_3d_hint(sm + s * IG_WSLOT, &maps.w, st * IG_WK, it.n0, it.g, &full_w[s], stream);
-          else tma_load_3d(sm + s * IG_WSLOT, &maps.w, st * IG_WK, it.n0, it.g, &full_w[s]);
+          if (once) tma_load_3d_hint(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, it.g, &full_w[s], stream);
+          else tma_load_3d(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, it.g, &full_w[s]);
         }
       }
       // every copy issued has landed before the CTA can exit (after an abort a
@@ -248,7 +255,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       const int half = warp >> 1;
       uint32_t gs = 0;
       bool go = true;
-      for (int item = blockIdx.x; item < items && go; item += gridDim.x) {
+      for (int item = first; item < items && go; item += step) {
         const IgItem it = item_at(item);
         const int all = (it.ntok + 15) / 16, first = BK == 64 && half ? 8 : 0, n16 = BK == 64 ? min(max(all - first, 0), 8) : all;
         for (int j = 0; j < nblk; ++j, ++gs) {
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
             const int i = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
 #pragma unroll
             for (int c = BK == 64 ? 0 : half; c < BK / 64; c += 2)
-              tma_load_2d(sm_b + s * S::BSLOT + c * (NT * 128) + row * 128, &maps.x[i], j * BK + 64 * c, it.row0 + row, &full[s]);
+              tma_load_2d(sm_b + s * S::BSLOT + c * (NT * 128) + row * 128, &maps.x[i], k0 * S::KSTEP + j * BK + 64 * c, it.row0 + row, &full[s]);
             row += 16 << i;
             left -= 1 << i;
           }
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       constexpr int TAIL = NT == 256 ? 1 : 2;
       uint32_t s = 0, ph = 0, a = 0, d = 0, dph = 1;
       bool ready = false, ok = true;
-      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+      for (int item = first; item < items; item += step) {
         const uint32_t idesc = umma_idesc((item_at(item).ntok + 15) & ~15);
         uint32_t acc = 0;          // whether the run has begun
         int left = run / BK;       // blocks to its end
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     // One after the other the CTA's blocks of 128 rows x 128 codes, the sets in
     // turn: a row a lane, all its loads before the first conversion.
     const int set = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
-    const uint32_t total = (uint32_t)(items > (int)blockIdx.x ? (items - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0) * (uint32_t)nw;
+    const uint32_t total = (uint32_t)(items > first ? (items - first - 1) / step + 1 : 0) * (uint32_t)nw;
     const uint32_t src = smem_u32(sm) + r * IG_WK, sw = (r & 7) * 16;  // 16-byte unit c of row r is at unit c ^ (r % 8)
     const uint32_t dst = taddr + ((uint32_t)(32 * q) << 16) + IG_ACOL;
     constexpr int PER = BK < IG_WK ? IG_WK / BK : 1;  // blocks of a slot, or
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     const float* xs = reinterpret_cast<const float*>(A.ws + off_xs);
     const uint32_t* xsum = reinterpret_cast<const uint32_t*>(xs) + A.P;
     uint32_t d = 0, dph = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    for (int item = first; item < items; item += step) {
       const IgItem it = item_at(item);
       const int cols = min(max(it.ntok - col0, 0), COLS);
       uint32_t acc[COLS];  // (modulo 2^32, in which the end result fits)
@@ -418,6 +425,37 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           dph ^= 1u;
         }
         if (run > IG_RUN) break;  // (no overflow of c)
+      }
+      if (splits > 1) {
+        // the parts of a tile meet in global memory: whole numbers, so their
+        // order is free; the last part adds the others and goes on to y
+        const int mine = (int)blockIdx.x % splits, row = 32 * q + lane;
+        uint32_t* tile = part + (size_t)item * splits * (NT * IG_M) + col0 * IG_M + row;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16)  // (whole sixteens of columns, also behind the last)
+          if (c < cols) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(tile + (size_t)mine * (NT * IG_M) + (c + i) * IG_M, acc[c + i]);
+          }
+        __threadfence();
+        named_bar(2, 256);
+        if (warp == 12 && lane == 0) s_most[1] = atomicAdd(reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES) + item, 1u);
+        named_bar(2, 256);
+        if (s_most[1] != (uint32_t)splits - 1) break;
+        __threadfence();
+        for (int z = 0; z < splits; ++z) {
+          if (z == mine) continue;
+          const uint32_t* other = tile + (size_t)z * (NT * IG_M);
+#pragma unroll
+          for (int c = 0; c < COLS; c += 16)
+            if (c < cols) {
+              uint32_t v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __ldcg(other + (c + i) * IG_M);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
+            }
+        }
       }
       const int n = it.n0 + 32 * q + lane;
       const bool live = n < A.N;
@@ -463,12 +501,15 @@ __device__ __forceinline__ uint32_t magnitudes(uint32_t w, uint32_t sum) {
 // their scales, 128 times their sums; and for each CTA the largest sum of a
 // row's magnitudes.  A warp a row.  A row out of range gets scale NaN.
 constexpr int WD_T = 256;
+// ROW: threads of a row, a warp or the CTA
+template <int ROW>
 __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb) {
   __shared__ int s_lo, s_hi;
-  __shared__ uint32_t s_most;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ uint32_t s_most, s_sum[WD_T / 32], s_plain[WD_T / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = threadIdx.x % ROW;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x < I8_SPLIT_CTAS) reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES)[threadIdx.x] = 0u;  // parts of a tile that are done
   if (threadIdx.x == 0) {
     s_lo = A.offsets ? i8_offset(A, 0) : 0;
     s_hi = A.offsets ? 0 : A.P;
@@ -484,30 +525,15 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
   }
   const int hi = s_hi;
   uint32_t top = 0;
-  for (long long p = s_lo + (long long)blockIdx.x * (WD_T / 32) + warp; p < hi; p += (long long)gridDim.x * (WD_T / 32)) {
+  constexpr int ROWS = WD_T / ROW;
+  for (long long p = s_lo + (long long)blockIdx.x * ROWS + threadIdx.x / ROW; p < hi; p += (long long)gridDim.x * ROWS) {
     const int row = A.rows ? __ldcg(A.rows + p) : (int)p;
     const bool ok = row >= 0 && row < A.X;
-    if (lane == 0) {
-      xs[p] = ok ? __ldcg(A.xs + row) : __uint_as_float(0x7fc00000u);
-      if (!ok) atomicOr(reinterpret_cast<uint32_t*>(A.ws), COLI_STATUS_BADIDX);
-    }
     const int8_t* src = A.x + (ok ? row : 0) * A.ldx;
     uint4* dst = xb + p * (kp / 8);
     uint32_t sum = 0;
     int plain = 0;
-#pragma unroll 4
-    for (int u = lane; u < kp / 16; u += 32) {
-      const int n = ok ? A.K - 16 * u : 0;
-      uint4 c = make_uint4(0, 0, 0, 0);
-      if (n >= 16) {
-        c = __ldcg(reinterpret_cast<const uint4*>(src + 16 * u));
-      } else if (n > 0) {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < n) w[i >> 2] |= (uint32_t)(uint8_t)src[16 * u + i] << (8 * (i & 3));
-        c = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+    auto put = [&](int u, const uint4& c) {
       sum = magnitudes(c.x, magnitudes(c.y, magnitudes(c.z, magnitudes(c.w, sum))));
       plain = dp4a_ss(c.x, 0x01010101u, dp4a_ss(c.y, 0x01010101u, dp4a_ss(c.z, 0x01010101u, dp4a_ss(c.w, 0x01010101u, plain))));
       uint32_t o[8];
@@ -515,12 +541,63 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
       cvt_int8x8(c.z, c.w, o + 4);
       dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
       dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    const int whole = ok ? A.K / 16 : 0;
+    constexpr int U = 4;  // loads under way together
+    int u = in;
+    for (; u + (U - 1) * ROW < whole; u += U * ROW) {
+      uint4 c[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) c[i] = __ldcg(reinterpret_cast<const uint4*>(src) + u + i * ROW);
+#pragma unroll
+      for (int i = 0; i < U; ++i) put(u + i * ROW, c[i]);
     }
-    top = max(top, __reduce_add_sync(0xffffffffu, sum));
+    uint4 c[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {  // the rest, and zeros up to kp
+      const int v = u + i * ROW, n = ok ? A.K - 16 * v : 0;
+      c[i] = make_uint4(0, 0, 0, 0);
+      if (v < whole) {
+        c[i] = __ldcg(reinterpret_cast<const uint4*>(src) + v);
+      } else if (n > 0 && v < kp / 16) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (k < n) w[k >> 2] |= (uint32_t)(uint8_t)src[16 * v + k] << (8 * (k & 3));
+        c[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (u + i * ROW < kp / 16) put(u + i * ROW, c[i]);
+    if (!ok)  // (a row out of range has no whole units, so the loop above covers its first ones alone)
+      for (int v = u + U * ROW; v < kp / 16; v += ROW) put(v, make_uint4(0, 0, 0, 0));
+    sum = __reduce_add_sync(0xffffffffu, sum);
     plain = __reduce_add_sync(0xffffffffu, plain);
-    if (lane == 0) reinterpret_cast<uint32_t*>(xs)[A.P + p] = 128u * (uint32_t)plain;
+    if (ROW > 32) {
+      if (lane == 0) {
+        s_sum[warp] = sum;
+        s_plain[warp] = (uint32_t)plain;
+      }
+      __syncthreads();
+      if (in == 0) {
+        sum = 0;
+        plain = 0;
+        for (int w = 0; w < WD_T / 32; ++w) {
+          sum += s_sum[w];
+          plain += (int)s_plain[w];
+        }
+      }
+      __syncthreads();
+    }
+    if (in == 0) {
+      top = max(top, sum);
+      reinterpret_cast<uint32_t*>(xs)[A.P + p] = 128u * (uint32_t)plain;
+      xs[p] = ok ? __ldcg(A.xs + row) : __uint_as_float(0x7fc00000u);
+      if (!ok) atomicOr(reinterpret_cast<uint32_t*>(A.ws), COLI_STATUS_BADIDX);
+    }
   }
-  if (lane == 0) atomicMax(&s_most, top);
+  if (in == 0) atomicMax(&s_most, top);
   __syncthreads();
   if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(A.ws + WS_HEADER_BYTES)[blockIdx.x] = s_most;
 }
@@ -564,14 +641,51 @@ cudaError_t check_kernel() {
   return cudaSuccess;
 }
 
+// K in parts: where the tiles fill less than half of the SMs, a part of at least
+// 512 codes for every SM (4096 x 6144 against 16 rows 22 us whole, 13 in four
+// parts; 1024 x 6144 against 256 rows 25 us in nine).  None is empty.
+template <int NT>
+int splits_of(const I8Params& A, long long items, int sms) {
+  const int kall = (A.K + IgShape<NT>::KSTEP - 1) / IgShape<NT>::KSTEP, ctas = sms < I8_SPLIT_CTAS ? sms : I8_SPLIT_CTAS;
+  if (NT > 128 || items < 1 || 2 * items > ctas) return 1;
+  const int most = kall / (512 / IgShape<NT>::KSTEP), n = (int)(ctas / items) < most ? (int)(ctas / items) : most;
+  if (n <= 1) return 1;
+  const int per = (kall + n - 1) / n;
+  return (kall + per - 1) / per;
+}
+
+// Cycles a call is expected to take with tiles of NT rows: a block of 128 codes
+// takes 560 to 1120 of them, and the parts of a split sum 8 a column to join.
+// (Groups: a tile and a half a group on average, at least one.)  8192 rows of
+// 4096 x 6144 take 268 us with tiles of 256 rows and 390 with 128; 512 rows of
+// 4096 x 4096 36 and TBD; 4096 rows in 32 groups of 4096 x 6144 361 and 270;
+// 16384 rows in 256 groups 1316 and 1080, 1208 with 64.
+template <int NT>
+double cycles_of(const I8Params& A, int sms) {
+  constexpr double PER = NT == 32 ? 4.4 : NT == 64 ? 4.7 : NT == 128 ? 5.5 : 8.75;  // a code
+  const int mt = (A.N + IG_M - 1) / IG_M;
+  if (A.G == 1) {
+    const long long items = (long long)((A.P + NT - 1) / NT) * mt;
+    const int splits = splits_of<NT>(A, items, sms);
+    const double waves = splits > 1 ? 1.0 / splits : (double)((items + sms - 1) / sms);
+    return PER * A.K * waves + (splits > 1 ? 8.0 * NT * splits : 0.0);
+  }
+  const int groups = A.G < A.P ? A.G : A.P;
+  const double each = (double)A.P / groups / NT + 0.5, items = groups * (each > 1.0 ? each : 1.0) * mt;
+  return PER * A.K * (items > sms ? items / sms : 1.0);
+}
+
 template <int NT>
 cudaError_t launch_nt(const IgMaps& maps, const I8Params& A, int sms, int wide, cudaStream_t st) {
   const cudaError_t e = check_kernel<NT>();
   if (e != cudaSuccess) return e;
   // (at most: a partial tile per group that can have rows)
-  const long long tiles = (long long)A.P / NT + (A.G < A.P ? A.G : A.P), items = tiles * ((A.N + IG_M - 1) / IG_M);
+  long long items = (A.G == 1 ? (A.P + NT - 1) / NT : A.P / NT + (A.G < A.P ? A.G : A.P)) * (long long)((A.N + IG_M - 1) / IG_M);
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(i8_gemm<NT>, (unsigned)(items < sms ? items : sms), IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs(), wide);
+  const int splits = splits_of<NT>(A, items, sms);
+  const long long grid = splits > 1 ? items * splits : items < sms ? items : sms;
+  return launch_pdl(i8_gemm<NT>, (unsigned)grid, IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs(), wide, splits,
+                    reinterpret_cast<uint32_t*>(A.ws + i8_off_part(A.P, A.K)));
 }
 
 }  // namespace
@@ -586,13 +700,15 @@ cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   bool ok = encode_weights(&maps.w, A);
   for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
   if (!ok) return cudaErrorInvalidValue;
-  const int most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = (A.P + WD_T / 32 - 1) / (WD_T / 32), wide = all < most ? all : most;
-  const cudaError_t e = launch_pdl(i8_widen, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
+  // a CTA a row where rows are long enough to fill it, or few
+  const bool one = A.K >= 2048 || A.P <= 4 * sms;
+  const int most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = one ? A.P : (A.P + WD_T / 32 - 1) / (WD_T / 32), wide = all < most ? all : most;
+  const cudaError_t e = launch_pdl(one ? i8_widen<WD_T> : i8_widen<32>, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
   if (e != cudaSuccess) return e;
   if (A.P <= 32) return launch_nt<32>(maps, A, sms, wide, st);
-  if (A.P <= 64) return launch_nt<64>(maps, A, sms, wide, st);
-  if (A.P < 192LL * A.G) return launch_nt<128>(maps, A, sms, wide, st);
-  return launch_nt<256>(maps, A, sms, wide, st);
+  const double c64 = cycles_of<64>(A, sms), c128 = cycles_of<128>(A, sms), c256 = cycles_of<256>(A, sms);
+  if (A.P <= 64 || (c64 < c128 && c64 < c256)) return launch_nt<64>(maps, A, sms, wide, st);
+  return c128 <= c256 ? launch_nt<128>(maps, A, sms, wide, st) : launch_nt<256>(maps, A, sms, wide, st);
 }
 
 }  // namespace colimoe

@@ -63,17 +63,41 @@ __device__ __forceinline__ void stream_block(const I8Params& A, int g, int p0, i
     __syncthreads();
     if (n0 < A.N) {
       const int8_t* w = A.w + g * A.wgroup + (long long)n0 * A.ldw + kc;
-#pragma unroll 3
-      for (int u = lane; u < units; u += 32) {
-        uint4 b[R];
+      const int8_t* wr[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) b[r] = codes16(w + (n0 + r < A.N ? r * A.ldw : 0) + 16 * u, span - 16 * u);
+      for (int r = 0; r < R; ++r) wr[r] = w + (n0 + r < A.N ? r * A.ldw : 0);
+      auto dots = [&](int u, const uint4* b) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const uint4 a = sx[t * (IS_KC / 16) + u];
 #pragma unroll
           for (int r = 0; r < R; ++r) acc[r][t] = dot16(a, b[r], acc[r][t]);
         }
+      };
+      // U units of every row under way together
+      constexpr int U = R == 2 ? 4 : 2;
+      const int whole = span / 16;
+      int u = lane;
+      for (; u + (U - 1) * 32 < whole; u += U * 32) {
+        uint4 b[U][R];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+          for (int r = 0; r < R; ++r) b[i][r] = __ldcs(reinterpret_cast<const uint4*>(wr[r]) + u + 32 * i);
+#pragma unroll
+        for (int i = 0; i < U; ++i) dots(u + 32 * i, b[i]);
+      }
+      for (; u < whole; u += 32) {
+        uint4 b[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) b[r] = __ldcs(reinterpret_cast<const uint4*>(wr[r]) + u);
+        dots(u, b);
+      }
+      if (u < units) {
+        uint4 b[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) b[r] = codes16(wr[r] + 16 * u, span - 16 * u);
+        dots(u, b);
       }
     }
   }
@@ -188,7 +212,7 @@ extern "C" int coli_i8_product(const coli_i8_product_args* a, cudaStream_t strea
   for (const void* p : ptrs)
     if (!aligned16(p)) return COLI_EALIGN;
   if (a->ldx % 16 || a->ldw % 16 || (a->G > 1 && a->w_group % 16)) return COLI_EALIGN;
-  if (a->ws_bytes < (a->P <= I8_FEW ? WS_HEADER_BYTES : i8_ws_bytes(a->P, a->K))) return COLI_EWORKSPACE;
+  if (a->ws_bytes < (i8_few(a->P, a->G) ? WS_HEADER_BYTES : i8_ws_bytes(a->P, a->K))) return COLI_EWORKSPACE;
   I8Params A{};
   A.x = a->x_codes;
   A.ldx = a->ldx;
@@ -209,5 +233,5 @@ extern "C" int coli_i8_product(const coli_i8_product_args* a, cudaStream_t strea
   A.y_type = a->y_type;
   A.ldy = a->ldy;
   A.ws = static_cast<uint8_t*>(a->ws);
-  return rc_of(a->P <= I8_FEW ? launch_i8_stream(A, stream) : launch_i8_gemm(A, stream));
+  return rc_of(i8_few(a->P, a->G) ? launch_i8_stream(A, stream) : launch_i8_gemm(A, stream));
 }

@@ -23,7 +23,11 @@ struct I8Params {
   uint8_t* ws;                // status word at 0
 };
 
-constexpr int I8_FEW = 8;     // up to this many rows: the streaming kernel
+// The streaming kernel takes up to 4 rows, and up to 8 of several groups, which
+// are most often one or two a group: 4096 x 6144 against 4 rows 11 us (13 on the
+// tensor cores), against 6 rows of one group 16 (13)
+constexpr int I8_FEW = 8;
+inline bool i8_few(int P, int G) { return P <= (G > 1 ? I8_FEW : 4); }
 
 // Workspace behind the header: a word for each CTA that widens activations,
 // the scales of the rows of y, 128 times the sums of their codes, fp16 copies of
@@ -32,7 +36,10 @@ constexpr int I8_WIDEN_CTAS = 1280;
 inline long long i8_kp(int K) { return ((long long)K + 63) / 64 * 64; }
 inline size_t i8_off_xs() { return WS_HEADER_BYTES + 4 * I8_WIDEN_CTAS; }
 inline size_t i8_off_xb(int P) { return align_up(i8_off_xs() + 8 * (size_t)P, 256); }
-inline size_t i8_ws_bytes(int P, int K) { return align_up(i8_off_xb(P) + 2 * (size_t)P * (size_t)i8_kp(K), 256); }
+inline size_t i8_off_part(int P, int K) { return align_up(i8_off_xb(P) + 2 * (size_t)P * (size_t)i8_kp(K), 256); }
+// then the parts of split sums: a tile of 128 weight rows for each CTA
+constexpr int I8_SPLIT_CTAS = 160;
+inline size_t i8_ws_bytes(int P, int K) { return i8_off_part(P, K) + (size_t)I8_SPLIT_CTAS * (P <= 32 ? 32 : P <= 64 ? 64 : 128) * 512; }
 
 // First row of group g: offsets clamped to [0, P]; ascending by running maximum
 __device__ __forceinline__ int i8_offset(const I8Params& A, int g) { return A.offsets ? min(max(__ldcg(A.offsets + g), 0), A.P) : g * A.P; }

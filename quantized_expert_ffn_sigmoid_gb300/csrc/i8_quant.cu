@@ -5,10 +5,9 @@
 // magnitude A:  scale = A / 127,  code = v * 127 / A rounded to the nearest
 // whole number, ties to even.  A row with A < 2^-100 is zeros; one that holds an
 // infinity or NaN gets scale NaN and codes 0, so that its products are NaN.
-// The quotient is taken in fp32; a value whose quotient lies so near the middle
-// of two codes that fp32 may turn it is decided by the sign of
-// v * 127 - middle * A, whose terms are exact in 64 bits: codes are those of
-// exact arithmetic.  (With SwiGLU the values themselves are fp32 results.)
+// The quotient is taken in fp32; where it lies so near the middle of two codes
+// that its rounding may decide, the sign of v * 127 - middle * A does: codes are
+// those of exact arithmetic.  (With SwiGLU the values themselves are fp32 results.)
 //
 // One pass: a row's values stay in registers between its maximum and its
 // codes (up to 8192 values, 32 a thread; longer rows are read twice).  Bound:
@@ -46,34 +45,53 @@ __device__ __forceinline__ void unit_values(const Raw8<TY>& a, const Raw8<TY>& b
   }
 }
 
-// t rounded to a whole number, as the low byte of the result's bits
-constexpr float IQ_MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole numbers, ties to even
+constexpr float IQ_MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole numbers, ties to even, into the low bits
 
-template <bool SW>
-__device__ __forceinline__ uint32_t code_of(float v, float inv, float amax) {
-  const float t = v * inv;
-  float r = t + IQ_MAGIC;
-  if (!SW) {
-    const float d = t - (r - IQ_MAGIC);
-    // (the quotient is within 127 * 2^-23 of the exact one)
-    if (fabsf(d) > 0.49996f) {
-      const float low = floorf(t);  // t is near low + 1/2
-      const double s = (double)v * 127.0 - ((double)low + 0.5) * (double)amax;
-      const float c = s > 0.0 || (s == 0.0 && ((int)low & 1)) ? low + 1.f : low;
-      r = c + IQ_MAGIC;
+// How a quotient's rounding to fp32 is kept from turning a code
+//   NONE    not at all: the values are fp32 results themselves (SwiGLU)
+//   SNAP    16-bit values: with A = b 2^j and v = a 2^i, a and b whole numbers of
+//           at most 11 bits, the quotient 127 a / (b 2^(j-i)) is the middle of two codes or at
+//           least 1 / (254 a) > 2^-20 of itself away from it, and the computed
+//           one at most 2^-23 from the exact one: rounded to 21 bits it is the
+//           middle where the exact one is, and else on its side
+//   DECIDE  fp32 values: near a middle the exact sign decides
+enum { NONE, SNAP, DECIDE };
+
+// 8 codes in two words
+template <int MODE>
+__device__ __forceinline__ uint2 codes8(const float* v, float inv, float amax) {
+  float r[8];
+  float far = 0.f;  // from a whole number, at most
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float t = v[i] * inv;
+    if (MODE == SNAP) {
+      const float c = __fmul_rn(t, 9.f);
+      t = __fsub_rn(c, __fsub_rn(c, t));
+    }
+    r[i] = t + IQ_MAGIC;
+    if (MODE == DECIDE) far = fmaxf(far, fabsf(t - (r[i] - IQ_MAGIC)));
+  }
+  if (MODE == DECIDE && far > 0.49996f) {  // (the quotient is within 127 * 2^-23 of the exact one)
+    // v * 127 - (low + 1/2) * A to its sign: the product and its rounding
+    // error, then a difference of near numbers, exact as they cancel.  (Scaled
+    // down, so that nothing overflows.)  Rare in fp32 values; 16-bit values, whose quotients
+    // often are middles, took 48 us this way instead of TBD (8192 x 6144).
+    const float f = amax > 1e30f ? 0x1p-10f : 1.f, a = amax * f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = v[i] * inv, low = floorf(t), h = low + 0.5f, p = h * a;
+      const float d = fmaf(v[i] * f, 127.f, -p) - fmaf(h, a, -p);
+      const float code = d > 0.f || (d == 0.f && ((int)low & 1)) ? low + 1.f : low;
+      if (fabsf(t - h) < 4e-5f) r[i] = code + IQ_MAGIC;
     }
   }
-  return __float_as_uint(r) & 0xffu;
-}
-
-template <bool SW>
-__device__ __forceinline__ uint2 codes8(const float* v, float inv, float amax) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    w[h] = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[h] |= code_of<SW>(v[4 * h + i], inv, amax) << (8 * i);
+    const uint32_t lo = __byte_perm(__float_as_uint(r[4 * h]), __float_as_uint(r[4 * h + 1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(r[4 * h + 2]), __float_as_uint(r[4 * h + 3]), 0x0040);
+    w[h] = __byte_perm(lo, hi, 0x5410);
   }
   return make_uint2(w[0], w[1]);
 }
@@ -114,44 +132,75 @@ __device__ __forceinline__ float row_scale(uint32_t bits, float* inv) {
   return __fdiv_rn(a, 127.f);
 }
 
-// ROW: threads of a row (a warp, or the CTA); LONG: rows of any length, read twice
+// What a thread keeps of a unit: the values as they came, or after SwiGLU
+template <typename TY, bool SW>
+struct Held {
+  Raw8<TY> raw;
+  __device__ __forceinline__ void values(float* v) const { floats8(raw, v); }
+};
+template <typename TY>
+struct Held<TY, true> {
+  float h[8];
+  __device__ __forceinline__ void values(float* v) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = h[i];
+  }
+};
+
+// ROW: threads of a row; LONG: rows of any length, read twice
 template <typename TY, bool VEC, bool SW, int ROW, bool LONG>
-__global__ void __launch_bounds__(IQ_T) i8_quantize_kernel(const QuantParams P) {
+__global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ? 6 : 1) i8_quantize_kernel(const QuantParams P) {
   __shared__ uint32_t s_max[IQ_T / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = threadIdx.x % ROW;
   pdl_wait();
   pdl_trigger();
   const long long t = (long long)blockIdx.x * (IQ_T / ROW) + threadIdx.x / ROW;
-  if (t >= P.T) return;  // (whole warps of rows, or the CTA)
+  if (t >= P.T) return;  // (all threads of a row)
   const TY* src = static_cast<const TY*>(P.x) + t * P.ldx;
   int8_t* dst = P.codes + t * P.ldc;
   const int K = P.K;
   auto reduce = [&](uint32_t m) {
     m = __reduce_max_sync(0xffffffffu, m);
     if (ROW > 32) {
+      constexpr int W = ROW / 32;
       if (lane == 0) s_max[warp] = m;
-      __syncthreads();
+      named_bar(1 + warp / W, ROW);
 #pragma unroll
-      for (int i = 0; i < IQ_T / 32; ++i) m = max(m, s_max[i]);
+      for (int i = 0; i < W; ++i) m = max(m, s_max[warp / W * W + i]);
     }
     return m;
   };
   if (!LONG) {
-    float v[IQ_U][8];
-    {
-      Raw8<TY> a[IQ_U], b[SW ? IQ_U : 1];
+    const int units = (K + ROW * 8 - 1) / (ROW * 8);  // of a thread; the branches on it are uniform
+    Held<TY, SW> x[IQ_U];
+    uint32_t m = 0;
+    if constexpr (SW) {
+      Raw8<TY> a[IQ_U], b[IQ_U];
 #pragma unroll
       for (int u = 0; u < IQ_U; ++u) {
         const int k = (in + u * ROW) * 8;
-        a[u] = load_unit<TY, VEC>(src + k, K - k);
-        if (SW) b[u] = load_unit<TY, VEC>(src + K + k, K - k);
+        if (u < units) {
+          a[u] = load_unit<TY, VEC>(src + k, K - k);
+          b[u] = load_unit<TY, VEC>(src + K + k, K - k);
+        }
       }
 #pragma unroll
-      for (int u = 0; u < IQ_U; ++u) unit_values<TY, SW>(a[u], b[SW ? u : 0], v[u]);
-    }
-    uint32_t m = 0;
+      for (int u = 0; u < IQ_U; ++u)
+        if (u < units) unit_values<TY, SW>(a[u], b[u], x[u].h);
+    } else {
 #pragma unroll
-    for (int u = 0; u < IQ_U; ++u) m = max(m, max_bits(v[u], K - (in + u * ROW) * 8));
+      for (int u = 0; u < IQ_U; ++u) {
+        const int k = (in + u * ROW) * 8;
+        if (u < units) x[u].raw = load_unit<TY, VEC>(src + k, K - k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < IQ_U; ++u)
+      if (u < units) {
+        float v[8];
+        x[u].values(v);
+        m = max(m, max_bits(v, SW ? K - (in + u * ROW) * 8 : 8));  // (loads beyond the row give zeros)
+      }
     m = reduce(m);
     float inv;
     const float scale = row_scale(m, &inv), amax = __uint_as_float(m);
@@ -159,7 +208,11 @@ __global__ void __launch_bounds__(IQ_T) i8_quantize_kernel(const QuantParams P) 
 #pragma unroll
     for (int u = 0; u < IQ_U; ++u) {
       const int k = (in + u * ROW) * 8;
-      if (k < K) store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW>(v[u], inv, amax) : make_uint2(0, 0));
+      if (u < units && k < K) {
+        float v[8];
+        x[u].values(v);
+        store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW ? NONE : sizeof(TY) == 2 ? SNAP : DECIDE>(v, inv, amax) : make_uint2(0, 0));
+      }
     }
   } else {
     uint32_t m = 0;
@@ -177,7 +230,7 @@ __global__ void __launch_bounds__(IQ_T) i8_quantize_kernel(const QuantParams P) 
     for (int k = in * 8; k < K; k += ROW * 8) {
       float v[8];
       unit_values<TY, SW>(load_unit<TY, VEC>(src + k, K - k), load_unit<TY, VEC>(src + (SW ? K : 0) + k, SW ? K - k : 0), v);
-      store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW>(v, inv, amax) : make_uint2(0, 0));
+      store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW ? NONE : sizeof(TY) == 2 ? SNAP : DECIDE>(v, inv, amax) : make_uint2(0, 0));
     }
   }
 }
@@ -191,16 +244,20 @@ __global__ void __launch_bounds__(IQ_T) i8_dequantize_kernel(const int8_t* __res
   const long long tasks = (long long)T * units, first = (long long)blockIdx.x * (IQ_T * U) + threadIdx.x;
   uint2 w[U];
   float s[U];
+  long long row[U];
+  int at[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const long long task = first + u * IQ_T;
     w[u] = make_uint2(0, 0);
     s[u] = 0.f;
+    at[u] = K;
     if (task >= tasks) continue;
-    const long long t = task / units;
-    const int k = (int)(task - t * units) * 8, n = K - k;
-    const int8_t* p = codes + t * ldc + k;
-    s[u] = __ldg(scales + t);
+    row[u] = tasks <= 0xffffffffLL ? (long long)((uint32_t)task / (uint32_t)units) : task / units;  // (a 64-bit division costs as much as the rest)
+    at[u] = (int)(task - row[u] * units) * 8;
+    const int n = K - at[u];
+    const int8_t* p = codes + row[u] * ldc + at[u];
+    s[u] = __ldg(scales + row[u]);
     if (VEC && n >= 8) {
       w[u] = __ldcs(reinterpret_cast<const uint2*>(p));
     } else {
@@ -211,19 +268,18 @@ __global__ void __launch_bounds__(IQ_T) i8_dequantize_kernel(const int8_t* __res
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long task = first + u * IQ_T;
-    if (task >= tasks) continue;
-    const long long t = task / units;
-    const int k = (int)(task - t * units) * 8, n = K - k;
+    const int n = K - at[u];
+    if (n <= 0) continue;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // the byte with its sign bit flipped is code + 128, the low byte of the float 2^23 + code + 128
-      const uint32_t b = ((i < 4 ? w[u].x : w[u].y) >> (8 * (i & 3)) & 0xffu) ^ 0x80u;
-      v[i] = (__uint_as_float(0x4b000000u | b) - 8388736.f) * s[u];
+      const uint32_t b = __byte_perm(i < 4 ? w[u].x ^ 0x80808080u : w[u].y ^ 0x80808080u, 0x4b000000u, 0x7650 | (i & 3));
+      v[i] = (__uint_as_float(b) - 8388736.f) * s[u];
     }
-    if (VEC && n >= 8) store8<TY, true>(out + t * ldo + k, 8, v);
-    else store8<TY, false>(out + t * ldo + k, n, v);
+    TY* dst = out + row[u] * ldo + at[u];
+    if (VEC && n >= 8) store8<TY, true>(dst, 8, v);
+    else store8<TY, false>(dst, n, v);
   }
 }
 
@@ -232,11 +288,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 template <typename TY, bool VEC, bool SW>
 cudaError_t quantize_v(const QuantParams& P, cudaStream_t st) {
-  if (P.K <= 32 * 8 * IQ_U) {
-    const long long grid = ((long long)P.T + IQ_T / 32 - 1) / (IQ_T / 32);
-    return launch_pdl(i8_quantize_kernel<TY, VEC, SW, 32, false>, (unsigned)grid, IQ_T, 0, st, P);
-  }
-  if (P.K <= IQ_T * 8 * IQ_U) return launch_pdl(i8_quantize_kernel<TY, VEC, SW, IQ_T, false>, (unsigned)P.T, IQ_T, 0, st, P);
+  auto go = [&](auto kernel, int row) { return launch_pdl(kernel, (unsigned)(((long long)P.T * row + IQ_T - 1) / IQ_T), IQ_T, 0, st, P); };
+  // as few threads a row as hold it
+  if (P.K <= 32 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 32, false>, 32);
+  if (P.K <= 64 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 64, false>, 64);
+  if (P.K <= 128 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 128, false>, 128);
+  if (P.K <= 256 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 256, false>, 256);
   return launch_pdl(i8_quantize_kernel<TY, VEC, SW, IQ_T, true>, (unsigned)P.T, IQ_T, 0, st, P);
 }
 template <typename TY>
