@@ -149,7 +149,7 @@ struct Held<TY, true> {
 
 // ROW: threads of a row; LONG: rows of any length, read twice
 template <typename TY, bool VEC, bool SW, int ROW, bool LONG>
-__global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ? 6 : 1) i8_quantize_kernel(const QuantParams P) {
+__global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ? 6 : 4) i8_quantize_kernel(const QuantParams P) {
   __shared__ uint32_t s_max[IQ_T / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = threadIdx.x % ROW;
   pdl_wait();

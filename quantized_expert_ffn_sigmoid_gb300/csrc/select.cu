@@ -11,10 +11,12 @@
 // underflow or saturate to one value the logits still tell them apart.
 //
 // One warp a position, E / 32 experts a lane (expert lane + 32 i) in registers.
-// Scores become integers of the same order (0: takes no part), so that a round
-// of the top-k is two warp reductions (redux): the largest key, then the lowest
-// id that has it.  Groups of whole warps take the same reductions; others are
-// scanned by one lane each in shared memory.  All sums are fp32.
+// Scores become integers of the same order (0: takes no part), so that maxima are
+// single warp reductions (redux).  The top-k first bounds the k-th best by the
+// k-th best of the lanes' best, then ranks the few keys that reach the bound, a
+// lane each; only where more than 32 do (many equal ones) it goes round by round.
+// Groups of whole warps take two reductions each; others are scanned by one lane
+// each in shared memory.  All sums are fp32.
 #include "mx4_common.cuh"
 
 namespace colimoe {
@@ -38,24 +40,27 @@ struct SelectParams {
 // floats as unsigned integers of the same order; -0 counts as +0
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // V: experts a lane; PART: x holds partial sums of the router product
 template <int V, typename TY, bool PART>
-__global__ void __launch_bounds__(256) select_kernel(const SelectParams P) {
+__global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const SelectParams P) {
   extern __shared__ float sm_sel[];  // [warps][E] scores, where groups are not whole warps
+  __shared__ uint4 s_cand[4][32];  // key, id, score
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  uint4* mine = s_cand[warp];
   const int E = P.E;
   const float NONE = -INFINITY;
   float b[V];
-  bool bias_bad = false;
+  bool bias_bad = false, bias_none = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 32 * i;
     b[i] = P.bias && e < E ? __ldg(P.bias + e) : 0.f;
     bias_bad |= !(b[i] < INFINITY);
+    bias_none |= b[i] == NONE;
   }
   pdl_wait();
   pdl_trigger();
@@ -74,12 +79,14 @@ __global__ void __launch_bounds__(256) select_kernel(const SelectParams P) {
 #pragma unroll
       for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < E ? to_f32(p[lane + 32 * i]) : NONE;
     }
-    bool bad = bias_bad;
+    bool bad = bias_bad, none = bias_none || E != 32 * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (PART && lane + 32 * i >= E) l[i] = NONE;
       bad |= !(l[i] < INFINITY);
+      none |= l[i] == NONE;
     }
+    const bool some_none = __any_sync(0xffffffffu, none);  // whether any expert takes no part
     if (__any_sync(0xffffffffu, bad)) {
       if (lane < P.k) {
         P.idx[t * P.k + lane] = -1;
@@ -88,7 +95,13 @@ __global__ void __launch_bounds__(256) select_kernel(const SelectParams P) {
       if (lane == 0 && P.status) atomicOr(P.status, COLI_STATUS_NONFINITE);
       continue;
     }
-    if (P.softmax) {
+    // Where the logits alone rank the experts, scores are needed of the selected
+    // only (softmax: also for its sum, which renormalised weights do without).
+    const bool late = !P.bias && P.keep == P.G && (!P.softmax || P.renorm);
+    if (late) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = l[i];
+    } else if (P.softmax) {
       float m = NONE, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
@@ -105,32 +118,35 @@ __global__ void __launch_bounds__(256) select_kernel(const SelectParams P) {
       for (int i = 0; i < V; ++i) s[i] *= inv;
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {  // no overflow on either side
-        const float x = expf(-fabsf(l[i])), q = __fdividef(1.f, 1.f + x);
-        s[i] = l[i] >= 0.f ? q : x * q;
-      }
+      for (int i = 0; i < V; ++i) s[i] = __fdividef(1.f, 1.f + expf(-l[i]));  // (0 from where the exponential overflows)
     }
     uint32_t key[V];
+    const bool by_logit = !P.bias;
     if (P.keep < P.G) {
-      float mine = NONE;  // lane g: score of group g
+      float group = NONE;  // lane g: score of group g
+      const bool whole = P.per % 32 == 0;
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float v = l[i] == NONE ? NONE : s[i] + b[i];
-        key[i] = v == NONE ? 0u : order_key(v);
-      }
-      if (P.per % 32 == 0) {
+        for (int i = 0; i < V; ++i) key[i] = order_key(s[i] + b[i]);
+        if (some_none)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
         const int span = P.per / 32;
         uint32_t a1 = 0, a2 = 0;  // the group's two best
         int g = 0, in = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const uint32_t m1 = __reduce_max_sync(0xffffffffu, key[i]);
-          const uint32_t who = __ballot_sync(0xffffffffu, key[i] == m1);
-          const uint32_t m2 = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? 0u : key[i]);
+          uint32_t m2 = 0;
+          if (P.top2) {
+            const uint32_t who = __ballot_sync(0xffffffffu, key[i] == m1);
+            m2 = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? 0u : key[i]);
+          }
           a2 = max(max(a2, m2), min(a1, m1));
           a1 = max(a1, m1);
           if (++in == span) {
-            if (lane == g) mine = a1 == 0 ? NONE : key_value(a1) + (P.top2 && a2 ? key_value(a2) : 0.f);
+            if (lane == g) group = a1 == 0 ? NONE : key_value(a1) + (P.top2 && a2 ? key_value(a2) : 0.f);
             a1 = a2 = 0;
             in = 0;
             ++g;
@@ -149,62 +165,127 @@ __global__ void __launch_bounds__(256) select_kernel(const SelectParams P) {
             a2 = fmaxf(a2, fminf(a1, v));
             a1 = fmaxf(a1, v);
           }
-          mine = a1 + (P.top2 && a2 != NONE ? a2 : 0.f);
+          group = a1 + (P.top2 && a2 != NONE ? a2 : 0.f);
         }
         __syncwarp();
       }
-      const uint32_t mk = lane < P.G && mine != NONE ? order_key(mine) : 0u;
+      const uint32_t mk = lane < P.G && group != NONE ? order_key(group) : 0u;
       int before = 0;
       for (int g = 0; g < P.G; ++g) {
         const uint32_t other = __shfl_sync(0xffffffffu, mk, g);
         before += other > mk || (other == mk && g < lane);
       }
       const uint32_t kept = __ballot_sync(0xffffffffu, lane < P.G && before < P.keep);
+      if (by_logit || !whole)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t g = ((uint32_t)(lane + 32 * i) * P.gmul) >> 20;
-        if (!P.bias && key[i]) key[i] = order_key(l[i]);
-        if (g >= 32 || !(kept >> g & 1u)) key[i] = 0u;
+        for (int i = 0; i < V; ++i) key[i] = order_key(by_logit ? l[i] : s[i] + b[i]);
+      if (some_none)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
+      if (whole) {
+        int g = 0, in = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (!(kept >> g & 1u)) key[i] = 0u;
+          if (++in == P.per / 32) {
+            in = 0;
+            ++g;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const uint32_t g = ((uint32_t)(lane + 32 * i) * P.gmul) >> 20;
+          if (g >= 32 || !(kept >> g & 1u)) key[i] = 0u;
+        }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float v = P.bias ? s[i] + b[i] : l[i];
-        key[i] = l[i] == NONE || v == NONE ? 0u : order_key(v);
-      }
+      for (int i = 0; i < V; ++i) key[i] = order_key(by_logit ? l[i] : s[i] + b[i]);
+      if (some_none)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
     }
-    int my_id = -1;
-    float my_w = 0.f, sum = 0.f;
+    // The k-th best of the lanes' best bounds the k-th best of all from below:
+    // what reaches it goes to shared memory, in the order of ids.
+    uint32_t top = 0, bound = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = max(top, key[i]);
     for (int j = 0; j < P.k; ++j) {
-      uint32_t best = 0;
+      bound = __reduce_max_sync(0xffffffffu, top);
+      const uint32_t who = __ballot_sync(0xffffffffu, top == bound);
+      if (lane == __ffs(who) - 1) top = 0u;
+    }
+    bound = max(bound, 1u);
+    int n = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) best = max(best, key[i]);
-      best = __reduce_max_sync(0xffffffffu, best);
-      if (best == 0u) break;  // no more experts take part
-      uint32_t id = 0xffffu;
+    for (int i = 0; i < V; ++i) {
+      const uint32_t who = __ballot_sync(0xffffffffu, key[i] >= bound);
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (key[i] >= bound && at < 32) {
+        mine[at] = make_uint4(key[i], lane + 32 * i, __float_as_uint(s[i]), 0u);
+      }
+      n += __popc(who);
+    }
+    __syncwarp();
+    auto score_of = [&](float logit, float best) { return P.softmax ? expf(logit - best) : __fdividef(1.f, 1.f + expf(-logit)); };
+    int my_id = -1, slot = lane;
+    float my_w = 0.f, sum = 0.f;
+    if (n <= 32) {
+      // a lane each: its place is how many come before it
+      const uint4 c = lane < n ? mine[lane] : make_uint4(0u, ~0u, 0u, 0u);
+      const uint32_t k0 = c.x;
+      my_id = (int)c.y;
+      my_w = __uint_as_float(c.z);
+      if (late) {
+        const float best = key_value(__reduce_max_sync(0xffffffffu, k0));
+        my_w = lane < n ? score_of(my_w, best) : 0.f;
+      }
+      if (lane < n) slot = 0;
+      for (int j = 0; j < n; ++j) {
+        const uint32_t kj = __shfl_sync(0xffffffffu, k0, j);
+        if (lane < n) slot += kj > k0 || (kj == k0 && j < lane);
+      }
+      sum = warp_sum(slot < P.k ? my_w : 0.f);
+    } else {
+      // many equal ones: round by round the best key and the lowest id that has it
+      float most = 0.f;
+      for (int j = 0; j < P.k; ++j) {
+        uint32_t best = 0;
 #pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (key[i] == best) id = lane + 32 * i;
-      id = __reduce_min_sync(0xffffffffu, id);
-      const int at = id >> 5;
-      float sv = 0.f;
+        for (int i = 0; i < V; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (best == 0u) break;  // no more experts take part
+        uint32_t id = 0xffffu;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == at) {
-          sv = s[i];
-          if (lane == (int)(id & 31u)) key[i] = 0u;
+        for (int i = V - 1; i >= 0; --i)
+          if (key[i] == best) id = lane + 32 * i;
+        id = __reduce_min_sync(0xffffffffu, id);
+        const int at = id >> 5;
+        float sv = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i == at) {
+            sv = s[i];
+            if (lane == (int)(id & 31u)) key[i] = 0u;
+          }
+        sv = __shfl_sync(0xffffffffu, sv, id & 31u);
+        if (j == 0) most = sv;
+        if (late) sv = score_of(sv, most);
+        sum += sv;
+        if (lane == j) {
+          my_id = (int)id;
+          my_w = sv;
         }
-      sv = __shfl_sync(0xffffffffu, sv, id & 31u);
-      sum += sv;
-      if (lane == j) {
-        my_id = (int)id;
-        my_w = sv;
       }
     }
+    __syncwarp();  // (the candidates are read: the next position's may come)
     if (P.renorm) my_w = sum > 0.f ? __fdiv_rn(my_w, sum) : 0.f;
-    if (lane < P.k) {
-      P.idx[t * P.k + lane] = my_id;
-      P.w[t * P.k + lane] = my_w * P.scaling;
+    if (slot < P.k) {
+      P.idx[t * P.k + slot] = my_id;
+      P.w[t * P.k + slot] = my_w * P.scaling;
     }
   }
 }
