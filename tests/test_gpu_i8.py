@@ -167,6 +167,22 @@ def test_rows_of_wide_tiles(P, N, K):
     check(P, 1, N, K, "f32", seed=P + N, ldy=N + 5)
 
 
+@pytest.mark.parametrize("P,N,K", [(9, 130, 700), (40, 300, 5000), (100, 1000, 3001), (1000, 4000, 6100), (300, 256, 20000)])
+def test_one_run_over_all_of_K(P, N, K):
+    # activations whose magnitudes add up to less than 2^24 / 255: other runs than those of the largest sums
+    x, xs, w, ws = make(P, 1, N, K, P)
+    x.copy_((torch.randn(x.shape, device="cuda") * (60000.0 / K)).clamp(-127, 127).round().to(torch.int8))
+    x[0] = 0
+    x[1 % P, :min(K, 517)] = 127                     # just below, and (two more rows) just above
+    for grow in (0, 3):
+        if grow:
+            x[2 % P, :min(K, 517 + grow)] = 127
+        y, space = torch.empty(P, N, device="cuda"), cm.new_i8_product_workspace(P, K)
+        cm.coli_i8_product(x, xs, w, ws, y, space)
+        ref, _ = want(x, xs, w, ws, [0, P], torch.arange(P, device="cuda"), torch.float32)
+        assert torch.equal(y, ref) and cm.coli_moe_status(space) == 0
+
+
 @pytest.mark.parametrize("P", [3, 40, 300])
 @pytest.mark.parametrize("K", [1023, 16384, 131071])
 def test_largest_sums(P, K):
@@ -287,3 +303,22 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for st, x, xs, w, ws, y, space in jobs:
         assert torch.equal(y, want(x, xs, w, ws, [0, len(x)], torch.arange(len(x), device="cuda"), torch.float32)[0]) and cm.coli_moe_status(space) == 0
+
+
+@pytest.mark.parametrize("P,G,N,K", [(7152, 23, 700, 5573), (1500, 9, 384, 2048), (500, 5, 300, 1000), (60, 5, 256, 1500)])
+def test_many_calls_one_behind_the_other(P, G, N, K):
+    # the pipeline of one call starts while the call before ends, and its copies land in any order
+    gen = torch.Generator(device="cuda").manual_seed(P)
+    x, xs, w, ws = make(P, G, N, K, P)
+    x.copy_((x.float() * 0.1).round().to(torch.int8))      # sums small enough for one run over all of K
+    off = [0] + sorted(torch.randint(0, P + 1, (G - 1,), generator=gen, device="cuda").tolist()) + [P]
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    space = cm.new_i8_product_workspace(P, K)
+    ref, _ = want(x, xs, w, ws, off, torch.arange(P, device="cuda"), torch.bfloat16)
+    ys = [torch.zeros(P, N, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for _ in range(100):
+        for y in ys:
+            cm.coli_i8_product(x, xs, w, ws, y, space, offsets=offsets)
+    for y in ys:
+        assert torch.equal(y, ref)
+    assert cm.coli_moe_status(space) == 0
