@@ -42,11 +42,12 @@ constexpr int IG_MAX_SMEM = 227 * 1024;
 constexpr int IG_MAXW = 9, IG_MAXB = 5;
 
 // NT: activation rows of a tile at most; BK: codes of a block, the unit in
-// which operands pass to the MMA warp.  Slots fill 208 KB.
+// which operands pass to the MMA warp.  Slots fill 208 KB, 224 for the widest
+// tiles, which leaves tables for IG_WIDE_G groups.
 template <int NT>
 struct IgShape {
   static constexpr int BK = NT == 256 ? 64 : NT == 128 ? 128 : 256;
-  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 7 : 3;
+  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 7 : 4;
   static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 3 : 5;
   static constexpr uint32_t BSLOT = NT * BK * 2;
   static constexpr uint32_t BARS = NW * IG_WSLOT + NB * BSLOT;
@@ -56,10 +57,18 @@ struct IgShape {
   // tensor memory: accumulators, then AS blocks of widened weights
   static constexpr int ACCS = NT == 256 ? 1 : 2, AW = BK / 2, AS = NT <= 64 ? 2 : NT == 128 ? 3 : 4;
   static_assert(ACCS * NT <= 256 && AS * AW <= 256 && AS <= NB, "tensor memory");
+  // A set of converters looks at every other slot, by the parity of its use, so
+  // it must not get to a slot before that slot's last use (the other set's, with
+  // NW odd) has landed: copies land in any order.  It gets to slot g once the
+  // products of slot g - 2 - AS * BK / 128 are complete.
+  static_assert(NW >= AS * BK / IG_WK + 2, "a slot's parity must not be ambiguous");
 };
 constexpr int IG_ACOL = 256;                 // first column of the widened weights
+constexpr int IG_WIDE_G = 128;
 template <int NT>
 constexpr size_t ig_smem(int G) { return IgShape<NT>::TABLES + 8 * (size_t)(G + 1) + 1024; }
+
+static_assert(ig_smem<256>(IG_WIDE_G) <= IG_MAX_SMEM && ig_smem<128>(COLI_I8_MAX_GROUPS) <= IG_MAX_SMEM, "shared memory");
 
 struct IgMaps {
   CUtensorMap w;     // weight codes [G][N][K]
@@ -708,7 +717,7 @@ cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   if (A.P <= 32) return launch_nt<32>(maps, A, sms, wide, st);
   const double c64 = cycles_of<64>(A, sms), c128 = cycles_of<128>(A, sms), c256 = cycles_of<256>(A, sms);
   if (A.P <= 64 || (c64 < c128 && c64 < c256)) return launch_nt<64>(maps, A, sms, wide, st);
-  return c128 <= c256 ? launch_nt<128>(maps, A, sms, wide, st) : launch_nt<256>(maps, A, sms, wide, st);
+  return c128 <= c256 || A.G > IG_WIDE_G ? launch_nt<128>(maps, A, sms, wide, st) : launch_nt<256>(maps, A, sms, wide, st);
 }
 
 }  // namespace colimoe
