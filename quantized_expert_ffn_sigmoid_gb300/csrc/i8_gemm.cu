@@ -3,7 +3,7 @@
 // Mathematics (i8_product.cu has the whole of it).  This target has no integer
 // tensor instruction, but codes are exact in fp16 and their products (at most
 // 2^14) and sums exact in fp32 up to 2^24: over 1024 of them.  So
-// tcgen05.mma kind::f16 sums runs of 1024 codes in tensor memory, and the runs
+// tcgen05.mma kind::f16 sums runs of codes in tensor memory, and the runs
 // are added as 32-bit integers in registers: the exact sum for any K.
 //
 // Operands.  Weights are the M side (128 rows a tile), widened to fp16 by
@@ -34,7 +34,8 @@ constexpr int IG_M = 128;                    // weight rows of a tile
 constexpr int IG_WK = 128;                   // codes of a weight slot's row
 constexpr uint32_t IG_WSLOT = IG_M * IG_WK;  // 16 KB
 constexpr int IG_RUN = 512;                  // codes of a run that is exact whatever they are: 512 * 128 * 255 < 2^24
-constexpr uint32_t IG_MOST = (1u << 24) / 255;  // largest sum of an activation row's magnitudes with which all of K is
+constexpr uint32_t IG_MOST = (1u << 24) / 255;  // sum of an activation row's magnitudes up to which any run is
+constexpr int IG_LEVELS = 9;                 // runs of 512 << level codes; the last: all of K
 constexpr int IG_MB = 8;                     // weight tiles that share activation tiles while they are in L2
 constexpr int IG_THREADS = 640;
 constexpr int IG_RCTL = 32, IG_RCONV = 64, IG_REPI = 160;
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   uint64_t* fin = d_empty + 2;
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_taddr + 1);
-  uint32_t* s_most = s_taddr + 2;
+  uint32_t* s_level = s_taddr + 2;
+  uint32_t* s_parts = s_taddr + 3;
   int* s_row0 = reinterpret_cast<int*>(sm + S::TABLES);          // [G + 1] first row of a group
   int* s_tiles = s_row0 + A.G + 1;                               // [G + 1] activation tiles before it
   uint32_t* status = reinterpret_cast<uint32_t*>(A.ws);
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     }
     mbar_init(fin, 1);
     *s_abort = 0;
-    *s_most = 0;
+    *s_level = IG_LEVELS - 1;
     fence_barrier_init();
   }
   if (warp == 2) {
@@ -196,18 +198,20 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     }
   }
   {
-    // the largest sum of magnitudes of any activation row (a value for each CTA of i8_widen)
-    const uint32_t* most = reinterpret_cast<const uint32_t*>(A.ws + WS_HEADER_BYTES);
-    uint32_t m = 0;
-    for (int i = threadIdx.x; i < wide; i += IG_THREADS) m = max(m, __ldcg(most + i));
-    m = __reduce_max_sync(0xffffffffu, m);
-    __syncthreads();  // (s_most is 0)
-    if (lane == 0) atomicMax(s_most, m);
+    // the longest runs that are exact for every activation row (a level from each CTA of i8_widen)
+    const uint32_t* level = reinterpret_cast<const uint32_t*>(A.ws + WS_HEADER_BYTES);
+    uint32_t m = IG_LEVELS - 1;
+    for (int i = threadIdx.x; i < wide; i += IG_THREADS) m = min(m, __ldcg(level + i));
+    m = __reduce_min_sync(0xffffffffu, m);
+    __syncthreads();  // (s_level is set)
+    if (lane == 0) atomicMin(s_level, m);
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const int run = *s_most <= IG_MOST ? 1 << 30 : IG_RUN;
+  const int run = *s_level < IG_LEVELS - 1 ? IG_RUN << *s_level : 1 << 30;
+  // (runs end at multiples of their length from the row's beginning)
+  const int kbegin = k0 * S::KSTEP % run;
   const uint32_t taddr = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int items = __shfl_sync(0xffffffffu, s_tiles[A.G] * mt, 0);
   const int first = (int)blockIdx.x / splits;  // (splits > 1: the only item)
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       for (int item = first; item < items; item += step) {
         const uint32_t idesc = umma_idesc((item_at(item).ntok + 15) & ~15);
         uint32_t acc = 0;          // whether the run has begun
-        int left = run / BK;       // blocks to its end
+        int left = (run - kbegin) / BK;  // blocks to its end
         for (int j = nblk; j > 0; --j) {
           if (acc == 0) ok = gwait(&d_empty[d], dph, status, s_abort) && ok;
           if (!ready) ok = gwait(&full[s], ph, status, s_abort) && ok;
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       uint32_t acc[COLS];  // (modulo 2^32, in which the end result fits)
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0;
-      for (int c = 0; c < nblk * BK; c += run) {
+      for (int c = -kbegin; c < nblk * BK; c += run) {
         pf_wait(&d_full[d], dph, status, s_abort);  // (long: suspended, out of the other warps' way)
         tmem_fence_after();
         __syncwarp();
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           d = 0;
           dph ^= 1u;
         }
-        if (run > IG_RUN) break;  // (no overflow of c)
+        if (run == 1 << 30) break;  // (no overflow of c)
       }
       if (splits > 1) {
         // the parts of a tile meet in global memory: whole numbers, so their
@@ -448,9 +452,9 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           }
         __threadfence();
         named_bar(2, 256);
-        if (warp == 12 && lane == 0) s_most[1] = atomicAdd(reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES) + item, 1u);
+        if (warp == 12 && lane == 0) *s_parts = atomicAdd(reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES) + item, 1u);
         named_bar(2, 256);
-        if (s_most[1] != (uint32_t)splits - 1) break;
+        if (*s_parts != (uint32_t)splits - 1) break;
         __threadfence();
         for (int z = 0; z < splits; ++z) {
           if (z == mine) continue;
@@ -507,14 +511,14 @@ __device__ __forceinline__ uint32_t magnitudes(uint32_t w, uint32_t sum) {
 }
 
 // The rows of y: fp16 copies of their activation codes, zero up to kp, and
-// their scales, 128 times their sums; and for each CTA the largest sum of a
-// row's magnitudes.  A warp a row.  A row out of range gets scale NaN.
+// their scales, 128 times their sums; and for each CTA the level of its runs.  A row out of range gets scale NaN.
 constexpr int WD_T = 256;
 // ROW: threads of a row, a warp or the CTA
 template <int ROW>
 __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb) {
   __shared__ int s_lo, s_hi;
-  __shared__ uint32_t s_most, s_sum[WD_T / 32], s_plain[WD_T / 32];
+  constexpr int ROWS = WD_T / ROW, WINDOWS = ROW > 32 ? 256 : 4;
+  __shared__ uint32_t s_level, s_plain[WD_T / 32], s_win[ROWS][WINDOWS];  // sums of magnitudes over 512 codes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = threadIdx.x % ROW;
   pdl_wait();
   pdl_trigger();
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
   if (threadIdx.x == 0) {
     s_lo = A.offsets ? i8_offset(A, 0) : 0;
     s_hi = A.offsets ? 0 : A.P;
-    s_most = 0;
+    s_level = IG_LEVELS - 1;
   }
   __syncthreads();
   if (A.offsets) {  // rows of any group: up to the largest offset
@@ -533,17 +537,16 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
     __syncthreads();
   }
   const int hi = s_hi;
-  uint32_t top = 0;
-  constexpr int ROWS = WD_T / ROW;
+  uint32_t level = IG_LEVELS - 1;
+  uint32_t* win = s_win[threadIdx.x / ROW];
+  const int windows = (kp + 511) / 512;
   for (long long p = s_lo + (long long)blockIdx.x * ROWS + threadIdx.x / ROW; p < hi; p += (long long)gridDim.x * ROWS) {
     const int row = A.rows ? __ldcg(A.rows + p) : (int)p;
     const bool ok = row >= 0 && row < A.X;
     const int8_t* src = A.x + (ok ? row : 0) * A.ldx;
     uint4* dst = xb + p * (kp / 8);
-    uint32_t sum = 0;
     int plain = 0;
-    auto put = [&](int u, const uint4& c) {
-      sum = magnitudes(c.x, magnitudes(c.y, magnitudes(c.z, magnitudes(c.w, sum))));
+    auto put = [&](int u, const uint4& c) {  // (32 units of a warp are a window)
       plain = dp4a_ss(c.x, 0x01010101u, dp4a_ss(c.y, 0x01010101u, dp4a_ss(c.z, 0x01010101u, dp4a_ss(c.w, 0x01010101u, plain))));
       uint32_t o[8];
       cvt_int8x8(c.x, c.y, o);
@@ -551,64 +554,74 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
       dst[2 * u] = make_uint4(o[0], o[1], o[2], o[3]);
       dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
     };
+    auto add = [&](int u, const uint4& c) {  // by whole warps
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, magnitudes(c.x, magnitudes(c.y, magnitudes(c.z, magnitudes(c.w, 0u)))));
+      if (lane == 0 && u / 32 < windows) win[u / 32] = sum;
+    };
     const int whole = ok ? A.K / 16 : 0;
     constexpr int U = 4;  // loads under way together
-    int u = in;
-    for (; u + (U - 1) * ROW < whole; u += U * ROW) {
+    for (int u = in; (u & ~31) < kp / 16; u += U * ROW) {  // (the same for a whole warp)
       uint4 c[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) c[i] = __ldcg(reinterpret_cast<const uint4*>(src) + u + i * ROW);
+      for (int i = 0; i < U; ++i) {
+        const int v = u + i * ROW;
+        c[i] = v < whole ? __ldcg(reinterpret_cast<const uint4*>(src) + v) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int i = 0; i < U; ++i) put(u + i * ROW, c[i]);
-    }
-    uint4 c[U];
+      for (int i = 0; i < U; ++i) {
+        const int v = u + i * ROW, n = ok && v == whole ? A.K & 15 : 0;
+        if (n > 0) {  // the row's last codes
+          uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < U; ++i) {  // the rest, and zeros up to kp
-      const int v = u + i * ROW, n = ok ? A.K - 16 * v : 0;
-      c[i] = make_uint4(0, 0, 0, 0);
-      if (v < whole) {
-        c[i] = __ldcg(reinterpret_cast<const uint4*>(src) + v);
-      } else if (n > 0 && v < kp / 16) {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (k < n) w[k >> 2] |= (uint32_t)(uint8_t)src[16 * v + k] << (8 * (k & 3));
-        c[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 16; ++k)
+            if (k < n) w[k >> 2] |= (uint32_t)(uint8_t)src[16 * v + k] << (8 * (k & 3));
+          c[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (v < kp / 16) put(v, c[i]);
+        add(v, c[i]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (u + i * ROW < kp / 16) put(u + i * ROW, c[i]);
-    if (!ok)  // (a row out of range has no whole units, so the loop above covers its first ones alone)
-      for (int v = u + U * ROW; v < kp / 16; v += ROW) put(v, make_uint4(0, 0, 0, 0));
-    sum = __reduce_add_sync(0xffffffffu, sum);
     plain = __reduce_add_sync(0xffffffffu, plain);
     if (ROW > 32) {
-      if (lane == 0) {
-        s_sum[warp] = sum;
-        s_plain[warp] = (uint32_t)plain;
-      }
+      if (lane == 0) s_plain[warp] = (uint32_t)plain;
       __syncthreads();
       if (in == 0) {
-        sum = 0;
         plain = 0;
-        for (int w = 0; w < WD_T / 32; ++w) {
-          sum += s_sum[w];
-          plain += (int)s_plain[w];
-        }
+        for (int w = 0; w < WD_T / 32; ++w) plain += (int)s_plain[w];
       }
-      __syncthreads();
     }
+    __syncwarp();
+    if (in < 32 && ok) {
+      // the level of this row: whole windows of 512 << level codes, each with
+      // magnitudes of at most IG_MOST in all (level 0 always)
+      uint32_t all = 0;
+      for (int w = lane; w < windows; w += 32) all += win[w];
+      if (__reduce_add_sync(0xffffffffu, all) > IG_MOST) {
+        uint32_t mine = 0;
+        for (int j = 1; j < IG_LEVELS - 1; ++j) {
+          uint32_t most = 0;
+          for (int w0 = lane << j; w0 < windows; w0 += 32 << j) {
+            uint32_t sum = 0;
+            for (int w = w0; w < min(w0 + (1 << j), windows); ++w) sum += win[w];
+            most = max(most, sum);
+          }
+          if (__reduce_max_sync(0xffffffffu, most) > IG_MOST) break;
+          mine = j;
+        }
+        level = min(level, mine);
+      }
+    }
+    if (ROW > 32) __syncthreads();
+    __syncwarp();
     if (in == 0) {
-      top = max(top, sum);
       reinterpret_cast<uint32_t*>(xs)[A.P + p] = 128u * (uint32_t)plain;
       xs[p] = ok ? __ldcg(A.xs + row) : __uint_as_float(0x7fc00000u);
       if (!ok) atomicOr(reinterpret_cast<uint32_t*>(A.ws), COLI_STATUS_BADIDX);
     }
   }
-  if (in == 0) atomicMax(&s_most, top);
+  if (in == 0) atomicMin(&s_level, level);
   __syncthreads();
-  if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(A.ws + WS_HEADER_BYTES)[blockIdx.x] = s_most;
+  if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(A.ws + WS_HEADER_BYTES)[blockIdx.x] = s_level;
 }
 
 bool encode_weights(CUtensorMap* m, const I8Params& A) {
