@@ -614,7 +614,7 @@ def _workspace_of(n: int, where: str, device):
 
 
 def _size32(*sizes):
-    if any(v >> 31 for v in sizes):
+    if any(v >> 31 > 0 for v in sizes):
         _beyond(*sizes)
 
 
