@@ -1,28 +1,44 @@
 // Products of 8-bit codes grouped by expert, on the tensor cores.
 //
 // Mathematics (i8_product.cu has the whole of it).  This target has no integer
-// tensor instruction, but codes are exact in fp16 and their products (at most
-// 2^14) and sums exact in fp32 up to 2^24: over 1024 of them.  So
-// tcgen05.mma kind::f16 sums runs of codes in tensor memory, and the runs
-// are added as 32-bit integers in registers: the exact sum for any K.
+// tensor instruction, but tcgen05.mma kind::f16 adds whole numbers exactly in
+// fp32 up to 2^24.  A weight code w becomes the fp16 whose bits are w + 128, a
+// subnormal of value (w + 128) 2^-24, for which three integer instructions a
+// four codes do; an activation code x becomes the fp16 x.  So tensor memory
+// holds 2^-24 sum x (w + 128), exact over any codes whose |x| add up to at most
+// 2^24 / 255: over 512 of them always, over all of K for most activations.  Runs
+// of such a length are added as 32-bit integers in registers, and 128 sum x, which
+// i8_widen has at hand, is taken off at the end.
 //
-// Operands.  Weights are the M side (128 rows a tile), widened to fp16 by
-// converter warps on their way from shared to tensor memory, where the
-// instruction reads them: they are read from HBM as single bytes, once for all
-// activation rows of a tile.  Activations are the N side, widened once per call
-// in the workspace (i8_widen, which also gathers the rows of y) and fetched by TMA.
+// Operands.  Weights are the M side (128 rows a tile), widened by converter warps
+// on their way from shared to tensor memory, where the instruction reads them:
+// they are read from HBM as single bytes, once for all activation rows of a tile.
+// Activations are the N side, widened once a call in the workspace (i8_widen,
+// which also gathers the rows of y and finds the runs' length) and fetched by TMA.
 //
 // One persistent CTA an SM, 20 warps meeting at mbarriers, every wait bounded:
 //   warp 0       TMA of weight codes, slots of 128 rows x 128 codes;
 //   warps 1, 3   TMA of activations, slots of up to NT rows x BK codes;
 //   warp 2       MMA issuer, blocks of BK codes;
 //   warps 4-11   converters, two sets of four (a warp for each lane quarter)
-//                that take the blocks in turn: a block's way through registers
-//                takes longer than its products;
-//   warps 12-19  epilogue: runs of 1024 codes into integer registers, at the
-//                end the scales and y.
-// Tensor memory: three accumulators of 128 columns (while one is read the
-// products go on in another) and four blocks of widened weights.
+//                that take the weight slots in turn;
+//   warps 12-19  epilogue: runs into integer registers, at the end the scales and y.
+// One barrier says that a block's operands are there, one that its products are
+// complete, which frees the activations' slot and the weights' columns alike.
+// Few tiles are split along K (splits_of), and join in the workspace.
+//
+// What bounds it (GB300; 6.79 TB/s copy, 1924 TFLOP/s bf16 measured).
+//   16384 rows over 256 groups, 4096 x 6144   1015 us, 6.4 TB/s: the weights' stream
+//   8192 rows, 4096 x 6144                    268-279 us, 1.5 PFLOP/s: of these 20 are
+//       i8_widen; the instructions' own time is 85 % at the clock (1.45 GHz) that the
+//       power limit leaves
+//   4096 rows over 32 groups, 4096 x 6144     255 us: the MMA warp's way from block to
+//       block (750-1000 cycles for 128 codes x 128 rows, the instructions 512)
+//   16 rows, 4096 x 6144                      13 us: two launches, 12 slots a CTA
+// Steps that brought most: instructions issued by one lane inside a branch (21
+// cycles each, 57 behind a wait in a predicated warp); the next block's barrier
+// looked at before a block's last instructions; conversions by integer instructions
+// alone; copies of activations by two warps.
 #include "i8_product.cuh"
 #include "tcgen05.cuh"
 #include "tensormap.cuh"

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
     bool bad = bias_bad, none = bias_none || E != 32 * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      if (PART) bad |= l[i] == NONE;  // (a product that is not finite masks nothing)
       if (PART && lane + 32 * i >= E) l[i] = NONE;
       bad |= !(l[i] < INFINITY);
       none |= l[i] == NONE;

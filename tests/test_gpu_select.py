@@ -141,6 +141,18 @@ def test_select_from_the_hidden_state(T, E, H):
         assert torch.equal(idx, i2) and (w - w2).abs().max() < 2e-5
 
 
+def test_hidden_state_without_value():
+    # no logit of a hidden state masks an expert, not even -inf everywhere
+    x, wr = torch.randn(12, 64, device="cuda"), -torch.rand(20, 64, device="cuda") - 0.1
+    x[1, 3], x[4, 0], x[5, 7] = float("inf"), float("nan"), float("-inf")
+    for T in (12, 6):
+        idx, w, ws = torch.empty(T, 4, dtype=torch.int32, device="cuda"), torch.empty(T, 4, device="cuda"), cm.new_select_workspace(T, 64, 20)
+        cm.coli_moe_select(x[:T].contiguous(), idx, w, router_w=wr, ws=ws)
+        bad = torch.tensor([t in (1, 4, 5) for t in range(T)], device="cuda")
+        assert cm.coli_moe_status(ws) == cm.STATUS_NONFINITE
+        assert (idx[bad] == -1).all() and (w[bad] == 0).all() and (idx[~bad] >= 0).all() and torch.allclose(w[~bad].sum(-1), torch.ones((), device="cuda"))
+
+
 def test_no_positions():
     e, f = torch.empty(0, 4, dtype=torch.int32, device="cuda"), torch.empty(0, 4, device="cuda")
     cm.coli_moe_select(torch.empty(0, 16, device="cuda"), e, f)
