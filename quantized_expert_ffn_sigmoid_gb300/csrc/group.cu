@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(GR_THREADS) group_count(const GroupParams P) {
 // MULTI: group_count has run over the same runs
 template <bool MULTI>
 __global__ void __launch_bounds__(GR_THREADS) group_scatter(const GroupParams P) {
-  extern __shared__ int sm_hist[];       // [warps][local], then [local] first places
+  extern __shared__ int sm_hist[];       // [warps][local], then [local] first places and [local] totals
   __shared__ int s_warp[GR_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, L = P.local;
   int* hist = sm_hist + warp * L;
@@ -87,21 +87,43 @@ __global__ void __launch_bounds__(GR_THREADS) group_scatter(const GroupParams P)
   // per expert: the warps' first places within this run, and the run's own
   // (experts ascending over the threads, so the scan below is over experts)
   const int e = tid;
+  if (MULTI) {
+    // the other runs' counts: threads share an expert's, all loads under way together
+    for (int i = tid; i < 2 * L; i += GR_THREADS) base[i] = 0;
+    __syncthreads();
+    int wide = 32;
+    while (wide < L) wide *= 2;  // threads for one run's counts
+    const int c = tid % wide, rows = GR_THREADS / wide;
+    if (c < L) {
+      int all = 0, ahead = 0;
+      for (int b0 = tid / wide; b0 < P.ctas; b0 += 16 * rows) {
+        int v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = b0 + i * rows < P.ctas ? __ldcg(P.counts + (long long)(b0 + i * rows) * L + c) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          all += v[i];
+          ahead += b0 + i * rows < (int)blockIdx.x ? v[i] : 0;
+        }
+      }
+      atomicAdd(&base[c], ahead);  // (sums of whole numbers: their order is free)
+      atomicAdd(&base[L + c], all);
+    }
+    __syncthreads();
+  }
   int total = 0, before = 0;
   if (e < L) {
+    int c[GR_WARPS];
+#pragma unroll
+    for (int w = 0; w < GR_WARPS; ++w) c[w] = sm_hist[w * L + e];
+#pragma unroll
     for (int w = 0; w < GR_WARPS; ++w) {
-      const int c = sm_hist[w * L + e];
       sm_hist[w * L + e] = total;
-      total += c;
+      total += c[w];
     }
     if (MULTI) {
-      total = 0;
-#pragma unroll 8
-      for (int b = 0; b < P.ctas; ++b) {
-        const int c = __ldcg(P.counts + (long long)b * L + e);
-        total += c;
-        before += b < (int)blockIdx.x ? c : 0;
-      }
+      before = base[e];
+      total = base[L + e];
     }
   }
   int scan = total;
@@ -266,12 +288,12 @@ extern "C" int coli_moe_group(const int32_t* topk_idx, int32_t T, int32_t top_k,
   P.slots = slots;
   P.counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + WS_HEADER_BYTES);
   P.status = static_cast<uint32_t*>(ws);
-  const size_t smem = (size_t)(GR_WARPS + 1) * P.local * 4;
+  const size_t smem = (size_t)(GR_WARPS + 2) * P.local * 4;
   static std::atomic<uint64_t> raised{0};  // the shared-memory limit, once a device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return COLI_ECUDA;
   if (!(raised.load(std::memory_order_acquire) >> dev & 1)) {
-    const int most = (GR_WARPS + 1) * MAX_E * 4;
+    const int most = (GR_WARPS + 2) * MAX_E * 4;
     if (cudaFuncSetAttribute(group_scatter<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
         cudaFuncSetAttribute(group_scatter<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
       return COLI_ECUDA;

@@ -517,23 +517,21 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512) : "memory");
 }
 
-// sum + the magnitudes of four codes
-__device__ __forceinline__ uint32_t magnitudes(uint32_t w, uint32_t sum) {
-  const uint32_t neg = (w >> 7) & 0x01010101u;
-  const uint32_t mag = (w ^ (neg * 0xffu)) + neg;  // (per byte: -128 becomes 128)
-  uint32_t d;
-  asm("dp4a.u32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(mag), "r"(0x01010101u), "r"(sum));
-  return d;
+// sum + the magnitudes of four codes: with m = -1 in the bytes of negative
+// codes, |c| = (c ^ m) + 1 there
+__device__ __forceinline__ int magnitudes(uint32_t w, int sum) {
+  const uint32_t m = prmt(w, 0u, 0xba98u);  // the bytes' signs
+  return dp4a_ss(w ^ m, 0x01010101u, dp4a_ss(m, 0xffffffffu, sum));
 }
 
 // The rows of y: fp16 copies of their activation codes, zero up to kp, and
 // their scales, 128 times their sums; and for each CTA the level of its runs.  A row out of range gets scale NaN.
 constexpr int WD_T = 256;
-// ROW: threads of a row, a warp or the CTA
+// ROW: threads of a row, a warp or four
 template <int ROW>
 __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb) {
   __shared__ int s_lo, s_hi;
-  constexpr int ROWS = WD_T / ROW, WINDOWS = ROW > 32 ? 256 : 4;
+  constexpr int ROWS = WD_T / ROW, WARPS = ROW / 32, WINDOWS = ROW > 32 ? 256 : 4;
   __shared__ uint32_t s_level, s_plain[WD_T / 32], s_win[ROWS][WINDOWS];  // sums of magnitudes over 512 codes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = threadIdx.x % ROW;
   pdl_wait();
@@ -571,7 +569,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
       dst[2 * u + 1] = make_uint4(o[4], o[5], o[6], o[7]);
     };
     auto add = [&](int u, const uint4& c) {  // by whole warps
-      const uint32_t sum = __reduce_add_sync(0xffffffffu, magnitudes(c.x, magnitudes(c.y, magnitudes(c.z, magnitudes(c.w, 0u)))));
+      const uint32_t sum = (uint32_t)__reduce_add_sync(0xffffffffu, magnitudes(c.x, magnitudes(c.y, magnitudes(c.z, magnitudes(c.w, 0)))));
       if (lane == 0 && u / 32 < windows) win[u / 32] = sum;
     };
     const int whole = ok ? A.K / 16 : 0;
@@ -586,6 +584,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int v = u + i * ROW, n = ok && v == whole ? A.K & 15 : 0;
+        if ((v & ~31) >= kp / 16) break;
         if (n > 0) {  // the row's last codes
           uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -600,10 +599,10 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
     plain = __reduce_add_sync(0xffffffffu, plain);
     if (ROW > 32) {
       if (lane == 0) s_plain[warp] = (uint32_t)plain;
-      __syncthreads();
+      named_bar(1 + warp / WARPS, ROW);
       if (in == 0) {
         plain = 0;
-        for (int w = 0; w < WD_T / 32; ++w) plain += (int)s_plain[w];
+        for (int w = 0; w < WARPS; ++w) plain += (int)s_plain[warp + w];
       }
     }
     __syncwarp();
@@ -627,7 +626,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
         level = min(level, mine);
       }
     }
-    if (ROW > 32) __syncthreads();
+    if (ROW > 32) named_bar(1 + warp / WARPS, ROW);
     __syncwarp();
     if (in == 0) {
       reinterpret_cast<uint32_t*>(xs)[A.P + p] = 128u * (uint32_t)plain;
@@ -738,10 +737,10 @@ cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   bool ok = encode_weights(&maps.w, A);
   for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
   if (!ok) return cudaErrorInvalidValue;
-  // a CTA a row where rows are long enough to fill it, or few
-  const bool one = A.K >= 2048 || A.P <= 4 * sms;
-  const int most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = one ? A.P : (A.P + WD_T / 32 - 1) / (WD_T / 32), wide = all < most ? all : most;
-  const cudaError_t e = launch_pdl(one ? i8_widen<WD_T> : i8_widen<32>, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
+  // four warps a row where rows are long enough to fill them, or few
+  const bool four = A.K >= 2048 || A.P <= 4 * sms;
+  const int rows = WD_T / (four ? 128 : 32), most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = (A.P + rows - 1) / rows, wide = all < most ? all : most;
+  const cudaError_t e = launch_pdl(four ? i8_widen<128> : i8_widen<32>, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
   if (e != cudaSuccess) return e;
   if (A.P <= 32) return launch_nt<32>(maps, A, sms, wide, st);
   const double c64 = cycles_of<64>(A, sms), c128 = cycles_of<128>(A, sms), c256 = cycles_of<256>(A, sms);

@@ -48,19 +48,21 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 template <int V, typename TY, bool PART>
 __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const SelectParams P) {
   extern __shared__ float sm_sel[];  // [warps][E] scores, where groups are not whole warps
-  __shared__ uint4 s_cand[4][32];  // key, id, score
+  __shared__ __align__(16) uint32_t s_keys[4][32];  // candidates: keys, ids and scores
+  __shared__ uint2 s_rest[4][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  uint4* mine = s_cand[warp];
+  uint32_t* keys = s_keys[warp];
+  uint2* rest = s_rest[warp];
   const int E = P.E;
   const float NONE = -INFINITY;
   float b[V];
-  bool bias_bad = false, bias_none = false;
+  bool bias_bad = false, bias_odd = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 32 * i;
     b[i] = P.bias && e < E ? __ldg(P.bias + e) : 0.f;
     bias_bad |= !(b[i] < INFINITY);
-    bias_none |= b[i] == NONE;
+    bias_odd |= !(fabsf(b[i]) < INFINITY);
   }
   pdl_wait();
   pdl_trigger();
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
     float l[V], s[V];
     if (PART) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) l[i] = 0.f;
+      for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < E ? 0.f : NONE;
       const float* p = static_cast<const float*>(P.x) + t * E;
       for (int z = 0; z < P.splits; ++z, p += (long long)P.T * E)
 #pragma unroll
@@ -79,22 +81,29 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
 #pragma unroll
       for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < E ? to_f32(p[lane + 32 * i]) : NONE;
     }
-    bool bad = bias_bad, none = bias_none || E != 32 * V;
+    // Whether any expert takes no part; looked at one by one only where a logit
+    // or bias is not finite (0 * l is NaN then) or registers are left over.
+    float z = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (PART) bad |= l[i] == NONE;  // (a product that is not finite masks nothing)
-      if (PART && lane + 32 * i >= E) l[i] = NONE;
-      bad |= !(l[i] < INFINITY);
-      none |= l[i] == NONE;
-    }
-    const bool some_none = __any_sync(0xffffffffu, none);  // whether any expert takes no part
-    if (__any_sync(0xffffffffu, bad)) {
-      if (lane < P.k) {
-        P.idx[t * P.k + lane] = -1;
-        P.w[t * P.k + lane] = 0.f;
+    for (int i = 0; i < V; ++i) z = fmaf(l[i], 0.f, z);
+    bool some_none = false;
+    if (__any_sync(0xffffffffu, bias_odd || z != z) || E != 32 * V) {
+      bool bad = bias_bad, none = E != 32 * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (PART) bad |= l[i] == NONE && lane + 32 * i < E;  // (a product that is not finite masks nothing)
+        bad |= !(l[i] < INFINITY);
+        none |= l[i] == NONE || b[i] == NONE;
       }
-      if (lane == 0 && P.status) atomicOr(P.status, COLI_STATUS_NONFINITE);
-      continue;
+      if (__any_sync(0xffffffffu, bad)) {
+        if (lane < P.k) {
+          P.idx[t * P.k + lane] = -1;
+          P.w[t * P.k + lane] = 0.f;
+        }
+        if (lane == 0 && P.status) atomicOr(P.status, COLI_STATUS_NONFINITE);
+        continue;
+      }
+      some_none = __any_sync(0xffffffffu, none);
     }
     // Where the logits alone rank the experts, scores are needed of the selected
     // only (softmax: also for its sum, which renormalised weights do without).
@@ -133,24 +142,57 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
 #pragma unroll
           for (int i = 0; i < V; ++i)
             if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
-        const int span = P.per / 32;
-        uint32_t a1 = 0, a2 = 0;  // the group's two best
-        int g = 0, in = 0;
+        if (P.G == V && P.per == 32) {
+          // a group a register: at each exchange a lane keeps half of the groups
+          // and takes its neighbour's share of them, then all lanes of one group join
+          uint32_t a1[V], a2[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const uint32_t m1 = __reduce_max_sync(0xffffffffu, key[i]);
-          uint32_t m2 = 0;
-          if (P.top2) {
-            const uint32_t who = __ballot_sync(0xffffffffu, key[i] == m1);
-            m2 = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? 0u : key[i]);
+          for (int i = 0; i < V; ++i) {
+            a1[i] = key[i];
+            a2[i] = 0u;
           }
-          a2 = max(max(a2, m2), min(a1, m1));
-          a1 = max(a1, m1);
-          if (++in == span) {
-            if (lane == g) group = a1 == 0 ? NONE : key_value(a1) + (P.top2 && a2 ? key_value(a2) : 0.f);
-            a1 = a2 = 0;
-            in = 0;
-            ++g;
+          int o = 1;
+#pragma unroll
+          for (int n = V / 2; n >= 1; n /= 2, o *= 2) {
+            const bool high = lane & o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+              const uint32_t r1 = __shfl_xor_sync(0xffffffffu, high ? a1[i] : a1[i + n], o), k1 = high ? a1[i + n] : a1[i];
+              const uint32_t r2 = n == V / 2 ? 0u : __shfl_xor_sync(0xffffffffu, high ? a2[i] : a2[i + n], o), k2 = n == V / 2 ? 0u : high ? a2[i + n] : a2[i];
+              a1[i] = max(k1, r1);
+              a2[i] = max(min(k1, r1), max(k2, r2));
+            }
+          }
+          for (; o < 32; o *= 2) {
+            const uint32_t r1 = __shfl_xor_sync(0xffffffffu, a1[0], o), r2 = __shfl_xor_sync(0xffffffffu, a2[0], o);
+            a2[0] = max(min(a1[0], r1), max(a2[0], r2));
+            a1[0] = max(a1[0], r1);
+          }
+          const float score = a1[0] == 0u ? NONE : key_value(a1[0]) + (P.top2 && a2[0] ? key_value(a2[0]) : 0.f);
+          // lane g looks at a lane that holds group g (its bits in the other order)
+          const int from = V > 1 ? (int)(__brev((uint32_t)lane) >> (32 - (31 - __clz(V)))) : 0;
+          group = __shfl_sync(0xffffffffu, score, from & 31);
+          if (lane >= P.G) group = NONE;
+        } else {
+          const int span = P.per / 32;
+          uint32_t a1 = 0, a2 = 0;  // the group's two best
+          int g = 0, in = 0;
+  #pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const uint32_t m1 = __reduce_max_sync(0xffffffffu, key[i]);
+            uint32_t m2 = 0;
+            if (P.top2) {
+              const uint32_t who = __ballot_sync(0xffffffffu, key[i] == m1);
+              m2 = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? 0u : key[i]);
+            }
+            a2 = max(max(a2, m2), min(a1, m1));
+            a1 = max(a1, m1);
+            if (++in == span) {
+              if (lane == g) group = a1 == 0 ? NONE : key_value(a1) + (P.top2 && a2 ? key_value(a2) : 0.f);
+              a1 = a2 = 0;
+              in = 0;
+              ++g;
+            }
           }
         }
       } else {
@@ -209,26 +251,38 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
         for (int i = 0; i < V; ++i)
           if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
     }
-    // The k-th best of the lanes' best bounds the k-th best of all from below:
-    // what reaches it goes to shared memory, in the order of ids.
+    // The k-th of the lanes' best (or one further down, where some are equal)
+    // bounds the k-th best of all from below.  What reaches it goes to shared memory.
     uint32_t top = 0, bound = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) top = max(top, key[i]);
     for (int j = 0; j < P.k; ++j) {
       bound = __reduce_max_sync(0xffffffffu, top);
-      const uint32_t who = __ballot_sync(0xffffffffu, top == bound);
-      if (lane == __ffs(who) - 1) top = 0u;
+      top = top == bound ? 0u : top;
     }
     bound = max(bound, 1u);
-    int n = 0;
+    int own = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t who = __ballot_sync(0xffffffffu, key[i] >= bound);
-      const int at = n + __popc(who & ((1u << lane) - 1u));
-      if (key[i] >= bound && at < 32) {
-        mine[at] = make_uint4(key[i], lane + 32 * i, __float_as_uint(s[i]), 0u);
+    for (int i = 0; i < V; ++i) own += key[i] >= bound;
+    int at = own;  // places up to and with this lane's
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += v;
+    }
+    const int n = __shfl_sync(0xffffffffu, at, 31);
+    at -= own;
+    keys[lane] = 0u;
+    __syncwarp();
+    if (n <= 32) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (key[i] >= bound) {
+          keys[at] = key[i];
+          rest[at] = make_uint2(lane + 32 * i, __float_as_uint(s[i]));
+          ++at;
+        }
       }
-      n += __popc(who);
     }
     __syncwarp();
     auto score_of = [&](float logit, float best) { return P.softmax ? expf(logit - best) : __fdividef(1.f, 1.f + expf(-logit)); };
@@ -236,19 +290,23 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
     float my_w = 0.f, sum = 0.f;
     if (n <= 32) {
       // a lane each: its place is how many come before it
-      const uint4 c = lane < n ? mine[lane] : make_uint4(0u, ~0u, 0u, 0u);
-      const uint32_t k0 = c.x;
-      my_id = (int)c.y;
-      my_w = __uint_as_float(c.z);
+      const uint32_t k0 = keys[lane];
+      const uint2 c = lane < n ? rest[lane] : make_uint2(~0u, 0u);
+      my_id = (int)c.x;
+      my_w = __uint_as_float(c.y);
       if (late) {
         const float best = key_value(__reduce_max_sync(0xffffffffu, k0));
         my_w = lane < n ? score_of(my_w, best) : 0.f;
       }
-      if (lane < n) slot = 0;
-      for (int j = 0; j < n; ++j) {
-        const uint32_t kj = __shfl_sync(0xffffffffu, k0, j);
-        if (lane < n) slot += kj > k0 || (kj == k0 && j < lane);
+      int before = 0, same = 0;
+      for (int j = 0; j < n; j += 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(keys + j);
+        before += (q.x > k0) + (q.y > k0) + (q.z > k0) + (q.w > k0);
+        same += (q.x == k0) + (q.y == k0) + (q.z == k0) + (q.w == k0);
       }
+      if (__any_sync(0xffffffffu, lane < n && same > 1))  // of equal keys the lower id comes first
+        for (int j = 0; j < n; ++j) before += keys[j] == k0 && rest[j].x < c.x;
+      if (lane < n) slot = before;
       sum = warp_sum(slot < P.k ? my_w : 0.f);
     } else {
       // many equal ones: round by round the best key and the lowest id that has it
