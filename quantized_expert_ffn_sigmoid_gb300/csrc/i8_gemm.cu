@@ -262,13 +262,14 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       bool go = true;
       for (int item = first; item < items && go; item += step) {
         const IgItem it = item_at(item);
-        const bool once = s_tiles[it.g + 1] - s_tiles[it.g] == 1;  // read for one activation tile alone
+        const bool once = A.wgroup && s_tiles[it.g + 1] - s_tiles[it.g] == 1;  // read for one activation tile alone
+        const int z = A.wgroup ? it.g : 0;  // (one matrix for all groups)
         for (int st = 0; st < nw; ++st, ++gs) {
           const uint32_t s = gs % NW;
           if (!gwait(&empty_w[s], ((gs / NW) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
           mbar_arrive_expect_tx(&full_w[s], IG_WSLOT);
-          if (once) tma_load_3d_hint(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, it.g, &full_w[s], stream);
-          else tma_load_3d(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, it.g, &full_w[s]);
+          if (once) tma_load_3d_hint(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, z, &full_w[s], stream);
+          else tma_load_3d(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, z, &full_w[s]);
         }
       }
       // every copy issued has landed before the CTA can exit (after an abort a
@@ -642,8 +643,8 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
 bool encode_weights(CUtensorMap* m, const I8Params& A) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)A.K, (cuuint64_t)A.N, (cuuint64_t)A.G};
-  const cuuint64_t strides[2] = {(cuuint64_t)A.ldw, (cuuint64_t)(A.G > 1 ? A.wgroup : A.ldw)};
+  const cuuint64_t dims[3] = {(cuuint64_t)A.K, (cuuint64_t)A.N, (cuuint64_t)(A.wgroup ? A.G : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)A.ldw, (cuuint64_t)(A.wgroup ? A.wgroup : A.ldw)};
   const cuuint32_t box[3] = {IG_WK, IG_M, 1}, estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(A.w), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -695,7 +696,7 @@ int splits_of(const I8Params& A, long long items, int sms) {
 // takes 560 to 1120 of them, and the parts of a split sum 8 a column to join.
 // (Groups: a tile and a half a group on average, at least one.)  8192 rows of
 // 4096 x 6144 take 268 us with tiles of 256 rows and 390 with 128; 512 rows of
-// 4096 x 4096 36 and TBD; 4096 rows in 32 groups of 4096 x 6144 361 and 270;
+// 4096 x 4096 36 and 27; 4096 rows in 32 groups of 4096 x 6144 361 and 270;
 // 16384 rows in 256 groups 1316 and 1080, 1208 with 64.
 template <int NT>
 double cycles_of(const I8Params& A, int sms) {
@@ -737,8 +738,9 @@ cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   bool ok = encode_weights(&maps.w, A);
   for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
   if (!ok) return cudaErrorInvalidValue;
-  // four warps a row where rows are long enough to fill them, or few
-  const bool four = A.K >= 2048 || A.P <= 4 * sms;
+  // four warps a row where rows are long enough to fill them (8192 rows of 1536:
+  // the call takes 43.6 us with a warp a row, 48.0 with four; a warp sums 4 windows at most)
+  const bool four = A.K >= 2048;
   const int rows = WD_T / (four ? 128 : 32), most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = (A.P + rows - 1) / rows, wide = all < most ? all : most;
   const cudaError_t e = launch_pdl(four ? i8_widen<128> : i8_widen<32>, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
   if (e != cudaSuccess) return e;

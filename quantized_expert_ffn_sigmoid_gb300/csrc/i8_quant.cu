@@ -18,6 +18,7 @@ namespace colimoe {
 namespace {
 
 constexpr int IQ_T = 256;   // threads of a CTA
+constexpr int IQ_FEW = 600; // rows of a small call
 constexpr int IQ_U = 4;     // 8-value units a thread holds
 constexpr float IQ_TINY = 7.8886090522101181e-31f;  // 2^-100
 
@@ -28,10 +29,35 @@ __device__ __forceinline__ Raw8<TY> load_unit(const TY* p, int n) {
   return load8<TY, false>(p, n);
 }
 
-// silu(g) u; exp of -|g| alone, so that nothing overflows on the way
-__device__ __forceinline__ float swiglu(float g, float u) {
-  const float x = expf(-fabsf(g)), q = __fdividef(1.f, 1.f + x);
-  return g * (g >= 0.f ? q : x * q) * u;
+// Two fp32 operations an instruction (x: the pair's first)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// silu(g) u of two values; exp of -|g| alone, so that nothing overflows on the way
+__device__ __forceinline__ float2 swiglu2(float2 g, float2 u) {
+  const float2 x = make_float2(expf(-fabsf(g.x)), expf(-fabsf(g.y))), y = add2(x, both(1.f));
+  float2 q;  // (of 1 to 2: within a unit)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(y.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(y.y));
+  const float2 n = make_float2(g.x >= 0.f ? 1.f : x.x, g.y >= 0.f ? 1.f : x.y);
+  return mul2(mul2(g, mul2(n, q)), u);
 }
 
 template <typename TY, bool SW>
@@ -41,7 +67,11 @@ __device__ __forceinline__ void unit_values(const Raw8<TY>& a, const Raw8<TY>& b
     float u[8];
     floats8(b, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = swiglu(v[i], u[i]);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 h = swiglu2(make_float2(v[i], v[i + 1]), make_float2(u[i], u[i + 1]));
+      v[i] = h.x;
+      v[i + 1] = h.y;
+    }
   }
 }
 
@@ -51,9 +81,10 @@ constexpr float IQ_MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole
 //   NONE    not at all: the values are fp32 results themselves (SwiGLU)
 //   SNAP    16-bit values: with A = b 2^j and v = a 2^i, a and b whole numbers of
 //           at most 11 bits, the quotient 127 a / (b 2^(j-i)) is the middle of two codes or at
-//           least 1 / (254 a) > 2^-20 of itself away from it, and the computed
-//           one at most 2^-23 from the exact one: rounded to 21 bits it is the
-//           middle where the exact one is, and else on its side
+//           least 1 / (254 a) > 2^-19 of itself away from it, and v * inv is at
+//           most 2^-24 from the exact one.  c - (c - v * inv) with c = 9 v * inv
+//           is that rounded to a multiple of 8 of its units: the middle where the
+//           exact quotient is one, and else on its side
 //   DECIDE  fp32 values: near a middle the exact sign decides
 enum { NONE, SNAP, DECIDE };
 
@@ -63,20 +94,28 @@ __device__ __forceinline__ uint2 codes8(const float* v, float inv, float amax) {
   float r[8];
   float far = 0.f;  // from a whole number, at most
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float t = v[i] * inv;
-    if (MODE == SNAP) {
-      const float c = __fmul_rn(t, 9.f);
-      t = __fsub_rn(c, __fsub_rn(c, t));
+  for (int i = 0; i < 8; i += 2) {
+    const float2 x = make_float2(v[i], v[i + 1]);
+    float2 q;
+    if (MODE == NONE) {
+      q = fma2(x, both(inv), both(IQ_MAGIC));
+    } else if (MODE == SNAP) {
+      const float2 c = mul2(x, both(9.f * inv)), d = fma2(x, both(-inv), c);
+      q = add2(fma2(d, both(-1.f), c), both(IQ_MAGIC));
+    } else {
+      const float2 t = mul2(x, both(inv));
+      q = add2(t, both(IQ_MAGIC));
+      const float2 off = fma2(add2(q, both(-IQ_MAGIC)), both(-1.f), t);
+      far = fmaxf(far, fmaxf(fabsf(off.x), fabsf(off.y)));
     }
-    r[i] = t + IQ_MAGIC;
-    if (MODE == DECIDE) far = fmaxf(far, fabsf(t - (r[i] - IQ_MAGIC)));
+    r[i] = q.x;
+    r[i + 1] = q.y;
   }
   if (MODE == DECIDE && far > 0.49996f) {  // (the quotient is within 127 * 2^-23 of the exact one)
     // v * 127 - (low + 1/2) * A to its sign: the product and its rounding
     // error, then a difference of near numbers, exact as they cancel.  (Scaled
     // down, so that nothing overflows.)  Rare in fp32 values; 16-bit values, whose quotients
-    // often are middles, took 48 us this way instead of TBD (8192 x 6144).
+    // often are middles, took 48 us this way when the other took 34 (8192 x 6144).
     const float f = amax > 1e30f ? 0x1p-10f : 1.f, a = amax * f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -116,27 +155,51 @@ struct QuantParams {
   float* scales;
 };
 
-__device__ __forceinline__ uint32_t max_bits(const float* v, int n) {
-  uint32_t m = 0;
+// the largest of m and 8 magnitudes, NaN if one is
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, const float* v) {
+  float f = __uint_as_float(m);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, i < n ? __float_as_uint(v[i]) & 0x7fffffffu : 0u);
-  return m;
+  for (int i = 0; i < 8; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(f) : "f"(v[i]), "f"(v[i + 1]));
+  return __float_as_uint(f);
 }
-// scale and factor of a row from the bits of its largest magnitude
-__device__ __forceinline__ float row_scale(uint32_t bits, float* inv) {
+// factor of a row's codes from the bits of its largest magnitude (0: no codes), and its scale
+__device__ __forceinline__ float row_inv(uint32_t bits) {
   const float a = __uint_as_float(bits);
-  *inv = 0.f;
-  if (bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-  if (a < IQ_TINY) return 0.f;
-  *inv = __fdiv_rn(127.f, a);
-  return __fdiv_rn(a, 127.f);
+  return bits >= 0x7f800000u || a < IQ_TINY ? 0.f : __fdiv_rn(127.f, a);
+}
+__device__ __forceinline__ float row_scale(uint32_t bits) {
+  const float a = __uint_as_float(bits);
+  return bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : a < IQ_TINY ? 0.f : __fdiv_rn(a, 127.f);
+}
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
-// What a thread keeps of a unit: the values as they came, or after SwiGLU
+// What a thread keeps of a unit: the values as they came, or after SwiGLU; and
+// the largest magnitude of units, as the bits of a float.  Magnitudes of 16-bit
+// values are compared as they are, two an instruction.  (Loads beyond a row give zeros.)
 template <typename TY, bool SW>
 struct Held {
   Raw8<TY> raw;
   __device__ __forceinline__ void values(float* v) const { floats8(raw, v); }
+  __device__ __forceinline__ uint32_t join(uint32_t m) const {
+    if constexpr (sizeof(TY) == 4) {
+      float v[8];
+      values(v);
+      return max_bits(m, v);
+    }
+    const uint32_t w[4] = {raw.q[0].x, raw.q[0].y, raw.q[0].z, raw.q[0].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max16x2(m, w[j] & 0x7fff7fffu);
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) {
+    if constexpr (sizeof(TY) == 4) return m;
+    const uint16_t top = (uint16_t)max(m & 0xffffu, m >> 16);
+    return __float_as_uint(to_f32(*reinterpret_cast<const TY*>(&top)));
+  }
 };
 template <typename TY>
 struct Held<TY, true> {
@@ -145,12 +208,14 @@ struct Held<TY, true> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = h[i];
   }
+  __device__ __forceinline__ uint32_t join(uint32_t m) const { return max_bits(m, h); }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
 };
 
 // ROW: threads of a row; LONG: rows of any length, read twice
 template <typename TY, bool VEC, bool SW, int ROW, bool LONG>
 __global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ? 6 : 4) i8_quantize_kernel(const QuantParams P) {
-  __shared__ uint32_t s_max[IQ_T / 32];
+  __shared__ __align__(16) uint32_t s_max[IQ_T / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = threadIdx.x % ROW;
   pdl_wait();
   pdl_trigger();
@@ -165,8 +230,16 @@ __global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ?
       constexpr int W = ROW / 32;
       if (lane == 0) s_max[warp] = m;
       named_bar(1 + warp / W, ROW);
+      if constexpr (W == 2) {
+        const uint2 a = *reinterpret_cast<const uint2*>(s_max + warp / W * W);
+        m = max(a.x, a.y);
+      } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) m = max(m, s_max[warp / W * W + i]);
+        for (int i = 0; i < W; i += 4) {
+          const uint4 a = *reinterpret_cast<const uint4*>(s_max + warp / W * W + i);
+          m = max(m, max(max(a.x, a.y), max(a.z, a.w)));
+        }
+      }
     }
     return m;
   };
@@ -196,15 +269,10 @@ __global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ?
     }
 #pragma unroll
     for (int u = 0; u < IQ_U; ++u)
-      if (u < units) {
-        float v[8];
-        x[u].values(v);
-        m = max(m, max_bits(v, SW ? K - (in + u * ROW) * 8 : 8));  // (loads beyond the row give zeros)
-      }
-    m = reduce(m);
-    float inv;
-    const float scale = row_scale(m, &inv), amax = __uint_as_float(m);
-    if (in == 0) P.scales[t] = scale;
+      if (u < units) m = x[u].join(m);
+    m = reduce(Held<TY, SW>::bits(m));
+    const float inv = row_inv(m), amax = __uint_as_float(m);
+    if (in == 0) P.scales[t] = row_scale(m);
 #pragma unroll
     for (int u = 0; u < IQ_U; ++u) {
       const int k = (in + u * ROW) * 8;
@@ -220,12 +288,11 @@ __global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ?
     for (int k = in * 8; k < K; k += ROW * 8) {
       float v[8];
       unit_values<TY, SW>(load_unit<TY, VEC>(src + k, K - k), load_unit<TY, VEC>(src + (SW ? K : 0) + k, SW ? K - k : 0), v);
-      m = max(m, max_bits(v, K - k));
+      m = max_bits(m, v);
     }
     m = reduce(m);
-    float inv;
-    const float scale = row_scale(m, &inv), amax = __uint_as_float(m);
-    if (in == 0) P.scales[t] = scale;
+    const float inv = row_inv(m), amax = __uint_as_float(m);
+    if (in == 0) P.scales[t] = row_scale(m);
 #pragma unroll 2
     for (int k = in * 8; k < K; k += ROW * 8) {
       float v[8];
@@ -289,9 +356,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 template <typename TY, bool VEC, bool SW>
 cudaError_t quantize_v(const QuantParams& P, cudaStream_t st) {
   auto go = [&](auto kernel, int row) { return launch_pdl(kernel, (unsigned)(((long long)P.T * row + IQ_T - 1) / IQ_T), IQ_T, 0, st, P); };
-  // as few threads a row as hold it
-  if (P.K <= 32 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 32, false>, 32);
-  if (P.K <= 64 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 64, false>, 64);
+  // As few threads a row as hold it; calls whose rows leave SMs idle that way take
+  // 128 at least (64 rows of 1024: 1.6 us, with 32 threads a row 2.4; 600 rows 1.8
+  // and 2.4; but 2400 rows 3.6 and 3.0, 16384 rows 19.6 and 10.9).
+  const int least = P.T <= IQ_FEW ? 128 : 32;
+  if (least <= 32 && P.K <= 32 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 32, false>, 32);
+  if (least <= 64 && P.K <= 64 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 64, false>, 64);
   if (P.K <= 128 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 128, false>, 128);
   if (P.K <= 256 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 256, false>, 256);
   return launch_pdl(i8_quantize_kernel<TY, VEC, SW, IQ_T, true>, (unsigned)P.T, IQ_T, 0, st, P);

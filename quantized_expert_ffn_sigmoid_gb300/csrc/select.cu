@@ -55,6 +55,8 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
   uint2* rest = s_rest[warp];
   const int E = P.E;
   const float NONE = -INFINITY;
+  pdl_wait();  // (the bias too may come from the kernel before: it is what a balancing step updates)
+  pdl_trigger();
   float b[V];
   bool bias_bad = false, bias_odd = false;
 #pragma unroll
@@ -64,8 +66,6 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
     bias_bad |= !(b[i] < INFINITY);
     bias_odd |= !(fabsf(b[i]) < INFINITY);
   }
-  pdl_wait();
-  pdl_trigger();
   for (long long t = (long long)blockIdx.x * warps + warp; t < P.T; t += (long long)gridDim.x * warps) {
     float l[V], s[V];
     if (PART) {
@@ -353,7 +353,7 @@ template <typename TY, bool PART>
 cudaError_t launch_select_t(const SelectParams& P, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int warps = P.T <= 4 * sms ? 1 : 4;
+  const int warps = 4;  // (against one: 600 positions 3.1 us and 3.2, 16384 15.8 and 19.0)
   long long grid = ((long long)P.T + warps - 1) / warps;
   if (grid > 16LL * sms) grid = 16LL * sms;
   const size_t smem = P.keep < P.G && P.per % 32 ? (size_t)warps * P.E * 4 : 0;

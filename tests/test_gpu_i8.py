@@ -250,6 +250,22 @@ def test_expert_records_as_weights():
             assert live.all() and torch.equal(y, ref)
 
 
+@pytest.mark.parametrize("P", [6, 40, 700])
+def test_weights_at_any_stride(P):
+    # one matrix for all groups (stride 0), and matrices whose rows stand between one another
+    G, N, K = 5, 140, 200
+    x, xs, w, ws = make(P, G, N, K, 21)
+    cuts = [0, P // 8, P // 8, P // 2, P - 1, P]
+    off = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    mixed = torch.zeros(N, G, 208, dtype=torch.int8, device="cuda").permute(1, 0, 2)[:, :, :K]
+    mixed.copy_(w)
+    for weights, scales in ((w[:1].expand(G, N, K), ws), (w[:1].expand(G, N, K), ws[:1].expand(G, N)), (mixed, ws)):
+        y, space = torch.empty(P, N, device="cuda"), cm.new_i8_product_workspace(P, K)
+        cm.coli_i8_product(x, xs, weights, scales, y, space, offsets=off)
+        ref, live = want(x, xs, weights, scales, cuts, torch.arange(P, device="cuda"), torch.float32)
+        assert live.all() and torch.equal(y, ref)
+
+
 def test_scales_without_value():
     for P in (4, 64):
         x, xs, w, ws = make(P, 1, 130, 200, 1)
@@ -322,3 +338,48 @@ def test_many_calls_one_behind_the_other(P, G, N, K):
     for y in ys:
         assert torch.equal(y, ref)
     assert cm.coli_moe_status(space) == 0
+
+
+def test_weights_beyond_32_bit_offsets():
+    G, N, K = 180, 4096, 6144                      # 4.5 GB of codes
+    for P in (6, 400):
+        gen = torch.Generator(device="cuda").manual_seed(P)
+        w = torch.zeros(G, N, K, dtype=torch.int8, device="cuda")
+        for g in (0, 88, G - 1):
+            w[g] = torch.randint(-128, 128, (N, K), generator=gen, device="cuda").to(torch.int8)
+        ws = torch.rand(G, N, generator=gen, device="cuda")
+        x, xs, _, _ = make(P, 1, 1, K, P)
+        cuts = torch.full((G + 1,), P // 2, dtype=torch.int32, device="cuda")
+        cuts[0], cuts[1:89], cuts[G] = 0, P // 3, P
+        y, space = torch.empty(P, N, device="cuda"), cm.new_i8_product_workspace(P, K)
+        cm.coli_i8_product(x, xs, w, ws, y, space, offsets=cuts)
+        for g, a, b in ((0, 0, P // 3), (88, P // 3, P // 2), (G - 1, P // 2, P)):
+            ref, _ = want(x[a:b], xs[a:b], w[g:g + 1], ws[g:g + 1], [0, b - a], torch.arange(b - a, device="cuda"), torch.float32)
+            assert torch.equal(y[a:b], ref)
+        del w
+
+
+def test_rows_beyond_32_bit_offsets():
+    # codes, their activations and the results of products, each beyond 2^31 bytes or values
+    T, K = 40000, 60000
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    some = torch.tensor([0, 17895, 35791, 35792, T - 1], device="cuda")
+    x[some] = torch.randn(5, K, device="cuda").bfloat16()
+    codes, scales = torch.empty(T, K, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    cm.coli_i8_quantize(x, codes, scales)
+    q, _ = token8.quantize(x[some].double().cpu().numpy())
+    assert np.array_equal(codes[some].cpu().numpy(), q) and int((scales != 0).sum()) == 5
+    cm.coli_i8_dequantize(codes, scales, x)
+    assert torch.equal(x[some], (codes[some].float() * scales[some][:, None]).bfloat16())
+    del x
+    w, ws = torch.randint(-128, 128, (64, K), device="cuda").to(torch.int8), torch.rand(64, device="cuda")
+    y, space = torch.empty(T, 64, device="cuda"), cm.new_i8_product_workspace(T, K)
+    cm.coli_i8_product(codes, scales, w, ws, y, space)
+    ref, _ = want(codes[some], scales[some], w[None], ws[None], [0, 5], torch.arange(5, device="cuda"), torch.float32)
+    assert cm.coli_moe_status(space) == 0 and torch.equal(y[some], ref)
+    del space, codes
+    x, xs, w, ws = make(T, 1, K, 64, 3)
+    y, space = torch.empty(T, K, dtype=torch.bfloat16, device="cuda"), cm.new_i8_product_workspace(T, 64)
+    cm.coli_i8_product(x, xs, w[0], ws[0], y, space)
+    ref, _ = want(x[some], xs[some], w, ws, [0, 5], torch.arange(5, device="cuda"), torch.bfloat16)
+    assert torch.equal(y[some], ref)

@@ -162,6 +162,23 @@ def test_no_positions():
     cm.coli_moe_combine(torch.empty(0, 8, device="cuda"), e, f, torch.empty(0, 8, device="cuda"))
 
 
+@pytest.mark.parametrize("T", [1, 3000])
+def test_bias_of_the_kernel_before(T):
+    # a bias that the step before on the stream updates
+    E, k = 64, 4
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    l = torch.linspace(-1.0, 1.0, E, device="cuda").expand(T, E).contiguous()
+    biases = 4 * torch.stack([torch.randperm(E, generator=gen, device="cuda") for _ in range(40)]).float()  # (whole numbers: v lie apart)
+    bias = torch.zeros(E, device="cuda")
+    idx = torch.empty(40, T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(40, T, k, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(40):
+        bias.copy_(biases[i])
+        cm.coli_moe_select(l, idx[i], w[i], bias=bias, score=cm.SCORE_SIGMOID)
+    assert torch.equal(idx, biases.topk(k, -1).indices.int()[:, None].expand(40, T, k))
+
+
 # ------------------------------------------------------------------------ grouping
 def run_group(idx, E, rank=0, size=0):
     T, k = idx.shape
