@@ -27,18 +27,21 @@
 // complete, which frees the activations' slot and the weights' columns alike.
 // Few tiles are split along K (splits_of), and join in the workspace.
 //
-// What bounds it (GB300; 6.79 TB/s copy, 1924 TFLOP/s bf16 measured).
-//   16384 rows over 256 groups, 4096 x 6144   1015 us, 6.4 TB/s: the weights' stream
-//   8192 rows, 4096 x 6144                    268-279 us, 1.5 PFLOP/s: of these 20 are
-//       i8_widen; the instructions' own time is 85 % at the clock (1.45 GHz) that the
-//       power limit leaves
-//   4096 rows over 32 groups, 4096 x 6144     255 us: the MMA warp's way from block to
-//       block (750-1000 cycles for 128 codes x 128 rows, the instructions 512)
+// What bounds it (GB300; 6.79 TB/s copy, 1924 TFLOP/s bf16 measured; times of whole calls).
+//   16384 rows over 256 groups, 4096 x 6144   930-955 us, 6.9 TB/s: the weights' stream
+//   8192 rows, 4096 x 6144                    274 us, 1.5 PFLOP/s: of these 20 are
+//       i8_widen; the instructions' own time is 96 % of the others at the clock (1.45
+//       GHz) that the power limit leaves, 74 % at the full one
+//   4096 rows over 32 groups, 4096 x 6144     238 us: the operands' way from L2 (a block of
+//       128 codes x 128 rows is 48 KB for 512 cycles of instructions; 46-55 bytes a
+//       cycle arrive)
 //   16 rows, 4096 x 6144                      13 us: two launches, 12 slots a CTA
 // Steps that brought most: instructions issued by one lane inside a branch (21
 // cycles each, 57 behind a wait in a predicated warp); the next block's barrier
 // looked at before a block's last instructions; conversions by integer instructions
-// alone; copies of activations by two warps.
+// alone; copies of activations by two warps; for tiles of 128 rows four slots of
+// activations and five of weights (three and seven: 257 us for the 32 groups, not 238).
+// Blocks of half the codes cost a third (the same: 347).
 #include "i8_product.cuh"
 #include "tcgen05.cuh"
 #include "tensormap.cuh"
@@ -64,8 +67,8 @@ constexpr int IG_MAXW = 9, IG_MAXB = 5;
 template <int NT>
 struct IgShape {
   static constexpr int BK = NT == 256 ? 64 : NT == 128 ? 128 : 256;
-  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 7 : 4;
-  static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 3 : 5;
+  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 5 : 4;
+  static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 4 : 5;
   static constexpr uint32_t BSLOT = NT * BK * 2;
   static constexpr uint32_t BARS = NW * IG_WSLOT + NB * BSLOT;
   static constexpr uint32_t TABLES = BARS + 512;
@@ -287,7 +290,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       bool go = true;
       for (int item = first; item < items && go; item += step) {
         const IgItem it = item_at(item);
-        const int all = (it.ntok + 15) / 16, first = BK == 64 && half ? 8 : 0, n16 = BK == 64 ? min(max(all - first, 0), 8) : all;
+        constexpr int HALF = NT / 32;  // sixteens of rows
+        const int all = (it.ntok + 15) / 16, first = BK == 64 && half ? HALF : 0, n16 = BK == 64 ? min(max(all - first, 0), HALF) : all;
         for (int j = 0; j < nblk; ++j, ++gs) {
           const uint32_t s = gs % NB;
           if (!gwait(&done[s], ((gs / NB) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
@@ -430,6 +434,22 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     for (int item = first; item < items; item += step) {
       const IgItem it = item_at(item);
       const int cols = min(max(it.ntok - col0, 0), COLS);
+      const int n = it.n0 + 32 * q + lane;
+      const bool live = n < A.N;
+      const float sw = live ? __ldg(A.ws_ + it.g * A.wsgroup + n) : 0.f;
+      // scales and sums of the tile's rows, loaded ahead of the sums (not in the
+      // widest tiles, whose accumulators fill the registers): lane l has columns l, l + 32
+      constexpr bool AHEAD = COLS <= 64;
+      constexpr int HELD = AHEAD ? (COLS + 31) / 32 : 1;
+      float sx_[HELD];
+      uint32_t bias_[HELD];
+      if (AHEAD)
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) {
+          const int c = 32 * h + lane;
+          sx_[h] = c < cols ? __ldcg(xs + it.row0 + col0 + c) : 0.f;
+          bias_[h] = c < cols ? __ldcg(xsum + it.row0 + col0 + c) : 0u;
+        }
       uint32_t acc[COLS];  // (modulo 2^32, in which the end result fits)
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0;
@@ -457,15 +477,14 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         if (run == 1 << 30) break;  // (no overflow of c)
       }
       if (splits > 1) {
-        // the parts of a tile meet in global memory: whole numbers, so their
-        // order is free; the last part adds the others and goes on to y
-        const int mine = (int)blockIdx.x % splits, row = 32 * q + lane;
-        uint32_t* tile = part + (size_t)item * splits * (NT * IG_M) + col0 * IG_M + row;
+        // the parts of a tile are added up in global memory (zeroed by i8_widen):
+        // whole numbers, so their order is free; the last part goes on to y
+        uint32_t* tile = part + (size_t)item * (NT * IG_M) + col0 * IG_M + 32 * q + lane;
 #pragma unroll
         for (int c = 0; c < COLS; c += 16)  // (whole sixteens of columns, also behind the last)
           if (c < cols) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) __stcg(tile + (size_t)mine * (NT * IG_M) + (c + i) * IG_M, acc[c + i]);
+            for (int i = 0; i < 16; ++i) atomicAdd(tile + (c + i) * IG_M, acc[c + i]);
           }
         __threadfence();
         named_bar(2, 256);
@@ -473,23 +492,13 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         named_bar(2, 256);
         if (*s_parts != (uint32_t)splits - 1) break;
         __threadfence();
-        for (int z = 0; z < splits; ++z) {
-          if (z == mine) continue;
-          const uint32_t* other = tile + (size_t)z * (NT * IG_M);
 #pragma unroll
-          for (int c = 0; c < COLS; c += 16)
-            if (c < cols) {
-              uint32_t v[16];
+        for (int c = 0; c < COLS; c += 16)
+          if (c < cols) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __ldcg(other + (c + i) * IG_M);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
-            }
-        }
+            for (int i = 0; i < 16; ++i) acc[c + i] = __ldcg(tile + (c + i) * IG_M);
+          }
       }
-      const int n = it.n0 + 32 * q + lane;
-      const bool live = n < A.N;
-      const float sw = live ? __ldg(A.ws_ + it.g * A.wsgroup + n) : 0.f;
       const long long at = (long long)(it.row0 + col0) * A.ldy + n;
       auto store = [&](auto* y) {
         using TY = std::remove_pointer_t<decltype(y)>;
@@ -497,12 +506,17 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
 #pragma unroll
         for (int c = 0; c < COLS; c += 16)
           if (c < cols) {
-            const int p = it.row0 + col0 + c + (lane & 15);
-            const float sx = c + (lane & 15) < cols ? __ldcg(xs + p) : 0.f;
-            const uint32_t bias = c + (lane & 15) < cols ? __ldcg(xsum + p) : 0u;
+            float sx = sx_[AHEAD ? c / 32 : 0];
+            uint32_t bias = bias_[AHEAD ? c / 32 : 0];
+            if (!AHEAD) {
+              const int p = it.row0 + col0 + c + (lane & 15);
+              sx = c + (lane & 15) < cols ? __ldcg(xs + p) : 0.f;
+              bias = c + (lane & 15) < cols ? __ldcg(xsum + p) : 0u;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float v = i8_value((int)(acc[c + i] - __shfl_sync(0xffffffffu, bias, i)), __shfl_sync(0xffffffffu, sx, i), sw);
+              const int from = AHEAD ? c % 32 + i : i;
+              const float v = i8_value((int)(acc[c + i] - __shfl_sync(0xffffffffu, bias, from)), __shfl_sync(0xffffffffu, sx, from), sw);
               if (live && c + i < cols) y[(c + i) * A.ldy] = from_f32<TY>(v);
             }
           }
@@ -530,14 +544,16 @@ __device__ __forceinline__ int magnitudes(uint32_t w, int sum) {
 constexpr int WD_T = 256;
 // ROW: threads of a row, a warp or four
 template <int ROW>
-__global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb) {
+__global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float* __restrict__ xs, uint4* __restrict__ xb, uint4* __restrict__ zero, int zeros) {
   __shared__ int s_lo, s_hi;
   constexpr int ROWS = WD_T / ROW, WARPS = ROW / 32, WINDOWS = ROW > 32 ? 256 : 4;
   __shared__ uint32_t s_level, s_plain[WD_T / 32], s_win[ROWS][WINDOWS];  // sums of magnitudes over 512 codes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = threadIdx.x % ROW;
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && threadIdx.x < I8_SPLIT_CTAS) reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES)[threadIdx.x] = 0u;  // parts of a tile that are done
+  // split sums: the parts of a tile that are done, and their sums
+  if (blockIdx.x == 0 && threadIdx.x < I8_SPLIT_TILES) reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES)[threadIdx.x] = 0u;
+  for (int i = blockIdx.x * WD_T + threadIdx.x; i < zeros; i += gridDim.x * WD_T) zero[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     s_lo = A.offsets ? i8_offset(A, 0) : 0;
     s_hi = A.offsets ? 0 : A.P;
@@ -681,10 +697,11 @@ cudaError_t check_kernel() {
 
 // K in parts: where the tiles fill less than half of the SMs, a part of at least
 // 512 codes for every SM (4096 x 6144 against 16 rows 22 us whole, 13 in four
-// parts; 1024 x 6144 against 256 rows 25 us in nine).  None is empty.
+// parts; parts of 256 codes gain nothing, and 500 x 496 against 30 rows takes 9.9 us
+// in two of them, 8.4 whole).  None is empty.
 template <int NT>
 int splits_of(const I8Params& A, long long items, int sms) {
-  const int kall = (A.K + IgShape<NT>::KSTEP - 1) / IgShape<NT>::KSTEP, ctas = sms < I8_SPLIT_CTAS ? sms : I8_SPLIT_CTAS;
+  const int kall = (A.K + IgShape<NT>::KSTEP - 1) / IgShape<NT>::KSTEP, ctas = sms < 2 * I8_SPLIT_TILES ? sms : 2 * I8_SPLIT_TILES;
   if (NT > 128 || items < 1 || 2 * items > ctas) return 1;
   const int most = kall / (512 / IgShape<NT>::KSTEP), n = (int)(ctas / items) < most ? (int)(ctas / items) : most;
   if (n <= 1) return 1;
@@ -692,38 +709,56 @@ int splits_of(const I8Params& A, long long items, int sms) {
   return (kall + per - 1) / per;
 }
 
-// Cycles a call is expected to take with tiles of NT rows: a block of 128 codes
-// takes 560 to 1120 of them, and the parts of a split sum 8 a column to join.
-// (Groups: a tile and a half a group on average, at least one.)  8192 rows of
-// 4096 x 6144 take 268 us with tiles of 256 rows and 390 with 128; 512 rows of
-// 4096 x 4096 36 and 27; 4096 rows in 32 groups of 4096 x 6144 361 and 270;
-// 16384 rows in 256 groups 1316 and 1080, 1208 with 64.
+// Cycles a call is expected to take with tiles of NT rows, fitted to measured
+// times: a code of a full tile's rows takes PER of them (2.4 for its 128 weights, the
+// rest falls with the rows), and a tile END where its epilogue is not hidden behind
+// the next tile's products (the widest), a call START + JOIN more where its sums
+// are split.  (Groups: a tile and a half a group on average, at least one.)  Measured, tiles
+// of 64, 128, 256 rows, us: 8192 rows of 4096 x 6144 406, 356, 274; 512 rows of
+// 4096 x 4096 29, 25, 35; 128 rows of 4096 x 6144 21, 23, -; in 32 groups of 4096 x 6144
+// 4000 rows a group of 250 456, 368, 403, of 1000 1631, 1156, 1100; 16384 rows in 256 groups
+// 1091, 930, -.
 template <int NT>
 double cycles_of(const I8Params& A, int sms) {
-  constexpr double PER = NT == 32 ? 4.4 : NT == 64 ? 4.7 : NT == 128 ? 5.5 : 8.75;  // a code
+  constexpr double WEIGHTS = 2.4, PER = NT == 64 ? 4.4 : NT == 128 ? 6.9 : 8.8, END = NT == 256 ? 22000 : 0, START = NT == 128 ? 4700 : 0,
+                   JOIN = NT == 128 ? 10000 : 5700;
   const int mt = (A.N + IG_M - 1) / IG_M;
   if (A.G == 1) {
     const long long items = (long long)((A.P + NT - 1) / NT) * mt;
     const int splits = splits_of<NT>(A, items, sms);
-    const double waves = splits > 1 ? 1.0 / splits : (double)((items + sms - 1) / sms);
-    return PER * A.K * waves + (splits > 1 ? 8.0 * NT * splits : 0.0);
+    return START + (splits > 1 ? PER * A.K / splits + JOIN : (PER * A.K + END) * (double)((items + sms - 1) / sms));
   }
   const int groups = A.G < A.P ? A.G : A.P;
-  const double each = (double)A.P / groups / NT + 0.5, items = groups * (each > 1.0 ? each : 1.0) * mt;
-  return PER * A.K * (items > sms ? items / sms : 1.0);
+  const double each = (double)A.P / groups / NT + 0.5, tiles = groups * (each > 1.0 ? each : 1.0) * mt, share = tiles > sms ? 1.0 / sms : 1.0 / tiles;
+  return START + ((WEIGHTS * A.K + END) * tiles + (PER - WEIGHTS) / NT * A.K * (double)A.P * mt) * share;
 }
 
 template <int NT>
-cudaError_t launch_nt(const IgMaps& maps, const I8Params& A, int sms, int wide, cudaStream_t st) {
-  const cudaError_t e = check_kernel<NT>();
+cudaError_t launch_nt(const I8Params& A, int sms, cudaStream_t st) {
+  cudaError_t e = check_kernel<NT>();
   if (e != cudaSuccess) return e;
+  const int kp = (int)i8_kp(A.K);
+  float* xs = reinterpret_cast<float*>(A.ws + i8_off_xs());
+  uint8_t *xb = A.ws + i8_off_xb(A.P), *part = A.ws + i8_off_part(A.P, A.K);
+  IgMaps maps;
+  bool ok = encode_weights(&maps.w, A);
+  for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
+  if (!ok) return cudaErrorInvalidValue;
   // (at most: a partial tile per group that can have rows)
-  long long items = (A.G == 1 ? (A.P + NT - 1) / NT : A.P / NT + (A.G < A.P ? A.G : A.P)) * (long long)((A.N + IG_M - 1) / IG_M);
+  const long long items = (A.G == 1 ? (A.P + NT - 1) / NT : A.P / NT + (A.G < A.P ? A.G : A.P)) * (long long)((A.N + IG_M - 1) / IG_M);
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const int splits = splits_of<NT>(A, items, sms);
+  const int splits = splits_of<NT>(A, items, sms), zeros = splits > 1 ? (int)items * NT * IG_M / 4 : 0;
+  // four warps a row where rows are long enough to fill them (8192 rows of 1536:
+  // the call takes 43.6 us with a warp a row, 48.0 with four; a warp sums 4 windows at most)
+  const bool four = A.K >= 2048;
+  const int rows = WD_T / (four ? 128 : 32), most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS;
+  int wide = (A.P + rows - 1) / rows;
+  if (wide < zeros / (4 * WD_T)) wide = zeros / (4 * WD_T);
+  if (wide > most) wide = most;
+  e = launch_pdl(four ? i8_widen<128> : i8_widen<32>, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb), reinterpret_cast<uint4*>(part), zeros);
+  if (e != cudaSuccess) return e;
   const long long grid = splits > 1 ? items * splits : items < sms ? items : sms;
-  return launch_pdl(i8_gemm<NT>, (unsigned)grid, IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs(), wide, splits,
-                    reinterpret_cast<uint32_t*>(A.ws + i8_off_part(A.P, A.K)));
+  return launch_pdl(i8_gemm<NT>, (unsigned)grid, IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs(), wide, splits, reinterpret_cast<uint32_t*>(part));
 }
 
 }  // namespace
@@ -731,23 +766,10 @@ cudaError_t launch_nt(const IgMaps& maps, const I8Params& A, int sms, int wide, 
 cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int kp = (int)i8_kp(A.K);
-  float* xs = reinterpret_cast<float*>(A.ws + i8_off_xs());
-  uint8_t* xb = A.ws + i8_off_xb(A.P);
-  IgMaps maps;
-  bool ok = encode_weights(&maps.w, A);
-  for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
-  if (!ok) return cudaErrorInvalidValue;
-  // four warps a row where rows are long enough to fill them (8192 rows of 1536:
-  // the call takes 43.6 us with a warp a row, 48.0 with four; a warp sums 4 windows at most)
-  const bool four = A.K >= 2048;
-  const int rows = WD_T / (four ? 128 : 32), most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS, all = (A.P + rows - 1) / rows, wide = all < most ? all : most;
-  const cudaError_t e = launch_pdl(four ? i8_widen<128> : i8_widen<32>, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb));
-  if (e != cudaSuccess) return e;
-  if (A.P <= 32) return launch_nt<32>(maps, A, sms, wide, st);
+  if (A.P <= 32) return launch_nt<32>(A, sms, st);
   const double c64 = cycles_of<64>(A, sms), c128 = cycles_of<128>(A, sms), c256 = cycles_of<256>(A, sms);
-  if (A.P <= 64 || (c64 < c128 && c64 < c256)) return launch_nt<64>(maps, A, sms, wide, st);
-  return c128 <= c256 || A.G > IG_WIDE_G ? launch_nt<128>(maps, A, sms, wide, st) : launch_nt<256>(maps, A, sms, wide, st);
+  if (A.P <= 64 || (c64 < c128 && c64 < c256)) return launch_nt<64>(A, sms, st);
+  return c128 <= c256 || A.G > IG_WIDE_G ? launch_nt<128>(A, sms, st) : launch_nt<256>(A, sms, st);
 }
 
 }  // namespace colimoe

@@ -9,7 +9,9 @@
 // Few rows (up to 8): a stream of the weights through 4-way integer dots, with
 // the codes of the group's rows in shared memory.  A warp takes R weight rows
 // (2, or 4 where 3 or more activation rows reuse the loads from shared memory),
-// each lane 16 bytes of every 512; the lanes' sums meet in redux.  Bound: HBM.
+// each lane 16 bytes of every 512; the lanes' sums meet in redux.  Bound: HBM;
+// 4096 x 6144 against one row 6.0 us (25 MB, in L2 here; 9.9 us cold), 8 experts' of
+// 256 for one position 41.7 us (4.8 TB/s: the last CTAs' tail).
 #include "i8_product.cuh"
 
 namespace colimoe {

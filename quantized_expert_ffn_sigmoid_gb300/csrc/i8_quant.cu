@@ -11,7 +11,11 @@
 //
 // One pass: a row's values stay in registers between its maximum and its
 // codes (up to 8192 values, 32 a thread; longer rows are read twice).  Bound:
-// HBM, 2 or 4 bytes in and one out a value.
+// HBM, 2 or 4 bytes in and one out a value, and close to it the instructions:
+// two values an fp32 instruction and, of 16-bit values, two magnitudes a
+// comparison.  8192 x 6144 bf16 24.5 us (6.2 TB/s of 6.79 copied; one value an
+// instruction 34), fp32 8192 x 4096 26 us (6.5), SwiGLU of 16384 x 2048 bf16 30.6 us
+// (5.5: exponentials); back to bf16, 8192 x 6144, 24 us (6.3).
 #include "mx4_common.cuh"
 
 namespace colimoe {
@@ -115,7 +119,7 @@ __device__ __forceinline__ uint2 codes8(const float* v, float inv, float amax) {
     // v * 127 - (low + 1/2) * A to its sign: the product and its rounding
     // error, then a difference of near numbers, exact as they cancel.  (Scaled
     // down, so that nothing overflows.)  Rare in fp32 values; 16-bit values, whose quotients
-    // often are middles, took 48 us this way when the other took 34 (8192 x 6144).
+    // often are middles, took 48 us this way when the other took 34 (8192 x 6144, before two values an instruction).
     const float f = amax > 1e30f ? 0x1p-10f : 1.f, a = amax * f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -357,8 +361,8 @@ template <typename TY, bool VEC, bool SW>
 cudaError_t quantize_v(const QuantParams& P, cudaStream_t st) {
   auto go = [&](auto kernel, int row) { return launch_pdl(kernel, (unsigned)(((long long)P.T * row + IQ_T - 1) / IQ_T), IQ_T, 0, st, P); };
   // As few threads a row as hold it; calls whose rows leave SMs idle that way take
-  // 128 at least (64 rows of 1024: 1.6 us, with 32 threads a row 2.4; 600 rows 1.8
-  // and 2.4; but 2400 rows 3.6 and 3.0, 16384 rows 19.6 and 10.9).
+  // 128 at least (600 rows of 1024: 1.66 us, with 32 threads a row 1.89; but 2400
+  // rows 3.1 and 2.2, 16384 rows 16.4 and 7.3).
   const int least = P.T <= IQ_FEW ? 128 : 32;
   if (least <= 32 && P.K <= 32 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 32, false>, 32);
   if (least <= 64 && P.K <= 64 * 8 * IQ_U) return go(i8_quantize_kernel<TY, VEC, SW, 64, false>, 64);

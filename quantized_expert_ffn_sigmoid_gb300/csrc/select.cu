@@ -17,6 +17,10 @@
 // lane each; only where more than 32 do (many equal ones) it goes round by round.
 // Groups of whole warps take two reductions each; others are scanned by one lane
 // each in shared memory.  All sums are fp32.
+//
+// Bound: instructions (about 920 a position of 256 experts with groups and a bias;
+// 16384 of them 15.8 us, issue slots 78 % busy, where their 17 MB would take 2.6;
+// softmax without groups 10.6 us; one position 2.7 us, from its hidden state 8.2).
 #include "mx4_common.cuh"
 
 namespace colimoe {
