@@ -18,30 +18,34 @@
 //
 // One persistent CTA an SM, 20 warps meeting at mbarriers, every wait bounded:
 //   warp 0       TMA of weight codes, slots of 128 rows x 128 codes;
-//   warps 1, 3   TMA of activations, slots of up to NT rows x BK codes;
-//   warp 2       MMA issuer, blocks of BK codes;
+//   warps 1, 3   TMA of activations, slots of up to NT rows x SUB codes;
+//   warp 2       MMA issuer, blocks of 256 codes;
 //   warps 4-11   converters, two sets of four (a warp for each lane quarter)
 //                that take the weight slots in turn;
 //   warps 12-19  epilogue: runs into integer registers, at the end the scales and y.
-// One barrier says that a block's operands are there, one that its products are
-// complete, which frees the activations' slot and the weights' columns alike.
-// Few tiles are split along K (splits_of), and join in the workspace.
+// One barrier says that a block's operands are there, one a slot that its products
+// are complete, which frees the activations and the weights' columns alike.
+// Tiles of 128 activation rows are taken by two CTAs (cta_group::2): 256 weight
+// rows, each CTA with 128 of them and half of the activations, the first issuing for
+// both.  Few tiles are split along K (splits_of), and join in the workspace.
 //
 // What bounds it (GB300; 6.79 TB/s copy, 1924 TFLOP/s bf16 measured; times of whole calls).
-//   16384 rows over 256 groups, 4096 x 6144   930-955 us, 6.9 TB/s: the weights' stream
-//   8192 rows, 4096 x 6144                    274 us, 1.5 PFLOP/s: of these 20 are
-//       i8_widen; the instructions' own time is 96 % of the others at the clock (1.45
-//       GHz) that the power limit leaves, 74 % at the full one
-//   4096 rows over 32 groups, 4096 x 6144     238 us: the operands' way from L2 (a block of
-//       128 codes x 128 rows is 48 KB for 512 cycles of instructions; 46-55 bytes a
-//       cycle arrive)
-//   16 rows, 4096 x 6144                      13 us: two launches, 12 slots a CTA
+//   16384 rows over 160 of 256 groups, 4096 x 6144   860 us, 4.7 TB/s of weights
+//   4096 rows over 32 groups, 4096 x 6144            218 us
+//       Both: the operands' way from L2 and the MMA warp's from block to block.
+//       One CTA for a tile moves 48 KB for 128 codes x 128 rows, which at the 64
+//       bytes a cycle of an SM's port take 768 cycles, the instructions 512: 935 and
+//       245 us.  Two CTAs move 32 KB each.
+//   8192 rows, 4096 x 6144                           280 us, 1.5 PFLOP/s: of these 20 are
+//       i8_widen; the others the instructions at the clock (1.45 GHz) that the power
+//       limit leaves
+//   16 rows, 4096 x 6144                             13 us: two launches, 12 slots a CTA
 // Steps that brought most: instructions issued by one lane inside a branch (21
 // cycles each, 57 behind a wait in a predicated warp); the next block's barrier
 // looked at before a block's last instructions; conversions by integer instructions
-// alone; copies of activations by two warps; for tiles of 128 rows four slots of
-// activations and five of weights (three and seven: 257 us for the 32 groups, not 238).
-// Blocks of half the codes cost a third (the same: 347).
+// alone; copies of activations by two warps; blocks of 256 codes (from one to the next the
+// MMA warp needs about 400 cycles beside its instructions' issue: with 64 codes that
+// was all a block's time); tiles of two CTAs.
 #include "i8_product.cuh"
 #include "tcgen05.cuh"
 #include "tensormap.cuh"
@@ -59,36 +63,40 @@ constexpr int IG_MB = 8;                     // weight tiles that share activati
 constexpr int IG_THREADS = 640;
 constexpr int IG_RCTL = 32, IG_RCONV = 64, IG_REPI = 160;
 constexpr int IG_MAX_SMEM = 227 * 1024;
-constexpr int IG_MAXW = 9, IG_MAXB = 5;
+constexpr int IG_MAXW = 9, IG_MAXB = 6;
 
-// NT: activation rows of a tile at most; BK: codes of a block, the unit in
-// which operands pass to the MMA warp.  Slots fill 208 KB, 224 for the widest
-// tiles, which leaves tables for IG_WIDE_G groups.
+// NT: activation rows of a tile at most; PAIR: two CTAs take a tile of 256 weight
+// rows together, each with 128 of them and half of the activations in its
+// shared memory; BK: codes of a block, the unit in which operands pass to the MMA
+// warp; SUB: codes of an activation slot, the unit in which space is freed.
+// Slots fill 208 KB.
 template <int NT>
 struct IgShape {
-  static constexpr int BK = NT == 256 ? 64 : NT == 128 ? 128 : 256;
-  static constexpr int NW = NT == 32 ? 9 : NT == 64 ? 7 : NT == 128 ? 5 : 4;
-  static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : NT == 128 ? 4 : 5;
-  static constexpr uint32_t BSLOT = NT * BK * 2;
+  static constexpr bool PAIR = NT == 128;
+  static constexpr int BK = 256, SUB = PAIR ? 128 : 256, SUBS = BK / SUB;
+  static constexpr int NW = NT == 32 ? 9 : 7;
+  static constexpr int NB = NT == 32 ? 4 : NT == 64 ? 3 : 6;
+  static constexpr int NF = PAIR ? 4 : NB;                     // barriers of blocks
+  static constexpr int BROWS = PAIR ? NT / 2 : NT;             // activation rows of a slot
+  static constexpr uint32_t BSLOT = BROWS * SUB * 2;
   static constexpr uint32_t BARS = NW * IG_WSLOT + NB * BSLOT;
   static constexpr uint32_t TABLES = BARS + 512;
   static constexpr int COLS = NT / 2;                          // columns of an epilogue warp
-  static constexpr int KSTEP = BK < IG_WK ? IG_WK : BK;        // K is filled up with zeros to a multiple of this
-  // tensor memory: accumulators, then AS blocks of widened weights
-  static constexpr int ACCS = NT == 256 ? 1 : 2, AW = BK / 2, AS = NT <= 64 ? 2 : NT == 128 ? 3 : 4;
-  static_assert(ACCS * NT <= 256 && AS * AW <= 256 && AS <= NB, "tensor memory");
+  // tensor memory: two accumulators, then widened weights for AS activation slots
+  static constexpr int AW = SUB / 2, AS = PAIR ? 4 : 2, OF = SUB / IG_WK;  // OF: weight slots to an activation slot
+  static_assert(2 * NT <= 256 && AS * AW <= 256 && AS <= NB && AS * SUB >= BK && NB * SUB >= BK && NB < 2 * NF, "tensor memory");
   // A set of converters looks at every other slot, by the parity of its use, so
   // it must not get to a slot before that slot's last use (the other set's, with
   // NW odd) has landed: copies land in any order.  It gets to slot g once the
-  // products of slot g - 2 - AS * BK / 128 are complete.
-  static_assert(NW >= AS * BK / IG_WK + 2, "a slot's parity must not be ambiguous");
+  // products of slot g - 2 - AS * SUB / 128 are complete.
+  static_assert(NW >= AS * OF + 2, "a slot's parity must not be ambiguous");
 };
 constexpr int IG_ACOL = 256;                 // first column of the widened weights
-constexpr int IG_WIDE_G = 128;
 template <int NT>
 constexpr size_t ig_smem(int G) { return IgShape<NT>::TABLES + 8 * (size_t)(G + 1) + 1024; }
 
-static_assert(ig_smem<256>(IG_WIDE_G) <= IG_MAX_SMEM && ig_smem<128>(COLI_I8_MAX_GROUPS) <= IG_MAX_SMEM, "shared memory");
+static_assert(ig_smem<32>(COLI_I8_MAX_GROUPS) <= IG_MAX_SMEM && ig_smem<64>(COLI_I8_MAX_GROUPS) <= IG_MAX_SMEM &&
+              ig_smem<128>(COLI_I8_MAX_GROUPS) <= IG_MAX_SMEM, "shared memory");
 
 struct IgMaps {
   CUtensorMap w;     // weight codes [G][N][K]
@@ -121,13 +129,44 @@ __device__ __forceinline__ void biased8(uint32_t w0, uint32_t w1, uint32_t* o) {
   o[2] = prmt(x1, 0u, 0x4140u);
   o[3] = prmt(x1, 0u, 0x4342u);
 }
-// D[tmem] (+)= A[tmem] x B[smem]
+// D[tmem] (+)= A[tmem] x B[smem]; PAIR: by both CTAs of a pair, each on its own
+// 128 rows of A and D, with its half of B
+template <bool PAIR>
 __device__ __forceinline__ void umma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// An arrival at `bar` once the products issued so far are complete; PAIR: at
+// that barrier of both CTAs
+template <bool PAIR>
+__device__ __forceinline__ void commit_to(uint64_t* bar) {
+  if (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+  else
+    umma_commit(bar);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// An arrival at the barrier of the pair's first CTA that stands where `bar` does
+// in this one.  What it announces is in tensor memory, or in shared memory by
+// asynchronous copies: no ordinary store has to be seen by the other CTA, and a
+// release to the whole cluster took 2000 cycles.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
 }
 
 struct IgItem {
@@ -138,17 +177,19 @@ template <int NT>
 __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__ IgMaps maps, const I8Params A, const uint32_t off_xs, const int wide,
                                                            const int n_splits, uint32_t* __restrict__ part) {
   using S = IgShape<NT>;
-  constexpr int NW = S::NW, NB = S::NB, BK = S::BK;
+  constexpr bool PAIR = S::PAIR;
+  constexpr int NW = S::NW, NB = S::NB, NF = S::NF, BK = S::BK, SUB = S::SUB, SUBS = S::SUBS;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<size_t>(sm_raw), 1024));
   uint8_t* sm_b = sm + NW * IG_WSLOT;
   uint64_t* full_w = reinterpret_cast<uint64_t*>(sm + S::BARS);  // [NW] weight codes landed
   uint64_t* empty_w = full_w + IG_MAXW;                          // [NW] the converters have read them
-  uint64_t* full = empty_w + IG_MAXW;                            // [NB] a block: activations landed, weights in tensor memory
-  uint64_t* done = full + IG_MAXB;                               // [NB] its products are complete
-  uint64_t* d_full = done + IG_MAXB;                             // [ACCS] a run is complete
-  uint64_t* d_empty = d_full + 2;                                // [ACCS] it has been read
-  uint64_t* fin = d_empty + 2;
+  uint64_t* full = empty_w + IG_MAXW;                            // [NF] a block: activations landed, weights in tensor memory
+  uint64_t* done = full + IG_MAXB;                               // [NB] an activation slot's products are complete
+  uint64_t* d_full = done + IG_MAXB;                             // [2] a run is complete
+  uint64_t* d_empty = d_full + 2;                                // [2] it has been read
+  uint64_t* full2 = d_empty + 2;                                 // [NF] PAIR, in the first CTA: the other one's operands are there
+  uint64_t* fin = full2 + IG_MAXB;
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_taddr + 1);
   uint32_t* s_level = s_taddr + 2;
@@ -159,24 +200,26 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   // (broadcast, so that the compiler knows them to be the same in every lane of a warp)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // With splits, this CTA takes one part of K of one tile (the grid holds all parts of all tiles)
-  const int splits = NT == 256 ? 1 : n_splits;
-  const int kall = (A.K + S::KSTEP - 1) / S::KSTEP, kpart = (kall + splits - 1) / splits;
+  const int splits = PAIR ? 1 : n_splits;
+  const int kall = (A.K + BK - 1) / BK, kpart = (kall + splits - 1) / splits;
   const int k0 = splits > 1 ? (int)blockIdx.x % splits * kpart : 0, ksteps = splits > 1 ? min(kpart, kall - k0) : kall;
-  const int nblk = ksteps * (S::KSTEP / BK), nw = ksteps * (S::KSTEP / IG_WK);
-  const int mt = (A.N + IG_M - 1) / IG_M;
+  const int nblk = ksteps, nw = nblk * (BK / IG_WK);
+  constexpr int MROWS = PAIR ? 2 * IG_M : IG_M;  // weight rows of an item
+  const int rank = PAIR ? (int)blockIdx.x & 1 : 0, mt = (A.N + MROWS - 1) / MROWS;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NW; ++i) {
       mbar_init(&full_w[i], 1);
       mbar_init(&empty_w[i], 4);
     }
-    for (int i = 0; i < NB; ++i) {
-      mbar_init(&full[i], 2 + 4 * (BK > IG_WK ? BK / IG_WK : 1));
-      mbar_init(&done[i], 1);
+    for (int i = 0; i < NF; ++i) {
+      mbar_init(&full[i], 2 * SUBS + 4 * (BK / IG_WK));
+      mbar_init(&full2[i], 1);
     }
-    for (int i = 0; i < S::ACCS; ++i) {
+    for (int i = 0; i < NB; ++i) mbar_init(&done[i], 1);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 8);
+      mbar_init(&d_empty[i], PAIR ? 16 : 8);
     }
     mbar_init(fin, 1);
     *s_abort = 0;
@@ -184,8 +227,13 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     fence_barrier_init();
   }
   if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)), "n"(512) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)), "n"(512) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)), "n"(512) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   pdl_wait();
   pdl_trigger();
@@ -227,14 +275,15 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   }
   tmem_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // (the other CTA's barriers are there)
   tmem_fence_after();
   const int run = *s_level < IG_LEVELS - 1 ? IG_RUN << *s_level : 1 << 30;
   // (runs end at multiples of their length from the row's beginning)
-  const int kbegin = k0 * S::KSTEP % run;
+  const int kbegin = k0 * BK % run;
   const uint32_t taddr = __shfl_sync(0xffffffffu, *s_taddr, 0);
   const int items = __shfl_sync(0xffffffffu, s_tiles[A.G] * mt, 0);
-  const int first = (int)blockIdx.x / splits;  // (splits > 1: the only item)
-  const int step = splits > 1 ? 1 << 30 : (int)gridDim.x;
+  const int first = (int)blockIdx.x / (PAIR ? 2 : splits);  // (splits > 1: the only item)
+  const int step = splits > 1 ? 1 << 30 : (int)gridDim.x / (PAIR ? 2 : 1);
 
   // Items of a group: IG_MB weight tiles for each activation tile, so that the
   // CTAs at work together share both operands in L2.
@@ -246,13 +295,14 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       if (s_tiles[mid] <= q) lo = mid; else hi = mid - 1;
     }
     const int t0 = s_tiles[lo], ntn = s_tiles[lo + 1] - t0, local = item - t0 * mt;
-    const int mb = local / (IG_MB * ntn), in = local - mb * IG_MB * ntn, width = min(IG_MB, mt - mb * IG_MB);
+    constexpr int MB = IG_MB / (PAIR ? 2 : 1);
+    const int mb = local / (MB * ntn), in = local - mb * MB * ntn, width = min(MB, mt - mb * MB);
     const int nt = in / width;
     IgItem it;
     it.g = lo;
     it.row0 = s_row0[lo] + nt * NT;
     it.ntok = min(NT, s_row0[lo + 1] - it.row0);
-    it.n0 = (mb * IG_MB + in - nt * width) * IG_M;
+    it.n0 = (mb * MB + in - nt * width) * MROWS + rank * IG_M;
     return it;
   };
 
@@ -271,8 +321,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           const uint32_t s = gs % NW;
           if (!gwait(&empty_w[s], ((gs / NW) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
           mbar_arrive_expect_tx(&full_w[s], IG_WSLOT);
-          if (once) tma_load_3d_hint(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, z, &full_w[s], stream);
-          else tma_load_3d(sm + s * IG_WSLOT, &maps.w, k0 * S::KSTEP + st * IG_WK, it.n0, z, &full_w[s]);
+          if (once) tma_load_3d_hint(sm + s * IG_WSLOT, &maps.w, k0 * BK + st * IG_WK, it.n0, z, &full_w[s], stream);
+          else tma_load_3d(sm + s * IG_WSLOT, &maps.w, k0 * BK + st * IG_WK, it.n0, z, &full_w[s]);
         }
       }
       // every copy issued has landed before the CTA can exit (after an abort a
@@ -282,38 +332,56 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         }
     } else if ((warp == 1 || warp == 3) && lane == 0) {
       // ------------------------------------------------ TMA of activations
-      // Each warp takes half of a slot (one thread issues a box of 16 KB every
-      // 380 cycles): every other 64 codes, or the tile's rows before or from 128 on.
+      // Each warp takes half of a slot, every other 64 codes (one thread issues a
+      // box of 16 KB every 380 cycles).
       fence_proxy_async_global();  // (the widened rows were written by ordinary stores of the kernel before)
       const int half = warp >> 1;
       uint32_t gs = 0;
       bool go = true;
       for (int item = first; item < items && go; item += step) {
         const IgItem it = item_at(item);
-        constexpr int HALF = NT / 32;  // sixteens of rows
-        const int all = (it.ntok + 15) / 16, first = BK == 64 && half ? HALF : 0, n16 = BK == 64 ? min(max(all - first, 0), HALF) : all;
-        for (int j = 0; j < nblk; ++j, ++gs) {
+        // PAIR: the tile's rows up to a multiple of 32, half of them in each CTA
+        const int n16 = PAIR ? (it.ntok + 31) / 32 : (it.ntok + 15) / 16, row0 = it.row0 + rank * 16 * n16;
+        for (int j = 0; j < nblk * SUBS; ++j, ++gs) {
           const uint32_t s = gs % NB;
+          uint64_t* bar = &full[gs / SUBS % NF];
           if (!gwait(&done[s], ((gs / NB) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
-          if (n16 == 0) {
-            mbar_arrive(&full[s]);
-            continue;
-          }
-          mbar_arrive_expect_tx(&full[s], (uint32_t)n16 * 2048 * (BK == 64 ? 1 : BK / 128));
-          int row = 16 * first;
+          mbar_arrive_expect_tx(bar, (uint32_t)n16 * 2048 * (SUB / 128));
+          int row = 0;
           for (int left = n16; left > 0;) {  // the rows in boxes of 128, 64, 32, 16
             const int i = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
 #pragma unroll
-            for (int c = BK == 64 ? 0 : half; c < BK / 64; c += 2)
-              tma_load_2d(sm_b + s * S::BSLOT + c * (NT * 128) + row * 128, &maps.x[i], k0 * S::KSTEP + j * BK + 64 * c, it.row0 + row, &full[s]);
+            for (int c = half; c < SUB / 64; c += 2)
+              tma_load_2d(sm_b + s * S::BSLOT + c * (S::BROWS * 128) + row * 128, &maps.x[i], k0 * BK + j * SUB + 64 * c, row0 + row, bar);
             row += 16 << i;
             left -= 1 << i;
           }
         }
       }
-      for (uint32_t k = gs > (uint32_t)NB ? gs - NB : 0; k < gs; ++k)
-        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full[k % NB], (k / NB) & 1u); ++i) {
+      // (the last copies are of the last blocks whose operands were asked for)
+      const uint32_t blocks = (gs + SUBS - 1) / SUBS;
+      for (uint32_t k = blocks > (uint32_t)NF ? blocks - NF : 0; k < blocks; ++k)
+        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full[k % NF], (k / NF) & 1u); ++i) {
         }
+    } else if (warp == 2 && PAIR && rank == 1) {
+      // ------------------- second CTA: tells the first that a block is there
+      uint32_t gs = 0;
+      bool go = true;
+      for (int item = first; item < items && go; item += step)
+        for (int j = 0; j < nblk; ++j, ++gs) {
+          if (!gwait(&full[gs % NF], (gs / NF) & 1u, status, s_abort)) { go = false; break; }
+          tmem_fence_after();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first(&full2[gs % NF]);
+        }
+      // the first CTA's last arrivals here
+      if (go) {
+        const uint32_t subs = gs * SUBS;
+        for (uint32_t k = subs > (uint32_t)NB ? subs - NB : 0; k < subs; ++k)
+          for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_test_wait(&done[k % NB], (k / NB) & 1u); ++i) {
+          }
+      }
     } else if (warp == 2) {
       // -------------------------------------------------------- MMA issuer
       // (one elected lane issues a block's instructions inside a branch: 21
@@ -322,46 +390,60 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       // waits at one barrier, looked at while the block before is under way)
       const uint32_t leader = elect_one();
       const uint64_t db0 = umma_desc_sw128(smem_u32(sm_b));
-      constexpr int TAIL = NT == 256 ? 1 : 2;
-      uint32_t s = 0, ph = 0, a = 0, d = 0, dph = 1;
+      constexpr int TAIL = 2;
+      uint32_t s = 0, f = 0, ph = 0, a = 0, d = 0, dph = 1;
       bool ready = false, ok = true;
       for (int item = first; item < items; item += step) {
-        const uint32_t idesc = umma_idesc((item_at(item).ntok + 15) & ~15);
+        const int ntok = item_at(item).ntok;
+        const uint32_t idesc = PAIR ? umma_idesc((ntok + 31) & ~31) + ((uint32_t)(IG_M >> 4) << 24) : umma_idesc((ntok + 15) & ~15);  // (PAIR: M = 256)
         uint32_t acc = 0;          // whether the run has begun
         int left = (run - kbegin) / BK;  // blocks to its end
         for (int j = nblk; j > 0; --j) {
           if (acc == 0) ok = gwait(&d_empty[d], dph, status, s_abort) && ok;
-          if (!ready) ok = gwait(&full[s], ph, status, s_abort) && ok;
+          if (!ready) {
+            ok = gwait(&full[f], ph, status, s_abort) && ok;
+            if (PAIR) ok = gwait(&full2[f], ph, status, s_abort) && ok;
+          }
           const bool end = --left == 0 || j == 1;
-          const uint32_t dc = taddr + d * NT, ac = taddr + IG_ACOL + a * S::AW, old = s;
-          const uint64_t db = db0 + s * (S::BSLOT >> 4);
+          const uint32_t dc = taddr + d * NT;
+          // instructions of the block's activation slots, and each slot's barrier behind its last
           auto issue = [&](int from, int to) {
 #pragma unroll
-            for (int k = from; k < to; ++k)
-              umma_f16(dc, ac + 8 * k, db + (k >> 2) * (NT * 128 / 16) + 2 * (k & 3), idesc, k ? 1u : acc);
+            for (int k = from; k < to; ++k) {
+              constexpr int EACH = SUB / 16;
+              const int sub = k / EACH, in = k % EACH;
+              const uint32_t at = s + sub < (uint32_t)NB ? s + sub : s + sub - NB, col = a + sub < (uint32_t)S::AS ? a + sub : a + sub - S::AS;
+              if (ok)  // (aborted: the results are flagged invalid; nothing is issued)
+                umma_f16<PAIR>(dc, taddr + IG_ACOL + col * S::AW + 8 * in, db0 + at * (S::BSLOT >> 4) + (in >> 2) * (S::BROWS * 128 / 16) + 2 * (in & 3), idesc,
+                         k ? 1u : acc);
+              if (in == EACH - 1) commit_to<PAIR>(&done[at]);
+            }
           };
           tmem_fence_after();
           __syncwarp();
-          if (leader && ok) issue(0, BK / 16 - TAIL);  // (aborted: the results are flagged invalid; nothing is issued)
+          if (leader) issue(0, BK / 16 - TAIL);
           // behind the last TAIL instructions, which are still under way then,
           // the next block follows without a gap
-          if (++s == (uint32_t)NB) {
-            s = 0;
+          if (++f == (uint32_t)NF) {
+            f = 0;
             ph ^= 1u;
           }
-          ready = mbar_test_wait(&full[s], ph);
+          ready = mbar_test_wait(&full[f], ph);
+          if (PAIR) ready = mbar_test_wait(&full2[f], ph) && ready;
           if (leader) {
-            if (ok) issue(BK / 16 - TAIL, BK / 16);
-            umma_commit(&done[old]);
-            if (end) umma_commit(&d_full[d]);
+            issue(BK / 16 - TAIL, BK / 16);
+            if (end) commit_to<PAIR>(&d_full[d]);
           }
           __syncwarp();
-          a = (a + 1) % S::AS;
+          s += SUBS;
+          if (s >= (uint32_t)NB) s -= NB;
+          a += SUBS;
+          if (a >= (uint32_t)S::AS) a -= S::AS;
           acc = 1;
           if (end) {
             acc = 0;
             left = run / BK;
-            if (++d == (uint32_t)S::ACCS) {
+            if (++d == 2u) {
               d = 0;
               dph ^= 1u;
             }
@@ -369,7 +451,10 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         }
       }
       // every MMA issued has completed before the accumulators are freed
-      if (leader) umma_commit(fin);
+      if (leader) {
+        if (PAIR) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(fin)) : "memory");
+        else umma_commit(fin);
+      }
       __syncwarp();
       for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(fin, 0u); ++i) {
       }
@@ -383,19 +468,18 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
     const uint32_t total = (uint32_t)(items > first ? (items - first - 1) / step + 1 : 0) * (uint32_t)nw;
     const uint32_t src = smem_u32(sm) + r * IG_WK, sw = (r & 7) * 16;  // 16-byte unit c of row r is at unit c ^ (r % 8)
     const uint32_t dst = taddr + ((uint32_t)(32 * q) << 16) + IG_ACOL;
-    constexpr int PER = BK < IG_WK ? IG_WK / BK : 1;  // blocks of a slot, or
-    constexpr int OF = BK > IG_WK ? BK / IG_WK : 1;   // slots of a block
+    constexpr int OF = S::OF;
     uint32_t s = set, sph = 0;
     for (uint32_t g = set; g < total; g += 2) {
       gwait(&full_w[s], sph, status, s_abort);
       uint4 w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = lds128(src + s * IG_WSLOT + ((16 * i) ^ sw));
-      // the block that held these columns is done (that phase cannot have been
-      // overtaken: the next block in its slot needs this one's weights first)
-      const uint32_t b = PER > 1 ? g * PER : g / OF;
-      if (b + PER > (uint32_t)S::AS) {
-        const uint32_t before = b + PER - 1 - S::AS;  // (done in order: the last of PER)
+      // what held these columns is done (that phase cannot have been overtaken:
+      // the next in its slot needs these weights first)
+      const uint32_t b = g / OF;
+      if (b >= (uint32_t)S::AS) {
+        const uint32_t before = b - S::AS;
         gwait(&done[before % NB], (before / NB) & 1u, status, s_abort);
       }
       tmem_fence_after();
@@ -408,15 +492,13 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         biased8(w[2 * h].z, w[2 * h].w, o + 4);
         biased8(w[2 * h + 1].x, w[2 * h + 1].y, o + 8);
         biased8(w[2 * h + 1].z, w[2 * h + 1].w, o + 12);
-        tmem_st16(at + 16 * h, o);  // (the blocks of a slot stand side by side)
+        tmem_st16(at + 16 * h, o);
       }
       if (lane == 0) mbar_arrive(&empty_w[s]);  // (every lane's loads are complete: its stores used them)
       tmem_wait_st();
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < PER; ++i) mbar_arrive(&full[(b + i) % NB]);
+      if (lane == 0) mbar_arrive(&full[g / (BK / IG_WK) % NF]);
       s += 2;
       if (s >= (uint32_t)NW) {
         s -= NW;
@@ -437,19 +519,16 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       const int n = it.n0 + 32 * q + lane;
       const bool live = n < A.N;
       const float sw = live ? __ldg(A.ws_ + it.g * A.wsgroup + n) : 0.f;
-      // scales and sums of the tile's rows, loaded ahead of the sums (not in the
-      // widest tiles, whose accumulators fill the registers): lane l has columns l, l + 32
-      constexpr bool AHEAD = COLS <= 64;
-      constexpr int HELD = AHEAD ? (COLS + 31) / 32 : 1;
+      // scales and sums of the tile's rows, loaded ahead of the sums: lane l has columns l, l + 32
+      constexpr int HELD = (COLS + 31) / 32;
       float sx_[HELD];
       uint32_t bias_[HELD];
-      if (AHEAD)
 #pragma unroll
-        for (int h = 0; h < HELD; ++h) {
-          const int c = 32 * h + lane;
-          sx_[h] = c < cols ? __ldcg(xs + it.row0 + col0 + c) : 0.f;
-          bias_[h] = c < cols ? __ldcg(xsum + it.row0 + col0 + c) : 0u;
-        }
+      for (int h = 0; h < HELD; ++h) {
+        const int c = 32 * h + lane;
+        sx_[h] = c < cols ? __ldcg(xs + it.row0 + col0 + c) : 0.f;
+        bias_[h] = c < cols ? __ldcg(xsum + it.row0 + col0 + c) : 0u;
+      }
       uint32_t acc[COLS];  // (modulo 2^32, in which the end result fits)
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0;
@@ -469,8 +548,11 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&d_empty[d]);
-        if (++d == (uint32_t)S::ACCS) {
+        if (lane == 0) {
+          if (PAIR && rank == 1) arrive_first(&d_empty[d]);
+          else mbar_arrive(&d_empty[d]);
+        }
+        if (++d == 2u) {
           d = 0;
           dph ^= 1u;
         }
@@ -506,17 +588,10 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
 #pragma unroll
         for (int c = 0; c < COLS; c += 16)
           if (c < cols) {
-            float sx = sx_[AHEAD ? c / 32 : 0];
-            uint32_t bias = bias_[AHEAD ? c / 32 : 0];
-            if (!AHEAD) {
-              const int p = it.row0 + col0 + c + (lane & 15);
-              sx = c + (lane & 15) < cols ? __ldcg(xs + p) : 0.f;
-              bias = c + (lane & 15) < cols ? __ldcg(xsum + p) : 0u;
-            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int from = AHEAD ? c % 32 + i : i;
-              const float v = i8_value((int)(acc[c + i] - __shfl_sync(0xffffffffu, bias, from)), __shfl_sync(0xffffffffu, sx, from), sw);
+              const int from = c % 32 + i;
+              const float v = i8_value((int)(acc[c + i] - __shfl_sync(0xffffffffu, bias_[c / 32], from)), __shfl_sync(0xffffffffu, sx_[c / 32], from), sw);
               if (live && c + i < cols) y[(c + i) * A.ldy] = from_f32<TY>(v);
             }
           }
@@ -528,8 +603,11 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
   }
   tmem_fence_before();
   __syncthreads();
-  if (warp == 2)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512) : "memory");
+  if (PAIR) cluster_sync();  // (neither CTA ends while the other may arrive at its barriers)
+  if (warp == 2) {
+    if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512) : "memory");
+  }
 }
 
 // sum + the magnitudes of four codes: with m = -1 in the bytes of negative
@@ -679,19 +757,39 @@ bool encode_rows_f16(CUtensorMap* m, const void* base, int kp, int rows, int box
 // fits in what a CTA is launched with (setmaxnreg.inc would otherwise wait for
 // registers that never come).
 template <int NT>
-cudaError_t check_kernel() {
+cudaError_t check_kernel(int* pairs) {
   static std::atomic<uint64_t> checked{0};
+  static std::atomic<int> fit[64];  // pairs of CTAs that run together
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (checked.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(i8_gemm<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, IG_MAX_SMEM);
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa{};
-  if ((e = cudaFuncGetAttributes(&fa, i8_gemm<NT>)) != cudaSuccess) return e;
-  const int need = 128 * IG_RCTL + 256 * IG_RCONV + 256 * IG_REPI;
-  if (fa.numRegs * IG_THREADS < need || fa.numRegs < IG_RCONV || fa.numRegs > IG_REPI || fa.maxThreadsPerBlock < IG_THREADS)
-    return cudaErrorInvalidConfiguration;
-  checked.fetch_or(1ull << dev, std::memory_order_release);
+  if (!(checked.load(std::memory_order_acquire) >> dev & 1)) {
+    const auto kernel = i8_gemm<NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, IG_MAX_SMEM);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa{};
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+    const int need = 128 * IG_RCTL + 256 * IG_RCONV + 256 * IG_REPI;
+    if (fa.numRegs * IG_THREADS < need || fa.numRegs < IG_RCONV || fa.numRegs > IG_REPI || fa.maxThreadsPerBlock < IG_THREADS)
+      return cudaErrorInvalidConfiguration;
+    if (IgShape<NT>::PAIR) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      cfg.gridDim = dim3(2);
+      cfg.blockDim = dim3(IG_THREADS);
+      cfg.dynamicSmemBytes = ig_smem<NT>(COLI_I8_MAX_GROUPS);
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      fit[dev].store(n, std::memory_order_relaxed);
+    }
+    checked.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  *pairs = fit[dev].load(std::memory_order_relaxed);
   return cudaSuccess;
 }
 
@@ -701,9 +799,10 @@ cudaError_t check_kernel() {
 // in two of them, 8.4 whole).  None is empty.
 template <int NT>
 int splits_of(const I8Params& A, long long items, int sms) {
-  const int kall = (A.K + IgShape<NT>::KSTEP - 1) / IgShape<NT>::KSTEP, ctas = sms < 2 * I8_SPLIT_TILES ? sms : 2 * I8_SPLIT_TILES;
-  if (NT > 128 || items < 1 || 2 * items > ctas) return 1;
-  const int most = kall / (512 / IgShape<NT>::KSTEP), n = (int)(ctas / items) < most ? (int)(ctas / items) : most;
+  constexpr int KSTEP = IgShape<NT>::BK;
+  const int kall = (A.K + KSTEP - 1) / KSTEP, ctas = sms < 2 * I8_SPLIT_TILES ? sms : 2 * I8_SPLIT_TILES;
+  if (IgShape<NT>::PAIR || items < 1 || 2 * items > ctas) return 1;
+  const int most = kall / (512 / KSTEP), n = (int)(ctas / items) < most ? (int)(ctas / items) : most;
   if (n <= 1) return 1;
   const int per = (kall + n - 1) / n;
   return (kall + per - 1) / per;
@@ -711,31 +810,32 @@ int splits_of(const I8Params& A, long long items, int sms) {
 
 // Cycles a call is expected to take with tiles of NT rows, fitted to measured
 // times: a code of a full tile's rows takes PER of them (2.4 for its 128 weights, the
-// rest falls with the rows), and a tile END where its epilogue is not hidden behind
-// the next tile's products (the widest), a call START + JOIN more where its sums
+// rest falls with the rows), a call START more with pairs, JOIN where its sums
 // are split.  (Groups: a tile and a half a group on average, at least one.)  Measured, tiles
-// of 64, 128, 256 rows, us: 8192 rows of 4096 x 6144 406, 356, 274; 512 rows of
-// 4096 x 4096 29, 25, 35; 128 rows of 4096 x 6144 21, 23, -; in 32 groups of 4096 x 6144
-// 4000 rows a group of 250 456, 368, 403, of 1000 1631, 1156, 1100; 16384 rows in 256 groups
-// 1091, 930, -.
+// of 64 and of 128 rows, us: 8192 rows of 4096 x 6144 406, 280; 512 rows of 4096 x
+// 4096 29, 26; 128 rows of 4096 x 6144 21, 23; in 32 groups of 4096 x 6144 10 rows a
+// group 113, 115, 96 rows 231, 188, 1000 rows 1631, 1077; 16384 rows in 256 groups 1091, 860.
 template <int NT>
 double cycles_of(const I8Params& A, int sms) {
-  constexpr double WEIGHTS = 2.4, PER = NT == 64 ? 4.4 : NT == 128 ? 6.9 : 8.8, END = NT == 256 ? 22000 : 0, START = NT == 128 ? 4700 : 0,
-                   JOIN = NT == 128 ? 10000 : 5700;
-  const int mt = (A.N + IG_M - 1) / IG_M;
+  constexpr bool PAIR = IgShape<NT>::PAIR;
+  constexpr double WEIGHTS = 2.4, PER = PAIR ? 5.3 : 4.4, START = PAIR ? 10000 : 0, JOIN = 5700;
+  constexpr int MROWS = (PAIR ? 2 : 1) * IG_M;
+  const int mt = (A.N + MROWS - 1) / MROWS, at_once = PAIR ? sms / 2 : sms;
   if (A.G == 1) {
     const long long items = (long long)((A.P + NT - 1) / NT) * mt;
     const int splits = splits_of<NT>(A, items, sms);
-    return START + (splits > 1 ? PER * A.K / splits + JOIN : (PER * A.K + END) * (double)((items + sms - 1) / sms));
+    return START + (splits > 1 ? PER * A.K / splits + JOIN : PER * A.K * (double)((items + at_once - 1) / at_once));
   }
   const int groups = A.G < A.P ? A.G : A.P;
-  const double each = (double)A.P / groups / NT + 0.5, tiles = groups * (each > 1.0 ? each : 1.0) * mt, share = tiles > sms ? 1.0 / sms : 1.0 / tiles;
-  return START + ((WEIGHTS * A.K + END) * tiles + (PER - WEIGHTS) / NT * A.K * (double)A.P * mt) * share;
+  const double each = (double)A.P / groups / NT + 0.5, tiles = groups * (each > 1.0 ? each : 1.0) * mt, share = 1.0 / (tiles > at_once ? at_once : tiles);
+  return START + (WEIGHTS * A.K * tiles + (PER - WEIGHTS) / NT * A.K * (double)A.P * mt) * share;
 }
 
 template <int NT>
 cudaError_t launch_nt(const I8Params& A, int sms, cudaStream_t st) {
-  cudaError_t e = check_kernel<NT>();
+  constexpr bool PAIR = IgShape<NT>::PAIR;
+  int pairs = 0;
+  cudaError_t e = check_kernel<NT>(&pairs);
   if (e != cudaSuccess) return e;
   const int kp = (int)i8_kp(A.K);
   float* xs = reinterpret_cast<float*>(A.ws + i8_off_xs());
@@ -745,11 +845,11 @@ cudaError_t launch_nt(const I8Params& A, int sms, cudaStream_t st) {
   for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
   if (!ok) return cudaErrorInvalidValue;
   // (at most: a partial tile per group that can have rows)
-  const long long items = (A.G == 1 ? (A.P + NT - 1) / NT : A.P / NT + (A.G < A.P ? A.G : A.P)) * (long long)((A.N + IG_M - 1) / IG_M);
+  const long long items = (A.G == 1 ? (A.P + NT - 1) / NT : A.P / NT + (A.G < A.P ? A.G : A.P)) * (long long)((A.N + (PAIR ? 2 : 1) * IG_M - 1) / ((PAIR ? 2 : 1) * IG_M));
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const int splits = splits_of<NT>(A, items, sms), zeros = splits > 1 ? (int)items * NT * IG_M / 4 : 0;
   // four warps a row where rows are long enough to fill them (8192 rows of 1536:
-  // the call takes 43.6 us with a warp a row, 48.0 with four; a warp sums 4 windows at most)
+  // the call took 43.6 us with a warp a row, 48.0 with four; a warp sums 4 windows at most)
   const bool four = A.K >= 2048;
   const int rows = WD_T / (four ? 128 : 32), most = 8 * sms < I8_WIDEN_CTAS ? 8 * sms : I8_WIDEN_CTAS;
   int wide = (A.P + rows - 1) / rows;
@@ -757,6 +857,22 @@ cudaError_t launch_nt(const I8Params& A, int sms, cudaStream_t st) {
   if (wide > most) wide = most;
   e = launch_pdl(four ? i8_widen<128> : i8_widen<32>, (unsigned)wide, WD_T, 0, st, A, kp, xs, reinterpret_cast<uint4*>(xb), reinterpret_cast<uint4*>(part), zeros);
   if (e != cudaSuccess) return e;
+  if (PAIR) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((unsigned)(2 * (items < pairs ? items : pairs)));
+    cfg.blockDim = dim3(IG_THREADS);
+    cfg.dynamicSmemBytes = ig_smem<NT>(A.G);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, i8_gemm<NT>, maps, A, (uint32_t)i8_off_xs(), wide, 1, reinterpret_cast<uint32_t*>(part));
+  }
   const long long grid = splits > 1 ? items * splits : items < sms ? items : sms;
   return launch_pdl(i8_gemm<NT>, (unsigned)grid, IG_THREADS, ig_smem<NT>(A.G), st, maps, A, (uint32_t)i8_off_xs(), wide, splits, reinterpret_cast<uint32_t*>(part));
 }
@@ -767,9 +883,7 @@ cudaError_t launch_i8_gemm(const I8Params& A, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   if (A.P <= 32) return launch_nt<32>(A, sms, st);
-  const double c64 = cycles_of<64>(A, sms), c128 = cycles_of<128>(A, sms), c256 = cycles_of<256>(A, sms);
-  if (A.P <= 64 || (c64 < c128 && c64 < c256)) return launch_nt<64>(A, sms, st);
-  return c128 <= c256 || A.G > IG_WIDE_G ? launch_nt<128>(A, sms, st) : launch_nt<256>(A, sms, st);
+  return A.P <= 64 || cycles_of<64>(A, sms) <= cycles_of<128>(A, sms) ? launch_nt<64>(A, sms, st) : launch_nt<128>(A, sms, st);
 }
 
 }  // namespace colimoe

@@ -383,3 +383,55 @@ def test_rows_beyond_32_bit_offsets():
     cm.coli_i8_product(x, xs, w[0], ws[0], y, space)
     ref, _ = want(x[some], xs[some], w, ws, [0, 5], torch.arange(5, device="cuda"), torch.bfloat16)
     assert torch.equal(y[some], ref)
+
+
+# calls whose tiles two CTAs take together: more rows than 64 and enough tiles
+PAIRS = [(333, 1, 6100, 6144), (5000, 1, 2100, 3001), (2000, 40, 2100, 3001), (700, 3, 2500, 6144), (9000, 150, 4200, 1500)]
+
+
+@pytest.mark.parametrize("P,G,N,K", PAIRS)
+def test_tiles_of_two_ctas(P, G, N, K):
+    gen = torch.Generator(device="cuda").manual_seed(P + G)
+    cuts = None if G == 1 else [0] + sorted(torch.randint(0, P + 1, (G - 1,), generator=gen, device="cuda").tolist()) + [P]
+    check(P, G, N, K, "bf16", seed=P + N, offsets=cuts, gather=G > 1, X=P // 2 + 7 if G > 1 else None)   # runs of 512 codes
+    check(P, G, N, K, "f32", seed=P + N, offsets=cuts, extreme=True, ldy=N + 3)
+
+
+@pytest.mark.parametrize("P,G,N,K", PAIRS)
+def test_tiles_of_two_ctas_in_many_calls(P, G, N, K):
+    x, xs, w, ws = make(P, G, N, K, P)
+    x.copy_((x.float() * 0.1).round().to(torch.int8))      # one run over all of K
+    gen = torch.Generator(device="cuda").manual_seed(P)
+    off = [0] + sorted(torch.randint(0, P + 1, (G - 1,), generator=gen, device="cuda").tolist()) + [P]
+    offsets, space = torch.tensor(off, dtype=torch.int32, device="cuda"), cm.new_i8_product_workspace(P, K)
+    ref, _ = want(x, xs, w, ws, off, torch.arange(P, device="cuda"), torch.float16)
+    y, few = torch.zeros(P, N, dtype=torch.float16, device="cuda"), torch.zeros(40, N, dtype=torch.float16, device="cuda")
+    for _ in range(60):
+        cm.coli_i8_product(x, xs, w, ws, y, space, offsets=offsets)
+        cm.coli_i8_product(x, xs, w[0], ws[0], few, space, rows=torch.arange(40, dtype=torch.int32, device="cuda"))   # another kernel between
+    assert cm.coli_moe_status(space) == 0 and torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("P,G,N,K", [(333, 1, 6100, 6144), (2000, 40, 2100, 3001)])
+def test_tiles_of_two_ctas_on_two_streams_and_in_a_graph(P, G, N, K):
+    x, xs, w, ws = make(P, G, N, K, P)
+    off = torch.linspace(0, P, G + 1, device="cuda").to(torch.int32)
+    ref, _ = want(x, xs, w, ws, off.tolist(), torch.arange(P, device="cuda"), torch.float32)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [cm.new_i8_product_workspace(P, K) for _ in range(2)]
+    ys = [torch.zeros(P, N, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, space, y in zip(streams, spaces, ys):
+            with torch.cuda.stream(st):
+                cm.coli_i8_product(x, xs, w, ws, y, space, offsets=off)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref) for y in ys)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cm.coli_i8_product(x, xs, w, ws, ys[0], spaces[0], offsets=off)
+    ys[0].zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], ref) and all(cm.coli_moe_status(space) == 0 for space in spaces)
