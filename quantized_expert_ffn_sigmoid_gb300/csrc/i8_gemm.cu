@@ -100,7 +100,7 @@ static_assert(ig_smem<32>(COLI_I8_MAX_GROUPS) <= IG_MAX_SMEM && ig_smem<64>(COLI
 
 struct IgMaps {
   CUtensorMap w;     // weight codes [G][N][K]
-  CUtensorMap x[4];  // widened activations, boxes of 64 codes x 16, 32, 64, 128 rows
+  CUtensorMap x[3];  // widened activations, boxes of 64 codes x 16, 32, 64 rows
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         }
     } else if ((warp == 1 || warp == 3) && lane == 0) {
       // ------------------------------------------------ TMA of activations
-      // Each warp takes half of a slot, every other 64 codes (one thread issues a
-      // box of 16 KB every 380 cycles).
+      // Each warp takes half of a slot, every other 64 codes (one thread issues
+      // 16 KB every 380 cycles).
       fence_proxy_async_global();  // (the widened rows were written by ordinary stores of the kernel before)
       const int half = warp >> 1;
       uint32_t gs = 0;
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           if (!gwait(&done[s], ((gs / NB) & 1u) ^ 1u, status, s_abort)) { go = false; break; }
           mbar_arrive_expect_tx(bar, (uint32_t)n16 * 2048 * (SUB / 128));
           int row = 0;
-          for (int left = n16; left > 0;) {  // the rows in boxes of 128, 64, 32, 16
-            const int i = left >= 8 ? 3 : left >= 4 ? 2 : left >= 2 ? 1 : 0;
+          for (int left = n16; left > 0;) {  // the rows in boxes of 64, 32, 16
+            const int i = left >= 4 ? 2 : left >= 2 ? 1 : 0;
 #pragma unroll
             for (int c = half; c < SUB / 64; c += 2)
               tma_load_2d(sm_b + s * S::BSLOT + c * (S::BROWS * 128) + row * 128, &maps.x[i], k0 * BK + j * SUB + 64 * c, row0 + row, bar);
@@ -842,7 +842,7 @@ cudaError_t launch_nt(const I8Params& A, int sms, cudaStream_t st) {
   uint8_t *xb = A.ws + i8_off_xb(A.P), *part = A.ws + i8_off_part(A.P, A.K);
   IgMaps maps;
   bool ok = encode_weights(&maps.w, A);
-  for (int i = 0; ok && i < 4; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
+  for (int i = 0; ok && i < 3; ++i) ok = encode_rows_f16(&maps.x[i], xb, kp, A.P, 16 << i);
   if (!ok) return cudaErrorInvalidValue;
   // (at most: a partial tile per group that can have rows)
   const long long items = (A.G == 1 ? (A.P + NT - 1) / NT : A.P / NT + (A.G < A.P ? A.G : A.P)) * (long long)((A.N + (PAIR ? 2 : 1) * IG_M - 1) / ((PAIR ? 2 : 1) * IG_M));

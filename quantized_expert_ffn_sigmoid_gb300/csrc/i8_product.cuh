@@ -39,7 +39,7 @@ inline size_t i8_off_xb(int P) { return align_up(i8_off_xs() + 8 * (size_t)P, 25
 inline size_t i8_off_part(int P, int K) { return align_up(i8_off_xb(P) + 2 * (size_t)P * (size_t)i8_kp(K), 256); }
 // then split sums: tiles of 128 weight rows
 constexpr int I8_SPLIT_TILES = 80;
-inline size_t i8_ws_bytes(int P, int K) { return i8_off_part(P, K) + (size_t)I8_SPLIT_TILES * (P <= 32 ? 32 : P <= 64 ? 64 : 128) * 512; }
+inline size_t i8_ws_bytes(int P, int K) { return i8_off_part(P, K) + (size_t)I8_SPLIT_TILES * (P <= 32 ? 32 : 64) * 512; }
 
 // First row of group g: offsets clamped to [0, P]; ascending by running maximum
 __device__ __forceinline__ int i8_offset(const I8Params& A, int g) { return A.offsets ? min(max(__ldcg(A.offsets + g), 0), A.P) : g * A.P; }
