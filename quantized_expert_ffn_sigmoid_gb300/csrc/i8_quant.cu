@@ -7,15 +7,17 @@
 // infinity or NaN gets scale NaN and codes 0, so that its products are NaN.
 // The quotient is taken in fp32; where it lies so near the middle of two codes
 // that its rounding may decide, the sign of v * 127 - middle * A does: codes are
-// those of exact arithmetic.  (With SwiGLU the values themselves are fp32 results.)
+// those of exact arithmetic.  (With SwiGLU those of the fp32 results silu(g) u,
+// which are within 2^-21 of the 64-bit ones.)
 //
 // One pass: a row's values stay in registers between its maximum and its
 // codes (up to 8192 values, 32 a thread; longer rows are read twice).  Bound:
 // HBM, 2 or 4 bytes in and one out a value, and close to it the instructions:
 // two values an fp32 instruction and, of 16-bit values, two magnitudes a
 // comparison.  8192 x 6144 bf16 24.5 us (6.2 TB/s of 6.79 copied; one value an
-// instruction 34), fp32 8192 x 4096 26 us (6.5), SwiGLU of 16384 x 2048 bf16 30.6 us
-// (5.5: exponentials); back to bf16, 8192 x 6144, 24 us (6.3).
+// instruction 34), fp32 8192 x 4096 26 us (6.5), SwiGLU of 16384 x 2048 bf16 33.9 us
+// (5.0: exponentials, and 31.0 without the look at middles, with codes one off
+// next to some); back to bf16, 8192 x 6144, 24 us (6.3).
 #include "mx4_common.cuh"
 
 namespace colimoe {
@@ -82,15 +84,14 @@ __device__ __forceinline__ void unit_values(const Raw8<TY>& a, const Raw8<TY>& b
 constexpr float IQ_MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole numbers, ties to even, into the low bits
 
 // How a quotient's rounding to fp32 is kept from turning a code
-//   NONE    not at all: the values are fp32 results themselves (SwiGLU)
 //   SNAP    16-bit values: with A = b 2^j and v = a 2^i, a and b whole numbers of
 //           at most 11 bits, the quotient 127 a / (b 2^(j-i)) is the middle of two codes or at
 //           least 1 / (254 a) > 2^-19 of itself away from it, and v * inv is at
 //           most 2^-24 from the exact one.  c - (c - v * inv) with c = 9 v * inv
 //           is that rounded to a multiple of 8 of its units: the middle where the
 //           exact quotient is one, and else on its side
-//   DECIDE  fp32 values: near a middle the exact sign decides
-enum { NONE, SNAP, DECIDE };
+//   DECIDE  fp32 values, also those of SwiGLU: near a middle the exact sign decides
+enum { SNAP, DECIDE };
 
 // 8 codes in two words
 template <int MODE>
@@ -101,9 +102,7 @@ __device__ __forceinline__ uint2 codes8(const float* v, float inv, float amax) {
   for (int i = 0; i < 8; i += 2) {
     const float2 x = make_float2(v[i], v[i + 1]);
     float2 q;
-    if (MODE == NONE) {
-      q = fma2(x, both(inv), both(IQ_MAGIC));
-    } else if (MODE == SNAP) {
+    if (MODE == SNAP) {
       const float2 c = mul2(x, both(9.f * inv)), d = fma2(x, both(-inv), c);
       q = add2(fma2(d, both(-1.f), c), both(IQ_MAGIC));
     } else {
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ?
       if (u < units && k < K) {
         float v[8];
         x[u].values(v);
-        store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW ? NONE : sizeof(TY) == 2 ? SNAP : DECIDE>(v, inv, amax) : make_uint2(0, 0));
+        store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW || sizeof(TY) == 4 ? DECIDE : SNAP>(v, inv, amax) : make_uint2(0, 0));
       }
     }
   } else {
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(IQ_T, sizeof(TY) == 2 && VEC && !SW && !LONG ?
     for (int k = in * 8; k < K; k += ROW * 8) {
       float v[8];
       unit_values<TY, SW>(load_unit<TY, VEC>(src + k, K - k), load_unit<TY, VEC>(src + (SW ? K : 0) + k, SW ? K - k : 0), v);
-      store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW ? NONE : sizeof(TY) == 2 ? SNAP : DECIDE>(v, inv, amax) : make_uint2(0, 0));
+      store_codes<VEC>(dst + k, K - k, inv > 0.f ? codes8<SW || sizeof(TY) == 4 ? DECIDE : SNAP>(v, inv, amax) : make_uint2(0, 0));
     }
   }
 }
