@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
           }
         __threadfence();
         named_bar(2, 256);
-        if (warp == 12 && lane == 0) *s_parts = atomicAdd(reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES) + item, 1u);
+        if (warp == 12 && lane == 0) *s_parts = atomicAdd(reinterpret_cast<uint32_t*>(A.ws + I8_OFF_PARTS) + item, 1u);
         named_bar(2, 256);
         if (*s_parts != (uint32_t)splits - 1) break;
         __threadfence();
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(WD_T) i8_widen(const I8Params A, int kp, float
   pdl_wait();
   pdl_trigger();
   // split sums: the parts of a tile that are done, and their sums
-  if (blockIdx.x == 0 && threadIdx.x < I8_SPLIT_TILES) reinterpret_cast<uint32_t*>(A.ws + WS_STATUS_BYTES)[threadIdx.x] = 0u;
+  if (blockIdx.x == 0 && threadIdx.x < I8_SPLIT_TILES) reinterpret_cast<uint32_t*>(A.ws + I8_OFF_PARTS)[threadIdx.x] = 0u;
   for (int i = blockIdx.x * WD_T + threadIdx.x; i < zeros; i += gridDim.x * WD_T) zero[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) {
     s_lo = A.offsets ? i8_offset(A, 0) : 0;

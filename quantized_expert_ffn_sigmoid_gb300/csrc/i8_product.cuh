@@ -29,16 +29,18 @@ struct I8Params {
 constexpr int I8_FEW = 8;
 inline bool i8_few(int P, int G) { return P <= (G > 1 ? I8_FEW : 4); }
 
-// Workspace behind the header: a word for each CTA that widens activations,
+// Workspace behind the header, whose words but the status are other operators': a
+// word for each CTA that widens activations, a count for each tile of split sums,
 // the scales of the rows of y, 128 times the sums of their codes, fp16 copies of
 // their activation rows padded to kp codes.
 constexpr int I8_WIDEN_CTAS = 1280;
+constexpr int I8_SPLIT_TILES = 80;
+constexpr size_t I8_OFF_PARTS = WS_HEADER_BYTES + 4 * I8_WIDEN_CTAS;
 inline long long i8_kp(int K) { return ((long long)K + 63) / 64 * 64; }
-inline size_t i8_off_xs() { return WS_HEADER_BYTES + 4 * I8_WIDEN_CTAS; }
+inline size_t i8_off_xs() { return I8_OFF_PARTS + 4 * I8_SPLIT_TILES; }
 inline size_t i8_off_xb(int P) { return align_up(i8_off_xs() + 8 * (size_t)P, 256); }
 inline size_t i8_off_part(int P, int K) { return align_up(i8_off_xb(P) + 2 * (size_t)P * (size_t)i8_kp(K), 256); }
 // then split sums: tiles of 128 weight rows
-constexpr int I8_SPLIT_TILES = 80;
 inline size_t i8_ws_bytes(int P, int K) { return i8_off_part(P, K) + (size_t)I8_SPLIT_TILES * (P <= 32 ? 32 : 64) * 512; }
 
 // First row of group g: offsets clamped to [0, P]; ascending by running maximum
