@@ -449,8 +449,10 @@ int coli_moe_block_norm(const coli_moe_norm_args* args, int32_t T, int32_t H, cu
  *     their best (ties to the lower group)
  *     topk_idx = the top_k best v of them, descending (ties to the lower id)
  *     topk_w = s of these, with renorm divided by their sum, times scaling
- * Without a bias the logits themselves rank the experts, also where scores
- * underflow to the same value.
+ * Without a bias the logits themselves rank the experts and the groups, also
+ * where scores saturate or underflow to the same fp32 value (a group by its two
+ * best logits; sums of two scores that differ by less than fp32 tells apart,
+ * from each other and in their distance from 0, 1 and 2, count as equal).
  *   x          logits [T] rows of n_experts values of `type` (COLI_F32, _BF16,
  *              _F16) with row stride ldx; or, with router_w, the hidden state
  *              [T][hidden] fp32 (ldx == hidden, hidden % 16 == 0), whose logits

@@ -8,7 +8,10 @@
 //     the top_k best v of these, ties to the lower id;  w = s_sel [/ sum s_sel] * scaling
 // An expert whose logit or bias is -inf takes no part.  Without a bias the
 // logits rank the experts: scores are monotone in them, and where scores
-// underflow or saturate to one value the logits still tell them apart.
+// underflow or saturate to one value the logits still tell them apart.  They
+// rank the groups by the groups' two best logits: by the best, or by the sum of
+// their scores, of which sums that are equal in fp32 are told apart by
+// sum_rest, their distance from 0, 1 or 2.
 //
 // One warp a position, E / 32 experts a lane (expert lane + 32 i) in registers.
 // Scores become integers of the same order (0: takes no part), so that maxima are
@@ -19,8 +22,9 @@
 // each in shared memory.  All sums are fp32.
 //
 // Bound: instructions (about 920 a position of 256 experts with groups and a bias;
-// 16384 of them 15.8 us, issue slots 78 % busy, where their 17 MB would take 2.6;
-// softmax without groups 10.6 us; one position 2.7 us, from its hidden state 8.2).
+// 16384 of them 14.6 us, issue slots 78 % busy, where their 17 MB would take 2.6;
+// groups without a bias 16.9 us, softmax without groups 9.9 us; one position 2.7 us,
+// from its hidden state 8.2).
 #include "mx4_common.cuh"
 
 namespace colimoe {
@@ -48,8 +52,30 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// V: experts a lane; PART: x holds partial sums of the router product
-template <int V, typename TY, bool PART>
+// What tells sums of two scores apart that fp32 does not, as a + b unevaluated
+// (logits l1 >= l2, without a bias; `sum` is the sum in fp32, f2 the score of l2):
+//   softmax, and sigmoids near 0     log(e^l1 + e^l2) = l1 + log(1 + e^(l2 - l1))
+//   one sigmoid near 1               s1 + s2 - 1 = s2 - sigmoid(-l1)
+//   both                             -log(2 - s1 - s2) -> l2 - log(1 + e^(l2 - l1))
+// Equal logits give equal values, so that the lower group comes first.
+__device__ __forceinline__ float2 sum_rest(float l1, float l2, float f2, float sum, int softmax) {
+  float a, b;
+  if (softmax || sum < 0.5f || sum >= 1.5f) {
+    const float t = log1pf(expf(l2 - l1));
+    a = softmax || sum < 0.5f ? l1 : l2;
+    b = softmax || sum < 0.5f ? t : -t;
+  } else {
+    a = f2;
+    b = -__fdividef(1.f, 1.f + expf(l1));
+  }
+  const float hi = a + b, c = hi - a;
+  return make_float2(hi, (a - (hi - c)) + (b - c));
+}
+
+// V: experts a lane; PART: x holds partial sums of the router product; LOGIT: no
+// bias, the logits rank (kernels of their own: with both in one, 16384 positions
+// of 256 experts with groups and a bias took 16.4 us instead of 14.6)
+template <int V, typename TY, bool PART, bool LOGIT>
 __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const SelectParams P) {
   extern __shared__ float sm_sel[];  // [warps][E] scores, where groups are not whole warps
   __shared__ __align__(16) uint32_t s_keys[4][32];  // candidates: keys, ids and scores
@@ -66,7 +92,7 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 32 * i;
-    b[i] = P.bias && e < E ? __ldg(P.bias + e) : 0.f;
+    b[i] = !LOGIT && e < E ? __ldg(P.bias + e) : 0.f;
     bias_bad |= !(b[i] < INFINITY);
     bias_odd |= !(fabsf(b[i]) < INFINITY);
   }
@@ -111,12 +137,13 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
     }
     // Where the logits alone rank the experts, scores are needed of the selected
     // only (softmax: also for its sum, which renormalised weights do without).
-    const bool late = !P.bias && P.keep == P.G && (!P.softmax || P.renorm);
+    const bool late = LOGIT && P.keep == P.G && (!P.softmax || P.renorm);
+    float m = NONE, inv = 0.f;  // of a softmax: largest logit, 1 / sum
     if (late) {
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] = l[i];
     } else if (P.softmax) {
-      float m = NONE, sum = 0.f;
+      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
       m = warp_max(m);
@@ -127,7 +154,7 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
         sum += s[i];
       }
       sum = warp_sum(sum);
-      const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+      inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] *= inv;
     } else {
@@ -135,17 +162,20 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
       for (int i = 0; i < V; ++i) s[i] = __fdividef(1.f, 1.f + expf(-l[i]));  // (0 from where the exponential overflows)
     }
     uint32_t key[V];
-    const bool by_logit = !P.bias;
+    auto make_keys = [&]() {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = order_key(LOGIT ? l[i] : s[i] + b[i]);
+      if (some_none)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
+    };
     if (P.keep < P.G) {
-      float group = NONE;  // lane g: score of group g
+      float group = NONE, second = NONE;  // lane g: score of group g; without a bias its best logits, for sums two
+      const bool sums = LOGIT && P.top2, add = !LOGIT && P.top2;
       const bool whole = P.per % 32 == 0;
       if (whole) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = order_key(s[i] + b[i]);
-        if (some_none)
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
+        make_keys();
         if (P.G == V && P.per == 32) {
           // a group a register: at each exchange a lane keeps half of the groups
           // and takes its neighbour's share of them, then all lanes of one group join
@@ -172,11 +202,12 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
             a2[0] = max(min(a1[0], r1), max(a2[0], r2));
             a1[0] = max(a1[0], r1);
           }
-          const float score = a1[0] == 0u ? NONE : key_value(a1[0]) + (P.top2 && a2[0] ? key_value(a2[0]) : 0.f);
           // lane g looks at a lane that holds group g (its bits in the other order)
           const int from = V > 1 ? (int)(__brev((uint32_t)lane) >> (32 - (31 - __clz(V)))) : 0;
+          const float score = a1[0] == 0u ? NONE : key_value(a1[0]) + (add && a2[0] ? key_value(a2[0]) : 0.f);
           group = __shfl_sync(0xffffffffu, score, from & 31);
           if (lane >= P.G) group = NONE;
+          if (sums) second = __shfl_sync(0xffffffffu, a2[0] ? key_value(a2[0]) : NONE, from & 31);
         } else {
           const int span = P.per / 32;
           uint32_t a1 = 0, a2 = 0;  // the group's two best
@@ -192,7 +223,10 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
             a2 = max(max(a2, m2), min(a1, m1));
             a1 = max(a1, m1);
             if (++in == span) {
-              if (lane == g) group = a1 == 0 ? NONE : key_value(a1) + (P.top2 && a2 ? key_value(a2) : 0.f);
+              if (lane == g) {
+                group = a1 == 0 ? NONE : key_value(a1) + (add && a2 ? key_value(a2) : 0.f);
+                second = a2 ? key_value(a2) : NONE;
+              }
               a1 = a2 = 0;
               in = 0;
               ++g;
@@ -203,33 +237,45 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
         float* row = sm_sel + warp * E;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (lane + 32 * i < E) row[lane + 32 * i] = l[i] == NONE ? NONE : s[i] + b[i];
+          if (lane + 32 * i < E) row[lane + 32 * i] = LOGIT || l[i] == NONE ? l[i] : s[i] + b[i];
         __syncwarp();
         if (lane < P.G) {
-          float a1 = NONE, a2 = NONE;
           for (int j = 0; j < P.per; ++j) {
             const float v = row[lane * P.per + j];
-            a2 = fmaxf(a2, fminf(a1, v));
-            a1 = fmaxf(a1, v);
+            second = fmaxf(second, fminf(group, v));
+            group = fmaxf(group, v);
           }
-          group = a1 + (P.top2 && a2 != NONE ? a2 : 0.f);
+          group += add && second != NONE ? second : 0.f;
         }
         __syncwarp();
       }
-      const uint32_t mk = lane < P.G && group != NONE ? order_key(group) : 0u;
+      const float first = group;
+      float f2 = 0.f;
+      if (sums && first != NONE) {
+        auto f = [&](float v) { return P.softmax ? expf(v - m) * inv : __fdividef(1.f, 1.f + expf(-v)); };
+        f2 = second == NONE ? 0.f : f(second);
+        group = f(first) + f2;
+        if (group < 0x1p-100f) group = 0.f;  // (subnormal numbers lose bits: sum_rest has them)
+      }
+      const uint32_t mk = group == NONE ? 0u : order_key(group);
       int before = 0;
       for (int g = 0; g < P.G; ++g) {
         const uint32_t other = __shfl_sync(0xffffffffu, mk, g);
         before += other > mk || (other == mk && g < lane);
       }
+      // (sums have the upper bit of their keys set: no lane's number is one)
+      if (sums && __any_sync(0xffffffffu, __popc(__match_any_sync(0xffffffffu, mk ? mk : (uint32_t)lane)) > 1)) {
+        const float2 r = mk ? sum_rest(first, second, f2, group, P.softmax) : make_float2(0.f, 0.f);
+        before = 0;
+        for (int g = 0; g < P.G; ++g) {
+          const uint32_t other = __shfl_sync(0xffffffffu, mk, g);
+          const float hi = __shfl_sync(0xffffffffu, r.x, g), lo = __shfl_sync(0xffffffffu, r.y, g);
+          const bool equal = other == mk && hi == r.x;
+          before += other > mk || (other == mk && hi > r.x) || (equal && lo > r.y) || (equal && lo == r.y && g < lane);
+        }
+      }
       const uint32_t kept = __ballot_sync(0xffffffffu, lane < P.G && before < P.keep);
-      if (by_logit || !whole)
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = order_key(by_logit ? l[i] : s[i] + b[i]);
-      if (some_none)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
+      if (!whole) make_keys();
       if (whole) {
         int g = 0, in = 0;
 #pragma unroll
@@ -248,12 +294,7 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
         }
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = order_key(by_logit ? l[i] : s[i] + b[i]);
-      if (some_none)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (l[i] == NONE || b[i] == NONE) key[i] = 0u;
+      make_keys();
     }
     // The k-th of the lanes' best (or one further down, where some are equal)
     // bounds the k-th best of all from below.  What reaches it goes to shared memory.
@@ -353,7 +394,7 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : 1) select_kernel(const Selec
   }
 }
 
-template <typename TY, bool PART>
+template <typename TY, bool PART, bool LOGIT>
 cudaError_t launch_select_t(const SelectParams& P, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -362,12 +403,16 @@ cudaError_t launch_select_t(const SelectParams& P, cudaStream_t st) {
   if (grid > 16LL * sms) grid = 16LL * sms;
   const size_t smem = P.keep < P.G && P.per % 32 ? (size_t)warps * P.E * 4 : 0;
   auto go = [&](auto kernel) { return launch_pdl(kernel, (unsigned)grid, 32u * warps, smem, st, P); };
-  if (P.E <= 32) return go(select_kernel<1, TY, PART>);
-  if (P.E <= 64) return go(select_kernel<2, TY, PART>);
-  if (P.E <= 128) return go(select_kernel<4, TY, PART>);
-  if (P.E <= 256) return go(select_kernel<8, TY, PART>);
-  if (P.E <= 512) return go(select_kernel<16, TY, PART>);
-  return go(select_kernel<32, TY, PART>);
+  if (P.E <= 32) return go(select_kernel<1, TY, PART, LOGIT>);
+  if (P.E <= 64) return go(select_kernel<2, TY, PART, LOGIT>);
+  if (P.E <= 128) return go(select_kernel<4, TY, PART, LOGIT>);
+  if (P.E <= 256) return go(select_kernel<8, TY, PART, LOGIT>);
+  if (P.E <= 512) return go(select_kernel<16, TY, PART, LOGIT>);
+  return go(select_kernel<32, TY, PART, LOGIT>);
+}
+template <typename TY, bool PART>
+cudaError_t launch_select(const SelectParams& P, cudaStream_t st) {
+  return P.bias ? launch_select_t<TY, PART, false>(P, st) : launch_select_t<TY, PART, true>(P, st);
 }
 
 int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }
@@ -444,9 +489,9 @@ extern "C" int coli_moe_select(const coli_moe_select_args* a, int32_t T, cudaStr
     const cudaError_t e = launch_route_partials(static_cast<const float*>(a->x), T, a->hidden, a->router_w, a->n_experts, part, P.status, &P.splits, stream);
     if (e != cudaSuccess) return COLI_ECUDA;
     P.x = part;
-    return rc_of(launch_select_t<float, true>(P, stream));
+    return rc_of(launch_select<float, true>(P, stream));
   }
-  if (a->type == COLI_F32) return rc_of(launch_select_t<float, false>(P, stream));
-  if (a->type == COLI_BF16) return rc_of(launch_select_t<__nv_bfloat16, false>(P, stream));
-  return rc_of(launch_select_t<__half, false>(P, stream));
+  if (a->type == COLI_F32) return rc_of(launch_select<float, false>(P, stream));
+  if (a->type == COLI_BF16) return rc_of(launch_select<__nv_bfloat16, false>(P, stream));
+  return rc_of(launch_select<__half, false>(P, stream));
 }
