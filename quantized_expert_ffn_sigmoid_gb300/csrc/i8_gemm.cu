@@ -16,7 +16,8 @@
 // Activations are the N side, widened once a call in the workspace (i8_widen,
 // which also gathers the rows of y and finds the runs' length) and fetched by TMA.
 //
-// One persistent CTA an SM, 20 warps meeting at mbarriers, every wait bounded:
+// One persistent CTA an SM, 20 warps meeting at mbarriers, every wait bounded
+// (after 0.3 s at a barrier it ends, and with it the other waits of both CTAs of a pair):
 //   warp 0       TMA of weight codes, slots of 128 rows x 128 codes;
 //   warps 1, 3   TMA of activations, slots of up to NT rows x SUB codes;
 //   warp 2       MMA issuer, blocks of 256 codes;
@@ -160,9 +161,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // An arrival at the barrier of the pair's first CTA that stands where `bar` does
-// in this one.  What it announces is in tensor memory, or in shared memory by
-// asynchronous copies: no ordinary store has to be seen by the other CTA, and a
-// release to the whole cluster took 2000 cycles.
+// in this one.  It announces this CTA's stores to tensor memory, which the tcgen05
+// fences before it and behind the other CTA's wait order, and shared memory filled by
+// asynchronous copies, whose completion has been seen here before; both are read by
+// the pair's instructions alone.  No ordinary store has to be seen by the other CTA, so
+// the arrival names no scope: for the copies that rests on their completion, where the
+// memory model would ask for a release to the cluster and a wait that acquires from
+// it; the release took 2000 cycles a block.
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
@@ -327,9 +332,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       }
       // every copy issued has landed before the CTA can exit (after an abort a
       // phase may lack the other warps' arrivals: the wait is bounded)
-      for (uint32_t k = gs > (uint32_t)NW ? gs - NW : 0; k < gs; ++k)
-        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full_w[k % NW], (k / NW) & 1u); ++i) {
-        }
+      uint32_t tries = SPIN_LIMIT;
+      for (uint32_t k = gs > (uint32_t)NW ? gs - NW : 0; k < gs; ++k) drain_wait(&full_w[k % NW], (k / NW) & 1u, tries);
     } else if ((warp == 1 || warp == 3) && lane == 0) {
       // ------------------------------------------------ TMA of activations
       // Each warp takes half of a slot, every other 64 codes (one thread issues
@@ -360,27 +364,26 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       }
       // (the last copies are of the last blocks whose operands were asked for)
       const uint32_t blocks = (gs + SUBS - 1) / SUBS;
-      for (uint32_t k = blocks > (uint32_t)NF ? blocks - NF : 0; k < blocks; ++k)
-        for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(&full[k % NF], (k / NF) & 1u); ++i) {
-        }
+      uint32_t tries = SPIN_LIMIT;
+      for (uint32_t k = blocks > (uint32_t)NF ? blocks - NF : 0; k < blocks; ++k) drain_wait(&full[k % NF], (k / NF) & 1u, tries);
     } else if (warp == 2 && PAIR && rank == 1) {
       // ------------------- second CTA: tells the first that a block is there
+      // (after an abort the lanes go on to the end: they meet here, and may learn of
+      // it at different blocks)
       uint32_t gs = 0;
-      bool go = true;
-      for (int item = first; item < items && go; item += step)
+      for (int item = first; item < items; item += step)
         for (int j = 0; j < nblk; ++j, ++gs) {
-          if (!gwait(&full[gs % NF], (gs / NF) & 1u, status, s_abort)) { go = false; break; }
+          const bool there = gwait(&full[gs % NF], (gs / NF) & 1u, status, s_abort);
           tmem_fence_after();
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_first(&full2[gs % NF]);
+          if (lane == 0 && there) arrive_first(&full2[gs % NF]);
         }
       // the first CTA's last arrivals here
-      if (go) {
+      if (!*s_abort) {
         const uint32_t subs = gs * SUBS;
-        for (uint32_t k = subs > (uint32_t)NB ? subs - NB : 0; k < subs; ++k)
-          for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_test_wait(&done[k % NB], (k / NB) & 1u); ++i) {
-          }
+        uint32_t tries = SPIN_LIMIT;
+        for (uint32_t k = subs > (uint32_t)NB ? subs - NB : 0; k < subs; ++k) drain_wait(&done[k % NB], (k / NB) & 1u, tries);
       }
     } else if (warp == 2) {
       // -------------------------------------------------------- MMA issuer
@@ -456,8 +459,8 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
         else umma_commit(fin);
       }
       __syncwarp();
-      for (uint32_t i = 0; i < SPIN_LIMIT && !mbar_try_wait(fin, 0u); ++i) {
-      }
+      uint32_t tries = SPIN_LIMIT;
+      drain_wait(fin, 0u, tries);
     }
   } else if (warp < 12) {
     setmaxnreg_dec<IG_RCONV>();
@@ -601,6 +604,9 @@ __global__ void __launch_bounds__(IG_THREADS, 1) i8_gemm(const __grid_constant__
       else store(static_cast<__half*>(A.y));
     }
   }
+  // A wait that has run out ends the other CTA's waits too (a warp gets here soon
+  // after: waits fail at once then, and the results are flagged invalid)
+  if (PAIR && lane == 0 && *s_abort) abort_other(s_abort);
   tmem_fence_before();
   __syncthreads();
   if (PAIR) cluster_sync();  // (neither CTA ends while the other may arrive at its barriers)

@@ -133,7 +133,9 @@ __device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t leader) {
 // (the abort flag), so that a broken pipeline drains.  Without a suspend-time
 // hint, with which a thread wakes late, and not polling, which takes issue
 // slots from the epilogue: one position took 45.3 us against 47.2 with the
-// scale writers and the MMA warp polling.
+// scale writers and the MMA warp polling.  On a barrier at which nothing arrives it
+// ends after 0.31 s (a look at the clock beside the tries cost the MX4 products of
+// 256 groups a tenth of their time).
 __device__ __forceinline__ bool gwait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
   for (uint32_t i = 0; i < SPIN_LIMIT; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -142,6 +144,22 @@ __device__ __forceinline__ bool gwait(uint64_t* bar, uint32_t parity, uint32_t* 
   *abort = 1;
   atomicOr(status, COLI_STATUS_TIMEOUT);
   return false;
+}
+// The same for what must have landed before a CTA ends, after an abort too, without
+// status or flag; `tries` are those left for all such waits of a thread.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint32_t& tries) {
+  for (; tries > 0 && !mbar_try_wait(bar, parity); --tries) {
+  }
+}
+// Sets the abort flag of the other CTA of a pair (a cluster of two), which must not have ended.
+__device__ __forceinline__ void abort_other(volatile int* abort) {
+  asm volatile(
+      "{\n\t.reg .b32 r, a;\n\t"
+      "mov.u32 r, %%cluster_ctarank;\n\t"
+      "xor.b32 r, r, 1;\n\t"
+      "mapa.shared::cluster.u32 a, %0, r;\n\t"
+      "st.relaxed.cluster.shared::cluster.u32 [a], %1;\n\t}"
+      ::"r"(smem_u32(const_cast<int*>(abort))), "r"(1) : "memory");
 }
 
 // kind::f16, fp16 x fp16 -> fp32, both K-major, M = 128
