@@ -140,9 +140,10 @@ __global__ void __launch_bounds__(IS_T, 2) i8_stream(const I8Params A) {
     for (int p = 0; p < A.P; ++p) {
       const int g = s_group[p] - 1;  // -1: before the first group, G: behind the last
       s_group[p] = g;
-      const int row = g < 0 || g >= A.G ? 0 : A.rows ? __ldcg(A.rows + p) : p;
+      const bool live = g >= 0 && g < A.G;
+      const int row = !live ? -1 : A.rows ? __ldcg(A.rows + p) : p;
       s_row[p] = row < 0 || row >= A.X ? -1 : row;
-      if (s_row[p] < 0 && blockIdx.x == 0) atomicOr(reinterpret_cast<uint32_t*>(A.ws), COLI_STATUS_BADIDX);
+      if (live && s_row[p] < 0 && blockIdx.x == 0) atomicOr(reinterpret_cast<uint32_t*>(A.ws), COLI_STATUS_BADIDX);
       if (g != last) s_seg[n++] = p;
       last = g;
     }
@@ -209,7 +210,7 @@ extern "C" int coli_i8_product(const coli_i8_product_args* a, cudaStream_t strea
   if (!a->offsets && a->G != 1) return COLI_EINVAL;
   if (!a->rows && a->P > a->x_rows) return COLI_EINVAL;
   if (a->P == 0) return COLI_OK;
-  if (!a->x_codes || !a->x_scales || !a->w_codes || !a->w_scales || !a->y || !a->ws) return COLI_EINVAL;
+  if ((a->x_rows > 0 && (!a->x_codes || !a->x_scales)) || !a->w_codes || !a->w_scales || !a->y || !a->ws) return COLI_EINVAL;
   const void* ptrs[] = {a->x_codes, a->x_scales, a->rows, a->w_codes, a->w_scales, a->offsets, a->y, a->ws};
   for (const void* p : ptrs)
     if (!aligned16(p)) return COLI_EALIGN;
