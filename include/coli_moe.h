@@ -468,7 +468,8 @@ int coli_moe_block_norm(const coli_moe_norm_args* args, int32_t T, int32_t H, cu
  * weight 0 in the slots that are left.  Weights whose sum is 0 stay 0.  Any other
  * non-finite logit or bias, and any non-finite logit of a hidden state, gives a
  * position ids -1 and weights 0 and sets COLI_STATUS_NONFINITE.  Limits: n_experts <= 1024, a multiple of n_groups <=
- * 32, top_k <= 32 and <= the experts of topk_group groups.  T == 0 is a no-op. */
+ * 32, top_k <= 32 and <= the experts of topk_group groups; with router_w at most 4194240 positions.  T == 0 is a
+ * no-op. */
 #define COLI_SCORE_SIGMOID 0
 #define COLI_SCORE_SOFTMAX 1
 #define COLI_GROUP_TOP2    0

@@ -418,6 +418,8 @@ cudaError_t launch_select(const SelectParams& P, cudaStream_t st) {
 int rc_of(cudaError_t e) { return e == cudaSuccess ? COLI_OK : COLI_ECUDA; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+constexpr int SELECT_MAX_T = 65535 * 64;  // positions of a product: the grid's second dimension is tiles of 64
+
 size_t partial_bytes(int T, int H, int E) {
   const size_t splits = T <= ROUTE_GEMV_MAX_T ? (size_t)GEMV_SPLITS : (size_t)route_ksplits(T, H, E);
   return splits * (size_t)T * (size_t)E * 4;
@@ -429,7 +431,7 @@ size_t partial_bytes(int T, int H, int E) {
 using namespace colimoe;
 
 extern "C" size_t coli_moe_select_workspace_size(int32_t max_T, int32_t hidden, int32_t n_experts) {
-  if (max_T < 0 || hidden < 1 || hidden % 16 || n_experts < 1 || n_experts > MAX_E) return 0;
+  if (max_T < 0 || max_T > SELECT_MAX_T || hidden < 1 || hidden % 16 || n_experts < 1 || n_experts > MAX_E) return 0;
   // (fewer positions can take more splits, and then more room in all)
   const size_t few = partial_bytes(max_T < ROUTE_GEMV_MAX_T ? max_T : ROUTE_GEMV_MAX_T, hidden, n_experts);
   size_t most = few;
@@ -459,6 +461,7 @@ extern "C" int coli_moe_select(const coli_moe_select_args* a, int32_t T, cudaStr
   const bool product = a->router_w != nullptr;
   if (product ? a->type != COLI_F32 || a->hidden < 1 || a->hidden % 16 || a->ldx != a->hidden : !float_type(a->type) || a->ldx < a->n_experts)
     return COLI_EINVAL;
+  if (product && T > SELECT_MAX_T) return COLI_EUNSUPPORTED;
   if (T == 0) return COLI_OK;
   if (!a->x || !a->topk_idx || !a->topk_w || (product && !a->ws)) return COLI_EINVAL;
   const void* ptrs[] = {a->x, a->router_w, a->bias, a->topk_idx, a->topk_w, a->ws};
