@@ -31,19 +31,22 @@ def matrices(experts, scales, inter: int, hidden: int):
 
 
 class Layer:
-    """One layer for up to ``positions`` positions per step; all buffers are allocated here, once.
+    """One layer for ``positions`` positions per step; all buffers are allocated here, once.
 
     experts [E, 3 inter hidden] int8 and expert_scales [E, 2 inter + hidden] float32 (with ``ep_size`` > 1 those of
     shard ``ep_rank``: experts e = ep_rank mod ep_size), router_w [experts of all shards, hidden] float32.  The
     selection's arguments are those of coli_moe_select.  A shard's y is its part of the sum over the shards; the
-    shared experts belong to shard 0.  ``dtype`` is the type of y and of the values between the products."""
+    shared experts (records of ``shared_inter``, or ``inter``) belong to shard 0.  ``dtype`` is the type of y and of
+    the values between the products."""
 
     def __init__(self, experts, expert_scales, router_w, inter: int, positions: int, dtype, top_k: int, bias=None, shared=None, shared_scales=None,
-                 score=cm.SCORE_SOFTMAX, n_groups=1, topk_group=1, group_score=cm.GROUP_TOP2, renorm=True, scaling=1.0, ep_rank=0, ep_size=0):
+                 score=cm.SCORE_SOFTMAX, n_groups=1, topk_group=1, group_score=cm.GROUP_TOP2, renorm=True, scaling=1.0, ep_rank=0, ep_size=0,
+                 shared_inter=None):
         import torch
         dev, (E, H), T, k = router_w.device, router_w.shape, positions, top_k
-        if inter % 16 or H % 16:
-            raise ValueError("hidden and inter must be multiples of 16: rows of codes begin on 16-byte boundaries")
+        si = inter if shared_inter is None else shared_inter
+        if inter % 16 or si % 16 or H % 16:
+            raise ValueError("hidden, inter and shared_inter must be multiples of 16: rows of codes begin on 16-byte boundaries")
         if T < 1:
             raise ValueError("at least one position")
         local = E if ep_size <= 1 else (E - ep_rank + ep_size - 1) // ep_size
@@ -66,15 +69,15 @@ class Layer:
         self.y = new(T, H, of=dtype)
         self.ws_select = cm.new_select_workspace(T, H, E, dev)
         self.ws_group = cm.new_group_workspace(T, k, E, dev)
-        self.ws = cm.new_i8_product_workspace(most, max(H, inter), dev)
+        self.ws = cm.new_i8_product_workspace(most, max(H, inter, si if ns else 0), dev)
         self.shared = None
         if ns:
-            self.shared = matrices(shared[:ns], shared_scales, inter, H)
+            self.shared = matrices(shared[:ns], shared_scales, si, H)
             position = torch.arange(T, dtype=torch.int32, device=dev)
             self.s_rows, self.s_offsets = position.repeat(ns), torch.arange(ns + 1, dtype=torch.int32, device=dev) * T
             self.s_slots = (position[:, None] + torch.arange(ns, dtype=torch.int32, device=dev) * T).contiguous()
             self.s_w = torch.ones(T, ns, device=dev)
-            self.s_gu, self.s_hq, self.s_hs, self.s_o = (new(ns * T, 2 * inter, of=dtype), new(ns * T, inter, of=torch.int8), new(ns * T),
+            self.s_gu, self.s_hq, self.s_hs, self.s_o = (new(ns * T, 2 * si, of=dtype), new(ns * T, si, of=torch.int8), new(ns * T),
                                                         new(ns * T, H, of=dtype))
 
     def step(self):
