@@ -18,7 +18,10 @@ namespace colimoe {
 namespace {
 
 constexpr int IS_WARPS = 8, IS_T = 32 * IS_WARPS;
-constexpr int IS_KC = 6144;   // codes of a row held in shared memory at a time
+// Codes of a row held in shared memory at a time: 48 KB for eight rows.  Each further
+// part costs two barriers, half a microsecond (1 row against 4096 x 6144 4.8 us, x 6160
+// 5.3, x 8192 5.8, x 12288 7.0).
+constexpr int IS_KC = 6144;
 
 // 16 codes at p of which n exist (the others 0)
 __device__ __forceinline__ uint4 codes16(const int8_t* p, int n) {

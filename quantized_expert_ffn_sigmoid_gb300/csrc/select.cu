@@ -21,7 +21,7 @@
 // Groups of whole warps take two reductions each; others are scanned by one lane
 // each in shared memory.  All sums are fp32.
 //
-// Bound: instructions (about 920 a position of 256 experts with groups and a bias;
+// Bound: instructions (about 870 a position of 256 experts with groups and a bias;
 // 16384 of them 14.6 us, issue slots 78 % busy, where their 17 MB would take 2.6;
 // groups without a bias 16.9 us, softmax without groups 9.9 us; one position 2.7 us,
 // from its hidden state 8.2).
